@@ -63,7 +63,9 @@ typedef enum {
     TBIK_ERR_TIMEOUT = 6,     /* a device-side bounded wait expired (kernel returned early) */
     TBIK_ERR_TARGET = 7,      /* a logprob target outside [0, V) (its output is NaN) */
     TBIK_ERR_POSITION = 8,    /* a RoPE position outside [0, max_pos) (its outputs are NaN) */
-    TBIK_ERR_UNSUPPORTED = 9  /* not a B200-class device (sm_100) */
+    TBIK_ERR_UNSUPPORTED = 9, /* not a B200-class device (sm_100) */
+    TBIK_ERR_PAGE = 10,       /* cache: a table row, page number, length or reference that cannot be, or no room */
+    TBIK_ERR_VALUE = 11       /* an input that is not finite where a number is needed (cache writes, logits) */
 } tbik_status;
 
 /* ---- mode bits ---------------------------------------------------------- */
@@ -408,6 +410,155 @@ TBIK_API tbik_status tbik_logprob_combine(const float* parts, const int32_t* tar
 TBIK_API tbik_status tbik_logprob_noalloc(const uint16_t* hidden, const uint16_t* W_lm, const int32_t* targets,
                                           float* out, int M, int V, int H, int T, int leaf, unsigned mode,
                                           void* stream);
+
+/* ---- paged 8-bit key/value cache ------------------------------------------ */
+/*
+ * The keys and values of sequences that are being generated, token by token
+ * (the pages behind this library call for bit-equal rollouts; no page gives a
+ * cache, so its layout and arithmetic are stated here).
+ *
+ * A page holds `page` (16, 32, 64 or 128) consecutive positions of one sequence
+ * for kv_heads heads of head_dim (64 or 128) dims, of one layer:
+ *   pages   e4m3 bytes [2][num_pages][kv_heads][page/8][head_dim/16][8][16]
+ *           (0: keys, 1: values; token t, dim d of the page at [t/8][d/16][t%8][d%16])
+ *   scales  fp32 [2][num_pages][kv_heads], powers of two: value = byte * scale
+ * and the bookkeeping, shared by all layers:
+ *   table   int32 [slots][max_pages]: page number of each page of a sequence, -1
+ *           behind its last one; a sequence is a row ("slot") of the table
+ *   lens    int32 [slots]: tokens of each sequence (0: the slot is empty)
+ *   refs    int32 [num_pages]: table entries that name the page (0: free)
+ * Everything is device memory of the caller (tables and arrays start filled
+ * with -1, 0 and 0).  Limits: slots <= 65536, num_pages <= 1048576, max_pages
+ * <= 1048576, sequences per call <= 8192.  `rows` lists the slots of a call's
+ * sequences; NULL means slot b for sequence b.  refs 16-byte aligned.
+ *
+ * The page operations are all or nothing: when an argument cannot be (a slot
+ * out of range or named twice, a length that does not fit max_pages, too few
+ * free pages), they change nothing and record TBIK_ERR_PAGE.  New pages are the
+ * lowest free ones, in the order of the call's sequences.
+ */
+
+/*
+ * Room for n_new[b] (>= 0) more tokens of sequence b: start[b] = its length
+ * before the call (the position of the first new token) and lens grows, or
+ * start[b] = -1 for every b when the call is refused.  Once per step, before
+ * the layers write and read.
+ */
+TBIK_API tbik_status tbik_cache_extend(int32_t* table, int32_t* lens, int32_t* refs, const int32_t* rows,
+                                       const int32_t* n_new, int32_t* start, int batch, int slots, int max_pages,
+                                       int num_pages, int page, void* stream);
+
+/*
+ * children[i] (an empty slot) becomes a copy of parents[i] (which may be named
+ * several times): full pages are shared, a partly filled last page is copied,
+ * with its scales, in all `layers` (pages [layers][2]..., scales [layers][2]...).
+ * A slot cannot be parent and child in one call.  ws: tbik_cache_fork_workspace().
+ */
+TBIK_API size_t tbik_cache_fork_workspace(int count);
+TBIK_API tbik_status tbik_cache_fork(uint8_t* pages, float* scales, int32_t* table, int32_t* lens, int32_t* refs,
+                                     const int32_t* parents, const int32_t* children, int count, int layers,
+                                     int slots, int max_pages, int num_pages, int kv_heads, int head_dim, int page,
+                                     void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * Gives up the pages of each listed sequence and empties its slot; a page is
+ * free when its last reference goes.  A slot named twice is freed once, an
+ * empty one is left as it is.
+ */
+TBIK_API tbik_status tbik_cache_free(int32_t* table, int32_t* lens, int32_t* refs, const int32_t* rows, int batch,
+                                     int slots, int max_pages, int num_pages, int page, void* stream);
+
+/*
+ * Moves live pages to the front of the pool: with n live pages, the k-th live
+ * page at index >= n goes to the k-th free index below n, in all layers; table
+ * and refs follow.  live (int32 [1]) receives n: indices >= n are free.
+ * ws: tbik_cache_compact_workspace().
+ */
+TBIK_API size_t tbik_cache_compact_workspace(int num_pages);
+TBIK_API tbik_status tbik_cache_compact(uint8_t* pages, float* scales, int32_t* table, const int32_t* lens,
+                                        int32_t* refs, int32_t* live, int layers, int slots, int max_pages,
+                                        int num_pages, int kv_heads, int head_dim, int page, void* ws,
+                                        size_t ws_bytes, void* stream);
+
+/*
+ * Page dst[i] = page src[i] in all layers, data and scales, without bookkeeping.
+ * The dst pages must be distinct and none of them a src (else nothing is copied
+ * and TBIK_ERR_PAGE is recorded).  ws: tbik_cache_fork_workspace(count).
+ */
+TBIK_API tbik_status tbik_cache_copy(uint8_t* pages, float* scales, const int32_t* src, const int32_t* dst, int count,
+                                     int layers, int num_pages, int kv_heads, int head_dim, int page, void* ws,
+                                     size_t ws_bytes, void* stream);
+
+/*
+ * Writes new tokens of one layer.  k, v bf16 [tokens][kv_heads][head_dim]; the
+ * tokens of sequence b are cu[b] .. cu[b+1]-1 (cu int32 [batch+1], ascending;
+ * NULL: token b is sequence b's only one) at positions start[b], start[b]+1, ...
+ * (start[b] < 0: nothing is written for b).  The value stored for x is
+ *   cut(round4(x) * 2^-E) * 2^E:  round4 to 4 significant bits (nearest even),
+ *   cut = truncation to e4m3's grid (spacing 2^-9 below 2^-6);  2^E the page's
+ *   scale: the smallest with max |round4| <= 448 * 2^E over the tokens the page
+ *   holds so far, E >= -100.
+ * When a token raises E, the page's older bytes are cut again under the larger
+ * scale.  A page's contents therefore depend on its tokens only, not on how
+ * they were split into calls.  Bytes of positions that no token has reached
+ * stay as they are.  Infinities are stored as +-448 * 2^E and NaN as 0, neither
+ * counts for E, and TBIK_ERR_VALUE is recorded.  A page that is not in the
+ * pool, that another sequence shares (refs != 1) or whose slot the call names
+ * twice is not written, and TBIK_ERR_PAGE is recorded.
+ */
+TBIK_API tbik_status tbik_cache_append(const uint16_t* k, const uint16_t* v, uint8_t* pages, float* scales,
+                                       const int32_t* table, const int32_t* refs, const int32_t* start,
+                                       const int32_t* cu, const int32_t* rows, int tokens, int batch, int slots,
+                                       int max_pages, int num_pages, int kv_heads, int head_dim, int page,
+                                       void* stream);
+
+/*
+ * Attention over the cache of one layer, with the key reduction in tree order
+ * (TBIK summary page, 技术框架): query t of sequence b (packed token cu[b] + t)
+ * sits at position i = start[b] + t and sees the keys at positions 0..i, which
+ * must have been written.  q, out bf16 [tokens][heads][head_dim]; heads is a
+ * multiple of kv_heads, at most 64 times it, and consecutive heads share a kv
+ * head.  Leaves of 128 positions, each a (max, sum, weighted sum) summary,
+ * combined by TREE over the ceil((i+1)/128) leaves like in tbik_attention_tc.
+ * A row's bits depend on its query and on the cache's contents at positions
+ * 0..i, not on the batch, the other queries, page numbers or the device's load.
+ * Checked against the binary64 definition by tolerance.
+ *   max_q     no sequence has more than max_q new tokens
+ *   max_keys  no query sees more than max_keys keys (start[b] + n_b <= max_keys)
+ * Rows of sequences with start[b] < 0, beyond max_q or max_keys, or with a page
+ * number outside the pool are NaN, the latter three with TBIK_ERR_PAGE.  Tokens
+ * outside every sequence's range are left as they are.  out may alias q.
+ * ws: tbik_cache_attention_workspace() bytes, not shared by concurrent calls.
+ */
+TBIK_API size_t tbik_cache_attention_workspace(int tokens, int batch, int max_q, int max_keys, int heads, int kv_heads,
+                                               int head_dim, int page);
+TBIK_API tbik_status tbik_cache_attention(const uint16_t* q, const uint8_t* pages, const float* scales,
+                                          const int32_t* table, const int32_t* start, const int32_t* cu,
+                                          const int32_t* rows, uint16_t* out, int tokens, int batch, int slots,
+                                          int max_pages, int num_pages, int heads, int kv_heads, int head_dim,
+                                          int page, int max_q, int max_keys, void* ws, size_t ws_bytes, void* stream);
+
+/* ---- sampling ------------------------------------------------------------- */
+/*
+ * out[i] = a token of row i of logits [batch][vocab] (fp32, or bf16 with
+ * bf16 != 0), chosen by the given number u[i] in [0, 1):
+ *   w_v = exp((z_v - max z) / temperature[i]), in units of 2^-32;
+ *   top_k[i] > 0 keeps the top_k[i] largest logits (of equal ones the lower
+ *   indices); then top_p[i] < 1 the shortest prefix of the rest, by descending
+ *   logit and ascending index, whose mass reaches top_p[i] of the rest's mass;
+ *   then min_p[i] the tokens with w_v >= min_p[i];
+ *   out[i] = the first index at which the running sum of the kept weights, by
+ *   index, exceeds u[i] times their total.
+ * The most likely token always stays; temperature[i] <= 0 takes it (the lowest
+ * index of the largest logit).  NULL for temperature, top_k, top_p or min_p
+ * means 1, off, 1, 0 for every row.  Logits of -inf are never chosen; a row
+ * that has nothing else, or a NaN (TBIK_ERR_VALUE), gives -1.  The weights' sums
+ * are sums of integers, so a row's token depends on that row only.
+ * vocab <= 393216.  logits 16-byte aligned.
+ */
+TBIK_API tbik_status tbik_sample(const void* logits, const float* u, const float* temperature, const int32_t* top_k,
+                                 const float* top_p, const float* min_p, int32_t* out, int batch, int vocab, int bf16,
+                                 void* stream);
 
 /* ---- errors -------------------------------------------------------------- */
 

@@ -14,11 +14,15 @@ from ._binding import (  # noqa: F401
     TBIK_ERR_TIMEOUT, TBIK_ERR_UNSUPPORTED, TBIK_ERR_WORKSPACE, TBIK_OK, VOCAB_LEAF, TbikError, debug_set,
     attention, attention_tc_workspace, declared_functions, embedding, gemm, gemm_workspace, get_error, load_library, logprob, logprob_workspace,
     rmsnorm_residual, rope_swiglu, rope_table, status_string, transpose, tree_combine, logprob_partial,
-    logprob_combine, vocab_shard,
+    logprob_combine, vocab_shard, TBIK_ERR_PAGE, TBIK_ERR_VALUE, cache_append, cache_attention,
+    cache_attention_workspace, cache_compact, cache_copy, cache_extend, cache_fork, cache_free, cache_pages, cache_table,
+    sample,
 )
 
 __all__ = [
     "gemm", "gemm_workspace", "rmsnorm_residual", "rope_table", "rope_swiglu", "logprob", "logprob_workspace",
     "attention", "attention_tc_workspace", "embedding", "transpose", "get_error", "debug_set", "load_library", "declared_functions", "TbikError",
     "tree_combine", "logprob_partial", "logprob_combine", "vocab_shard",
+    "cache_pages", "cache_table", "cache_extend", "cache_append", "cache_attention", "cache_attention_workspace",
+    "cache_fork", "cache_free", "cache_compact", "cache_copy", "sample",
 ]

@@ -27,6 +27,8 @@ TBIK_ERR_TIMEOUT = 6
 TBIK_ERR_TARGET = 7
 TBIK_ERR_POSITION = 8
 TBIK_ERR_UNSUPPORTED = 9
+TBIK_ERR_PAGE = 10
+TBIK_ERR_VALUE = 11
 
 EXACT = 0x1
 TC = 0x2
@@ -92,6 +94,17 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
             "tbik_logprob_partial_workspace": (sz, [i32, i32, i32, i32, i32, u32]),
             "tbik_logprob_partial": (i32, [vp, vp, vp, vp, i32, i32, i32, i32, i32, i32, u32, vp, sz, vp]),
             "tbik_logprob_combine": (i32, [vp, vp, vp, i32, i32, i32, vp]),
+            "tbik_cache_extend": (i32, [vp] * 6 + [i32] * 5 + [vp]),
+            "tbik_cache_fork_workspace": (sz, [i32]),
+            "tbik_cache_fork": (i32, [vp] * 7 + [i32] * 8 + [vp, sz, vp]),
+            "tbik_cache_free": (i32, [vp] * 4 + [i32] * 5 + [vp]),
+            "tbik_cache_compact_workspace": (sz, [i32]),
+            "tbik_cache_compact": (i32, [vp] * 6 + [i32] * 7 + [vp, sz, vp]),
+            "tbik_cache_copy": (i32, [vp] * 4 + [i32] * 6 + [vp, sz, vp]),
+            "tbik_cache_append": (i32, [vp] * 9 + [i32] * 8 + [vp]),
+            "tbik_cache_attention_workspace": (sz, [i32] * 8),
+            "tbik_cache_attention": (i32, [vp] * 8 + [i32] * 11 + [vp, sz, vp]),
+            "tbik_sample": (i32, [vp] * 7 + [i32] * 3 + [vp]),
             "tbik_get_error": (i32, [vp]),
             "tbik_debug_set": (i32, [u32, ull]),
         }
@@ -487,6 +500,285 @@ def logprob_combine(parts, targets, V: int, *, out=None, stream=None):
     _need_out(out, torch.float32, (M,))
     _check(lib.tbik_logprob_combine(_ptr(parts), _ptr(targets), _ptr(out), M, V, T, _stream_handle(stream)),
            "tbik_logprob_combine")
+    return out
+
+
+# ------------------------------------------------ paged 8-bit key/value cache
+
+def cache_pages(num_pages: int, kv_heads: int, head_dim: int, page: int, layers: int = 1, device="cuda"):
+    """An empty pool (tbik.h, paged 8-bit key/value cache): (pages e4m3 [layers, 2, num_pages, kv_heads, page/8,
+    head_dim/16, 8, 16], scales fp32 [layers, 2, num_pages, kv_heads], refs int32 [num_pages])."""
+    torch = _torch()
+    if page not in (16, 32, 64, 128) or head_dim not in (64, 128):
+        raise ValueError("page must be 16, 32, 64 or 128 and head_dim 64 or 128")
+    pages = torch.zeros((layers, 2, num_pages, kv_heads, page // 8, head_dim // 16, 8, 16), dtype=torch.uint8,
+                        device=device).view(torch.float8_e4m3fn)
+    scales = torch.ones((layers, 2, num_pages, kv_heads), dtype=torch.float32, device=device)
+    return pages, scales, torch.zeros(num_pages, dtype=torch.int32, device=device)
+
+
+def cache_table(slots: int, max_pages: int, device="cuda"):
+    """Empty slots: (table int32 [slots, max_pages] of -1, lens int32 [slots] of 0)."""
+    torch = _torch()
+    return (torch.full((slots, max_pages), -1, dtype=torch.int32, device=device),
+            torch.zeros(slots, dtype=torch.int32, device=device))
+
+
+def _on_device(first, others, stream, fn, args, what):
+    """Calls the library on `first`'s device and stream (its current one by default), whatever the current device
+    is; every tensor of the call has to be there."""
+    torch = _torch()
+    index = first.device.index
+    for t in others:
+        if t is not None and t.device.index != index:
+            raise ValueError("all tensors must be on one device")
+    if stream is None:
+        stream = torch.cuda.current_stream(index)
+    handle = stream.cuda_stream
+    if index == torch.cuda.current_device():
+        status = fn(*args, handle)
+    else:
+        with torch.cuda.device(index):
+            status = fn(*args, handle)
+    if status != TBIK_OK:
+        raise TbikError(status, what)
+
+
+def _need_i32(t, name, n=None):
+    torch = _torch()
+    if t is None:
+        return None
+    _need(t, torch.int32, name)
+    if n is not None and t.numel() != n:
+        raise ValueError(f"{name} must hold {n} values, got {t.numel()}")
+    return t.data_ptr()
+
+
+def _pool(pages, scales, layered):
+    """(layers, num_pages, kv_heads, page, head_dim) of a pool; one layer's has no leading dimension."""
+    torch = _torch()
+    _need(pages, torch.float8_e4m3fn, "pages")
+    _need(scales, torch.float32, "scales")
+    s = tuple(pages.shape)
+    if not layered:
+        s = (1,) + s
+    if len(s) != 8 or s[1] != 2 or s[6] != 8 or s[7] != 16:
+        raise ValueError("pages must be [%s2, num_pages, kv_heads, page/8, head_dim/16, 8, 16]" % ("layers, " if layered else ""))
+    if tuple(scales.shape) != tuple(pages.shape[: len(pages.shape) - 4]):
+        raise ValueError("scales must be [%s2, num_pages, kv_heads]" % ("layers, " if layered else ""))
+    return s[0], s[2], s[3], s[4] * 8, s[5] * 16
+
+
+def _meta(table, lens, refs):
+    """(slots, max_pages, num_pages) of the bookkeeping."""
+    torch = _torch()
+    _need(table, torch.int32, "table")
+    _need(lens, torch.int32, "lens")
+    _need(refs, torch.int32, "refs")
+    if table.dim() != 2:
+        raise ValueError("table must be [slots, max_pages]")
+    if lens.numel() != table.shape[0]:
+        raise ValueError("lens must hold one length per slot")
+    return table.shape[0], table.shape[1], refs.numel()
+
+
+def cache_extend(table, lens, refs, n_new, *, page: int, rows=None, start=None, stream=None):
+    """Room for n_new[b] more tokens of each sequence (slots `rows`, default 0, 1, ...): returns start int32 [batch],
+    the position of each sequence's first new token, or -1 for all when the call is refused (tbik_cache_extend)."""
+    torch = _torch()
+    lib = load_library()
+    slots, max_pages, num_pages = _meta(table, lens, refs)
+    _need(n_new, torch.int32, "n_new")
+    batch = n_new.numel()
+    rp = _need_i32(rows, "rows", batch)
+    if start is None:
+        start = torch.empty(batch, dtype=torch.int32, device=table.device)
+    _need_out(start, torch.int32, (batch,), "start")
+    _on_device(table, (lens, refs, n_new, rows, start), stream, lib.tbik_cache_extend,
+               (table.data_ptr(), lens.data_ptr(), refs.data_ptr(), rp, n_new.data_ptr(), start.data_ptr(), batch,
+                slots, max_pages, num_pages, page), "tbik_cache_extend")
+    return start
+
+
+def _bytes_on(nbytes, device, workspace):
+    """(tensor, pointer, bytes) of the caller's workspace, or of a new one."""
+    torch = _torch()
+    if nbytes == (1 << 64) - 1:
+        raise TbikError(TBIK_ERR_SHAPE, "workspace query")
+    if workspace is None:
+        if nbytes == 0:
+            return None, None, 0
+        workspace = torch.empty(nbytes, dtype=torch.uint8, device=device)
+    return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
+def cache_fork(pages, scales, table, lens, refs, parents, children, *, workspace=None, stream=None):
+    """children[i] (empty slots) become copies of parents[i] (tbik_cache_fork); pages and scales of all layers,
+    [layers, 2, ...]."""
+    torch = _torch()
+    lib = load_library()
+    layers, num_pages, kv_heads, page, head_dim = _pool(pages, scales, True)
+    slots, max_pages, n_refs = _meta(table, lens, refs)
+    if n_refs != num_pages:
+        raise ValueError("refs must hold one count per page")
+    _need(parents, torch.int32, "parents")
+    count = parents.numel()
+    cp = _need_i32(children, "children", count)
+    ws, wsp, wsb = _bytes_on(lib.tbik_cache_fork_workspace(count), pages.device, workspace)
+    _on_device(pages, (scales, table, lens, refs, parents, children, ws), stream, lib.tbik_cache_fork,
+               (pages.data_ptr(), scales.data_ptr(), table.data_ptr(), lens.data_ptr(), refs.data_ptr(),
+                parents.data_ptr(), cp, count, layers, slots, max_pages, num_pages, kv_heads, head_dim, page, wsp, wsb),
+               "tbik_cache_fork")
+
+
+def cache_free(table, lens, refs, rows, *, page: int, stream=None):
+    """Gives up the pages of the sequences in slots `rows` (tbik_cache_free)."""
+    torch = _torch()
+    lib = load_library()
+    slots, max_pages, num_pages = _meta(table, lens, refs)
+    _need(rows, torch.int32, "rows")
+    _on_device(table, (lens, refs, rows), stream, lib.tbik_cache_free,
+               (table.data_ptr(), lens.data_ptr(), refs.data_ptr(), rows.data_ptr(), rows.numel(), slots, max_pages,
+                num_pages, page), "tbik_cache_free")
+
+
+def cache_compact(pages, scales, table, lens, refs, *, live=None, workspace=None, stream=None):
+    """Live pages to the front of the pool (tbik_cache_compact); returns their number as int32 [1]."""
+    torch = _torch()
+    lib = load_library()
+    layers, num_pages, kv_heads, page, head_dim = _pool(pages, scales, True)
+    slots, max_pages, n_refs = _meta(table, lens, refs)
+    if n_refs != num_pages:
+        raise ValueError("refs must hold one count per page")
+    if live is None:
+        live = torch.empty(1, dtype=torch.int32, device=pages.device)
+    _need_out(live, torch.int32, (1,), "live")
+    ws, wsp, wsb = _bytes_on(lib.tbik_cache_compact_workspace(num_pages), pages.device, workspace)
+    _on_device(pages, (scales, table, lens, refs, live, ws), stream, lib.tbik_cache_compact,
+               (pages.data_ptr(), scales.data_ptr(), table.data_ptr(), lens.data_ptr(), refs.data_ptr(),
+                live.data_ptr(), layers, slots, max_pages, num_pages, kv_heads, head_dim, page, wsp, wsb),
+               "tbik_cache_compact")
+    return live
+
+
+def cache_copy(pages, scales, src, dst, *, workspace=None, stream=None):
+    """Page dst[i] = page src[i] in all layers (tbik_cache_copy); no bookkeeping."""
+    torch = _torch()
+    lib = load_library()
+    layers, num_pages, kv_heads, page, head_dim = _pool(pages, scales, True)
+    _need(src, torch.int32, "src")
+    count = src.numel()
+    dp = _need_i32(dst, "dst", count)
+    ws, wsp, wsb = _bytes_on(lib.tbik_cache_fork_workspace(count), pages.device, workspace)
+    _on_device(pages, (scales, src, dst, ws), stream, lib.tbik_cache_copy,
+               (pages.data_ptr(), scales.data_ptr(), src.data_ptr(), dp, count, layers, num_pages, kv_heads, head_dim,
+                page, wsp, wsb), "tbik_cache_copy")
+
+
+def _packed(x, name, table, start, cu, rows):
+    """(tokens, batch, slots, max_pages) of a call on packed tokens."""
+    torch = _torch()
+    if x.dim() != 3:
+        raise ValueError(f"{name} must be [tokens, heads, head_dim]")
+    _need(table, torch.int32, "table")
+    if table.dim() != 2:
+        raise ValueError("table must be [slots, max_pages]")
+    _need(start, torch.int32, "start")
+    batch, tokens = start.numel(), x.shape[0]
+    if cu is None and tokens != batch:
+        raise ValueError("without cu there is one token per sequence")
+    if rows is None and batch > table.shape[0]:
+        raise ValueError("more sequences than slots")
+    return tokens, batch, table.shape[0], table.shape[1]
+
+
+def cache_append(k, v, pages, scales, table, refs, start, *, cu=None, rows=None, stream=None):
+    """Writes new tokens of one layer into its pages [2, num_pages, ...] (tbik_cache_append): k, v bf16 [tokens,
+    kv_heads, head_dim], sequence b's tokens cu[b] .. cu[b+1]-1 (cu None: one token each) at positions start[b], ..."""
+    torch = _torch()
+    lib = load_library()
+    _need(k, torch.bfloat16, "k")
+    _need(v, torch.bfloat16, "v")
+    _, num_pages, kv_heads, page, head_dim = _pool(pages, scales, False)
+    tokens, batch, slots, max_pages = _packed(k, "k", table, start, cu, rows)
+    if v.shape != k.shape or k.shape[1] != kv_heads or k.shape[2] != head_dim:
+        raise ValueError("k and v must be [tokens, kv_heads, head_dim] of the pool")
+    rfp = _need_i32(refs, "refs", num_pages)
+    cup, rp = _need_i32(cu, "cu", batch + 1), _need_i32(rows, "rows", batch)
+    _on_device(pages, (k, v, scales, table, refs, start, cu, rows), stream, lib.tbik_cache_append,
+               (k.data_ptr(), v.data_ptr(), pages.data_ptr(), scales.data_ptr(), table.data_ptr(), rfp,
+                start.data_ptr(), cup, rp, tokens, batch, slots, max_pages, num_pages, kv_heads, head_dim, page),
+               "tbik_cache_append")
+
+
+def cache_attention_workspace(tokens, batch, max_q, max_keys, heads, kv_heads, head_dim, page) -> int:
+    n = load_library().tbik_cache_attention_workspace(tokens, batch, max_q, max_keys, heads, kv_heads, head_dim, page)
+    if n == (1 << 64) - 1:
+        raise TbikError(TBIK_ERR_SHAPE, "tbik_cache_attention_workspace: unsupported shape")
+    return n
+
+
+def cache_attention(q, pages, scales, table, start, *, cu=None, rows=None, max_q=None, max_keys=None, out=None,
+                    workspace=None, stream=None):
+    """Attention of new queries over one layer's pages [2, num_pages, ...] (tbik_cache_attention): q bf16 [tokens,
+    heads, head_dim], packed like cache_append's tokens, query t of sequence b at position start[b] + t over the keys
+    at positions up to its own.  max_q and max_keys bound the tokens of a sequence in this call and the keys that any
+    query sees (default: all tokens; what a table row can hold); tight bounds keep the workspace and the grid small."""
+    torch = _torch()
+    lib = load_library()
+    _need(q, torch.bfloat16, "q")
+    _, num_pages, kv_heads, page, head_dim = _pool(pages, scales, False)
+    tokens, batch, slots, max_pages = _packed(q, "q", table, start, cu, rows)
+    heads = q.shape[1]
+    if q.shape[2] != head_dim:
+        raise ValueError("q must have the head_dim of the pool")
+    if max_q is None:
+        max_q = 1 if cu is None else max(tokens, 1)
+    if max_keys is None:
+        max_keys = max_pages * page
+    cup, rp = _need_i32(cu, "cu", batch + 1), _need_i32(rows, "rows", batch)
+    if out is None:
+        # tokens outside every sequence are left as they are: zeros in a new tensor
+        out = torch.empty_like(q) if cu is None else torch.zeros_like(q)
+    else:
+        _need_out(out, torch.bfloat16, q.shape)
+    ws, wsp, wsb = _bytes_on(lib.tbik_cache_attention_workspace(tokens, batch, max_q, max_keys, heads, kv_heads,
+                                                                head_dim, page), q.device, workspace)
+    _on_device(pages, (q, scales, table, start, cu, rows, out, ws), stream, lib.tbik_cache_attention,
+               (q.data_ptr(), pages.data_ptr(), scales.data_ptr(), table.data_ptr(), start.data_ptr(), cup, rp,
+                out.data_ptr(), tokens, batch, slots, max_pages, num_pages, heads, kv_heads, head_dim, page, max_q,
+                max_keys, wsp, wsb), "tbik_cache_attention")
+    return out
+
+
+# -------------------------------------------------------------------- sampling
+
+def sample(logits, u, *, temperature=None, top_k=None, top_p=None, min_p=None, out=None, stream=None):
+    """One token per row of logits (fp32 or bf16 [batch, vocab]) from given numbers u (fp32 [batch], in [0, 1)):
+    temperature, top-k, top-p, min-p, then the inverse of the running sum in index order (tbik_sample).  The settings
+    are device tensors of one value per row (fp32; top_k int32), or None."""
+    torch = _torch()
+    lib = load_library()
+    if logits.dtype not in (torch.float32, torch.bfloat16):
+        raise TypeError("logits must be fp32 or bf16")
+    _need(logits, logits.dtype, "logits")
+    if logits.dim() != 2:
+        raise ValueError("logits must be [batch, vocab]")
+    batch, vocab = logits.shape
+    ptrs = []
+    for t, name in ((u, "u"), (temperature, "temperature"), (top_k, "top_k"), (top_p, "top_p"), (min_p, "min_p")):
+        if t is None and name != "u":
+            ptrs.append(None)
+            continue
+        _need(t, torch.int32 if name == "top_k" else torch.float32, name)
+        if t.numel() != batch:
+            raise ValueError(f"{name} must hold one value per row")
+        ptrs.append(t.data_ptr())
+    if out is None:
+        out = torch.empty(batch, dtype=torch.int32, device=logits.device)
+    _need_out(out, torch.int32, (batch,))
+    _on_device(logits, (u, temperature, top_k, top_p, min_p, out), stream, lib.tbik_sample,
+               (logits.data_ptr(), *ptrs, out.data_ptr(), batch, vocab, int(logits.dtype == torch.bfloat16)), "tbik_sample")
     return out
 
 

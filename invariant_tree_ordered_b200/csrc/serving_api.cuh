@@ -1,0 +1,305 @@
+// Host side of the cache, its attention and the sampling: argument checks and launches.  Included at the end of
+// tbik_api.cu, whose helpers and device error word it shares.
+#pragma once
+
+namespace {
+
+struct CacheShape {
+    int slots, max_pages, num_pages, kv_heads, head_dim, page;
+};
+
+tbik_status check_meta(int batch, int slots, int max_pages, int num_pages, int page) {
+    if (batch < 0 || slots <= 0 || max_pages <= 0 || num_pages <= 0) return TBIK_ERR_ARG;
+    if (page != 16 && page != 32 && page != 64 && page != 128) return TBIK_ERR_SHAPE;
+    if (batch > CACHE_MAX_BATCH || slots > CACHE_MAX_SLOTS || num_pages > CACHE_MAX_PAGES || max_pages > CACHE_MAX_PAGES)
+        return TBIK_ERR_SHAPE;
+    return TBIK_OK;
+}
+
+tbik_status check_data(int layers, int num_pages, int kv_heads, int head_dim, int page) {
+    if (layers <= 0 || kv_heads <= 0) return TBIK_ERR_ARG;
+    if (head_dim != 64 && head_dim != 128) return TBIK_ERR_SHAPE;
+    if (kv_heads > 65535 || (long long)kv_heads * page * head_dim > (1 << 30) || layers > (1 << 20)) return TBIK_ERR_SHAPE;
+    return check_meta(0, 1, 1, num_pages, page);
+}
+
+CacheMetaParams meta_params(int32_t* table, const int32_t* lens, int32_t* refs, int slots, int max_pages, int num_pages, int page) {
+    CacheMetaParams m;
+    m.table = table, m.lens = const_cast<int32_t*>(lens), m.refs = refs;
+    m.slots = slots, m.max_pages = max_pages, m.num_pages = num_pages, m.page = page;
+    return m;
+}
+
+CacheMoveParams move_params(uint8_t* pages, float* scales, int layers, int num_pages, int kv_heads, int head_dim, int page, void* ws) {
+    CacheMoveParams p;
+    p.pages = pages, p.scales = scales, p.planes = 2 * layers, p.num_pages = num_pages, p.kv_heads = kv_heads;
+    p.page_bytes = kv_heads * page * head_dim;
+    p.ws = reinterpret_cast<const int*>(ws);
+    return p;
+}
+
+// Shared memory of a plan kernel: prefix sums over the call's sequences and a bit per slot.
+size_t plan_smem(int count, int slots) { return ((size_t)count + 1) * 4 + ((size_t)slots + 31) / 32 * 4; }
+
+// Blocks of a kernel that walks over page data: eight of 256 threads fill an SM.
+int move_grid(const DeviceInfo* info, long long most) {
+    const long long full = (long long)info->sms * 8;
+    return (int)(most < 1 ? 1 : most < full ? most : full);
+}
+
+template <int D>
+void launch_append(const CacheAppendParams& p, cudaStream_t s) {
+    if (!p.cu) {
+        cache_append_kernel<D, 32, 1><<<dim3(p.batch, p.kv_heads, 2), 32, 0, s>>>(p);
+        return;
+    }
+    const dim3 grid(p.tokens / p.page + 2 * p.batch, p.kv_heads, 2);
+    switch (p.page * D / 8 / 128) {
+        case 1: cache_append_kernel<D, 128, 1><<<grid, 128, 0, s>>>(p); break;
+        case 2: cache_append_kernel<D, 128, 2><<<grid, 128, 0, s>>>(p); break;
+        case 4: cache_append_kernel<D, 128, 4><<<grid, 128, 0, s>>>(p); break;
+        case 8: cache_append_kernel<D, 128, 8><<<grid, 128, 0, s>>>(p); break;
+        default: cache_append_kernel<D, 128, 16><<<grid, 128, 0, s>>>(p); break;
+    }
+}
+
+tbik_status check_attention(int tokens, int batch, int max_q, int max_keys, int heads, int kv_heads, int head_dim, int page) {
+    if (tokens < 0 || batch < 0 || max_q <= 0 || max_keys <= 0 || heads <= 0 || kv_heads <= 0) return TBIK_ERR_ARG;
+    if (heads % kv_heads || heads / kv_heads > 64 || kv_heads > 65535) return TBIK_ERR_SHAPE;
+    if (head_dim != 64 && head_dim != 128) return TBIK_ERR_SHAPE;
+    if (batch > CACHE_MAX_BATCH || max_keys > (1 << 26)) return TBIK_ERR_SHAPE;
+    return check_meta(batch, 1, 1, 1, page);
+}
+
+template <typename T>
+tbik_status launch_sample(SampleParams& p, const DeviceInfo* info, int dev, cudaStream_t s) {
+    // Blocks per row: as few as hold the row in 48 KB each, more (up to 8) while the device has room for them and a
+    // block has at least 4096 tokens.
+    int cl = 1;
+    while (cl < SMP_MAX_CLUSTER && ((long long)p.vocab * (int)sizeof(T) > 49152LL * cl ||
+                                    ((long long)p.batch * cl * 2 <= info->sms && p.vocab > 4096 * cl)))
+        cl *= 2;
+    p.seg = ((p.vocab + cl - 1) / cl + 15) / 16 * 16;
+    const size_t smem = (size_t)p.seg * sizeof(T) + 32;
+    static bool ready[kMaxDevices];
+    {
+        std::lock_guard<std::mutex> lk(g_mu);
+        if (!ready[dev]) {
+            if (cudaFuncSetAttribute(sample_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                     SMP_MAX_SEG * (int)sizeof(T) + 32) != cudaSuccess)
+                return TBIK_ERR_CUDA;
+            ready[dev] = true;
+        }
+    }
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(p.batch * cl));
+    cfg.blockDim = dim3(SMP_THREADS);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = (unsigned)cl;
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, sample_kernel<T>, (const SampleParams)p) != cudaSuccess) return TBIK_ERR_CUDA;
+    return launch_status();
+}
+
+}  // namespace
+
+extern "C" {
+
+tbik_status tbik_cache_extend(int32_t* table, int32_t* lens, int32_t* refs, const int32_t* rows, const int32_t* n_new,
+                              int32_t* start, int batch, int slots, int max_pages, int num_pages, int page, void* stream) {
+    int dev;
+    DeviceInfo* info;
+    tbik_status st = device_info(dev, info);
+    if (st != TBIK_OK) return st;
+    if ((st = check_meta(batch, slots, max_pages, num_pages, page)) != TBIK_OK) return st;
+    if (!rows && batch > slots) return TBIK_ERR_SHAPE;
+    if (batch == 0) return TBIK_OK;
+    if (!table || !lens || !refs || !n_new || !start) return TBIK_ERR_ARG;
+    if (!aligned16(refs)) return TBIK_ERR_ALIGN;
+    cache_extend_kernel<<<1, CACHE_PLAN_THREADS, plan_smem(batch, slots), reinterpret_cast<cudaStream_t>(stream)>>>(
+        meta_params(table, lens, refs, slots, max_pages, num_pages, page), rows, n_new, start, batch);
+    return launch_status();
+}
+
+size_t tbik_cache_fork_workspace(int count) {
+    return count < 0 || count > CACHE_MAX_BATCH ? (size_t)-1 : ((size_t)count + 1) * 8;
+}
+
+tbik_status tbik_cache_fork(uint8_t* pages, float* scales, int32_t* table, int32_t* lens, int32_t* refs,
+                            const int32_t* parents, const int32_t* children, int count, int layers, int slots,
+                            int max_pages, int num_pages, int kv_heads, int head_dim, int page, void* ws,
+                            size_t ws_bytes, void* stream) {
+    int dev;
+    DeviceInfo* info;
+    tbik_status st = device_info(dev, info);
+    if (st != TBIK_OK) return st;
+    if ((st = check_meta(count, slots, max_pages, num_pages, page)) != TBIK_OK) return st;
+    if ((st = check_data(layers, num_pages, kv_heads, head_dim, page)) != TBIK_OK) return st;
+    if (count == 0) return TBIK_OK;
+    if (!pages || !scales || !table || !lens || !refs || !parents || !children) return TBIK_ERR_ARG;
+    if (!aligned16(pages) || !aligned16(scales) || !aligned16(refs) || (ws && !aligned16(ws))) return TBIK_ERR_ALIGN;
+    if (!ws || ws_bytes < tbik_cache_fork_workspace(count)) return TBIK_ERR_WORKSPACE;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    const CacheMetaParams m = meta_params(table, lens, refs, slots, max_pages, num_pages, page);
+    const CacheMoveParams p = move_params(pages, scales, layers, num_pages, kv_heads, head_dim, page, ws);
+    cache_fork_plan_kernel<<<1, CACHE_PLAN_THREADS, plan_smem(count, slots), s>>>(m, parents, children, count,
+                                                                                   reinterpret_cast<int*>(ws));
+    if ((st = launch_status()) != TBIK_OK) return st;
+    const long long most = (long long)count * p.planes * ((p.page_bytes + CACHE_MOVE_BYTES - 1) / CACHE_MOVE_BYTES);
+    cache_fork_kernel<<<move_grid(info, most), CACHE_MOVE_THREADS, 0, s>>>(p, m, parents, children, count);
+    return launch_status();
+}
+
+tbik_status tbik_cache_free(int32_t* table, int32_t* lens, int32_t* refs, const int32_t* rows, int batch, int slots,
+                            int max_pages, int num_pages, int page, void* stream) {
+    int dev;
+    DeviceInfo* info;
+    tbik_status st = device_info(dev, info);
+    if (st != TBIK_OK) return st;
+    if ((st = check_meta(batch, slots, max_pages, num_pages, page)) != TBIK_OK) return st;
+    if (!rows && batch > slots) return TBIK_ERR_SHAPE;
+    if (batch == 0) return TBIK_OK;
+    if (!table || !lens || !refs) return TBIK_ERR_ARG;
+    cache_free_kernel<<<batch, 128, 0, reinterpret_cast<cudaStream_t>(stream)>>>(
+        meta_params(table, lens, refs, slots, max_pages, num_pages, page), rows);
+    return launch_status();
+}
+
+size_t tbik_cache_compact_workspace(int num_pages) {
+    if (num_pages <= 0 || num_pages > CACHE_MAX_PAGES) return (size_t)-1;
+    return (2 + 2 * (((size_t)num_pages + 1) / 2) + (size_t)num_pages) * 4;
+}
+
+tbik_status tbik_cache_compact(uint8_t* pages, float* scales, int32_t* table, const int32_t* lens, int32_t* refs,
+                               int32_t* live, int layers, int slots, int max_pages, int num_pages, int kv_heads,
+                               int head_dim, int page, void* ws, size_t ws_bytes, void* stream) {
+    int dev;
+    DeviceInfo* info;
+    tbik_status st = device_info(dev, info);
+    if (st != TBIK_OK) return st;
+    if ((st = check_meta(0, slots, max_pages, num_pages, page)) != TBIK_OK) return st;
+    if ((st = check_data(layers, num_pages, kv_heads, head_dim, page)) != TBIK_OK) return st;
+    if (!pages || !scales || !table || !lens || !refs || !live) return TBIK_ERR_ARG;
+    if (!aligned16(pages) || !aligned16(scales) || !aligned16(refs) || (ws && !aligned16(ws))) return TBIK_ERR_ALIGN;
+    if (!ws || ws_bytes < tbik_cache_compact_workspace(num_pages)) return TBIK_ERR_WORKSPACE;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    const CacheMetaParams m = meta_params(table, lens, refs, slots, max_pages, num_pages, page);
+    const CacheMoveParams p = move_params(pages, scales, layers, num_pages, kv_heads, head_dim, page, ws);
+    cache_compact_plan_kernel<<<1, CACHE_PLAN_THREADS, 0, s>>>(m, live, reinterpret_cast<int*>(ws));
+    if ((st = launch_status()) != TBIK_OK) return st;
+    const long long most = (long long)(num_pages / 2 + 1) * p.planes * ((p.page_bytes + CACHE_MOVE_BYTES - 1) / CACHE_MOVE_BYTES);
+    cache_compact_kernel<<<move_grid(info, most), CACHE_MOVE_THREADS, 0, s>>>(p, m);
+    return launch_status();
+}
+
+tbik_status tbik_cache_copy(uint8_t* pages, float* scales, const int32_t* src, const int32_t* dst, int count, int layers,
+                            int num_pages, int kv_heads, int head_dim, int page, void* ws, size_t ws_bytes, void* stream) {
+    int dev;
+    DeviceInfo* info;
+    tbik_status st = device_info(dev, info);
+    if (st != TBIK_OK) return st;
+    if ((st = check_meta(count, 1, 1, num_pages, page)) != TBIK_OK) return st;
+    if ((st = check_data(layers, num_pages, kv_heads, head_dim, page)) != TBIK_OK) return st;
+    if (count == 0) return TBIK_OK;
+    if (!pages || !scales || !src || !dst) return TBIK_ERR_ARG;
+    if (!aligned16(pages) || !aligned16(scales) || (ws && !aligned16(ws))) return TBIK_ERR_ALIGN;
+    if (!ws || ws_bytes < tbik_cache_fork_workspace(count)) return TBIK_ERR_WORKSPACE;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    const size_t smem = ((size_t)num_pages + 31) / 32 * 4;
+    if (smem > 48 * 1024 &&
+        cudaFuncSetAttribute(cache_copy_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, CACHE_MAX_PAGES / 8) != cudaSuccess)
+        return TBIK_ERR_CUDA;
+    const CacheMoveParams p = move_params(pages, scales, layers, num_pages, kv_heads, head_dim, page, ws);
+    cache_copy_plan_kernel<<<1, CACHE_PLAN_THREADS, smem, s>>>(src, dst, count, num_pages, reinterpret_cast<int*>(ws));
+    if ((st = launch_status()) != TBIK_OK) return st;
+    const long long most = (long long)count * p.planes * ((p.page_bytes + CACHE_MOVE_BYTES - 1) / CACHE_MOVE_BYTES);
+    cache_move_kernel<<<move_grid(info, most), CACHE_MOVE_THREADS, 0, s>>>(p);
+    return launch_status();
+}
+
+tbik_status tbik_cache_append(const uint16_t* k, const uint16_t* v, uint8_t* pages, float* scales, const int32_t* table,
+                              const int32_t* refs, const int32_t* start, const int32_t* cu, const int32_t* rows,
+                              int tokens, int batch, int slots, int max_pages, int num_pages, int kv_heads, int head_dim,
+                              int page, void* stream) {
+    int dev;
+    DeviceInfo* info;
+    tbik_status st = device_info(dev, info);
+    if (st != TBIK_OK) return st;
+    if (tokens < 0) return TBIK_ERR_ARG;
+    if ((st = check_meta(batch, slots, max_pages, num_pages, page)) != TBIK_OK) return st;
+    if ((st = check_data(1, num_pages, kv_heads, head_dim, page)) != TBIK_OK) return st;
+    if ((!cu && tokens != batch) || (!rows && batch > slots)) return TBIK_ERR_SHAPE;
+    if (tokens == 0 || batch == 0) return TBIK_OK;
+    if (!k || !v || !pages || !scales || !table || !refs || !start) return TBIK_ERR_ARG;
+    if (!aligned16(k) || !aligned16(v) || !aligned16(pages) || !aligned16(scales)) return TBIK_ERR_ALIGN;
+    CacheAppendParams p;
+    p.k = k, p.v = v, p.pages = pages, p.scales = scales, p.table = table, p.refs = refs, p.start = start;
+    p.cu = cu, p.rows = rows, p.tokens = tokens, p.batch = batch, p.slots = slots, p.max_pages = max_pages;
+    p.num_pages = num_pages, p.kv_heads = kv_heads, p.page = page;
+    if (head_dim == 128)
+        launch_append<128>(p, reinterpret_cast<cudaStream_t>(stream));
+    else
+        launch_append<64>(p, reinterpret_cast<cudaStream_t>(stream));
+    return launch_status();
+}
+
+size_t tbik_cache_attention_workspace(int tokens, int batch, int max_q, int max_keys, int heads, int kv_heads,
+                                      int head_dim, int page) {
+    int dev;
+    DeviceInfo* info;
+    if (device_info(dev, info) != TBIK_OK) return (size_t)-1;
+    if (check_attention(tokens, batch, max_q, max_keys, heads, kv_heads, head_dim, page) != TBIK_OK) return (size_t)-1;
+    return 0;
+}
+
+tbik_status tbik_cache_attention(const uint16_t* q, const uint8_t* pages, const float* scales, const int32_t* table,
+                                 const int32_t* start, const int32_t* cu, const int32_t* rows, uint16_t* out, int tokens,
+                                 int batch, int slots, int max_pages, int num_pages, int heads, int kv_heads, int head_dim,
+                                 int page, int max_q, int max_keys, void* ws, size_t ws_bytes, void* stream) {
+    int dev;
+    DeviceInfo* info;
+    tbik_status st = device_info(dev, info);
+    if (st != TBIK_OK) return st;
+    if ((st = check_attention(tokens, batch, max_q, max_keys, heads, kv_heads, head_dim, page)) != TBIK_OK) return st;
+    if ((st = check_meta(batch, slots, max_pages, num_pages, page)) != TBIK_OK) return st;
+    if ((!cu && tokens != batch) || (!rows && batch > slots)) return TBIK_ERR_SHAPE;
+    if (tokens == 0 || batch == 0) return TBIK_OK;
+    if (!q || !pages || !scales || !table || !start || !out) return TBIK_ERR_ARG;
+    if (!aligned16(q) || !aligned16(pages) || !aligned16(scales) || !aligned16(out)) return TBIK_ERR_ALIGN;
+    CacheAttParams p;
+    p.q = q, p.pages = pages, p.scales = scales, p.table = table, p.start = start, p.cu = cu, p.rows = rows, p.out = out;
+    p.tokens = tokens, p.batch = batch, p.slots = slots, p.max_pages = max_pages, p.num_pages = num_pages;
+    p.heads = heads, p.kv_heads = kv_heads, p.page = page, p.max_q = max_q, p.max_keys = max_keys;
+    p.scale = (float)(1.4426950408889634 / std::sqrt((double)head_dim));
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    if (head_dim == 128)
+        cache_attention_simple_kernel<128><<<dim3(tokens, heads), 128, 0, s>>>(p);
+    else
+        cache_attention_simple_kernel<64><<<dim3(tokens, heads), 128, 0, s>>>(p);
+    return launch_status();
+}
+
+tbik_status tbik_sample(const void* logits, const float* u, const float* temperature, const int32_t* top_k,
+                        const float* top_p, const float* min_p, int32_t* out, int batch, int vocab, int bf16, void* stream) {
+    int dev;
+    DeviceInfo* info;
+    tbik_status st = device_info(dev, info);
+    if (st != TBIK_OK) return st;
+    if (batch < 0 || vocab <= 0) return TBIK_ERR_ARG;
+    if (vocab > SMP_MAX_SEG * SMP_MAX_CLUSTER || batch > (1 << 24)) return TBIK_ERR_SHAPE;
+    if (batch == 0) return TBIK_OK;
+    if (!logits || !u || !out) return TBIK_ERR_ARG;
+    if (!aligned16(logits)) return TBIK_ERR_ALIGN;
+    SampleParams p;
+    p.logits = logits, p.u = u, p.temperature = temperature, p.top_k = top_k, p.top_p = top_p, p.min_p = min_p;
+    p.out = out, p.batch = batch, p.vocab = vocab;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    return bf16 ? launch_sample<uint16_t>(p, info, dev, s) : launch_sample<float>(p, info, dev, s);
+}
+
+}  // extern "C"

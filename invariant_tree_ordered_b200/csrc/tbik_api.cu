@@ -18,6 +18,8 @@
 #include "logprob.cuh"
 #include "attention.cuh"
 #include "reduce.cuh"
+#include "cache_attention.cuh"
+#include "sample.cuh"
 #include "tbik.h"
 
 namespace {
@@ -671,6 +673,8 @@ const char* tbik_status_string(tbik_status s) {
         case TBIK_ERR_TARGET: return "target index out of range";
         case TBIK_ERR_POSITION: return "RoPE position out of range";
         case TBIK_ERR_UNSUPPORTED: return "device is not sm_100";
+        case TBIK_ERR_PAGE: return "cache row, page or length out of range, or no room";
+        case TBIK_ERR_VALUE: return "input is not finite";
     }
     return "unknown status";
 }
@@ -1104,3 +1108,5 @@ tbik_status tbik_debug_set(unsigned flags, unsigned long long wait_limit_ns) {
 }
 
 }  // extern "C"
+
+#include "serving_api.cuh"

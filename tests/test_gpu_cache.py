@@ -1,0 +1,505 @@
+"""The paged 8-bit cache on the device: writes and page operations bit for bit against tests/cache_model.py,
+attention against binary64, its bitwise independence of the batch and the split, and the refusals."""
+import numpy as np
+import pytest
+
+from tests import cache_model as cm
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+
+import invariant_tree_ordered_b200 as tbik  # noqa: E402
+
+DEV = "cuda"
+NAN_BYTE = 0x7F
+
+
+def i32(v):
+    return torch.tensor(list(v), dtype=torch.int32, device=DEV)
+
+
+def cu_of(n):
+    return i32(np.concatenate([[0], np.cumsum(n)]))
+
+
+def raw(pages):
+    return pages.view(torch.uint8)
+
+
+class Cache:
+    """Device state and its numpy model side by side."""
+
+    def __init__(self, slots, max_pages, num_pages, H, D, page, layers=1, fill=NAN_BYTE):
+        self.pages, self.scales, self.refs = tbik.cache_pages(num_pages, H, D, page, layers)
+        raw(self.pages).fill_(fill)  # what no token has reached is garbage
+        self.table, self.lens = tbik.cache_table(slots, max_pages)
+        self.book = cm.Book(slots, max_pages, num_pages, page)
+        self.page, self.H, self.D = page, H, D
+
+    def check(self):
+        for a, b in ((self.table, self.book.table), (self.lens, self.book.lens), (self.refs, self.book.refs)):
+            assert np.array_equal(a.cpu().numpy(), b)
+
+    def extend(self, rows, n):
+        start = tbik.cache_extend(self.table, self.lens, self.refs, i32(n), page=self.page, rows=i32(rows))
+        ref = self.book.extend(rows, n)
+        assert start.tolist() == ref
+        self.check()
+        return start
+
+    def append(self, k, v, start, n, rows, layer=0, packed=True):
+        tbik.cache_append(k, v, self.pages[layer], self.scales[layer], self.table, self.refs, start,
+                          cu=cu_of(n) if packed else None, rows=i32(rows))
+
+    def attend(self, q, start, n, rows, layer=0, packed=True, **kw):
+        return tbik.cache_attention(q, self.pages[layer], self.scales[layer], self.table, start,
+                                    cu=cu_of(n) if packed else None, rows=i32(rows), **kw)
+
+    def stored(self, row, n, layer=0):
+        """float64 [2, H, n, D]: what the device holds of a sequence's first n positions."""
+        ids = self.book.table[row, :self.book.pages_of(n)]
+        v = cm.unpack(raw(self.pages)[layer][:, ids].cpu().numpy())          # [2, pages, H, page, D]
+        v = v * self.scales[layer][:, ids].double().cpu().numpy()[..., None, None]
+        return np.swapaxes(v, 1, 2).reshape(2, self.H, -1, self.D)[:, :, :n]
+
+
+def tokens(seed, n, H, D, spread=True):
+    g = torch.Generator(device=DEV).manual_seed(seed)
+    x = torch.randn(n, H, D, device=DEV, generator=g)
+    if spread:  # magnitudes over many binades, zeros and tiny values among them
+        x = x * torch.exp2(torch.randint(-24, 6, (n, H, 1), device=DEV, generator=g).float())
+        x = x * torch.exp2(torch.randint(-12, 1, (n, H, D), device=DEV, generator=g).float())
+        x = x * (torch.rand(n, H, 1, device=DEV, generator=g) > 0.1)
+    return x.to(torch.bfloat16)
+
+
+def model_pages(x, page):
+    """[(values [tokens, D] in units, E)] per page and head of one sequence's tokens x float64 [n, H, D]."""
+    return [[cm.page_values(x[a:a + page, h]) for h in range(x.shape[1])] for a in range(0, x.shape[0], page)]
+
+
+def check_written(c, row, k, v, layer=0):
+    n = k.shape[0]
+    ids = c.book.table[row, :c.book.pages_of(n)]
+    for kv, x in ((0, k), (1, v)):
+        x = x.double().cpu().numpy()
+        got = cm.unpack(raw(c.pages)[layer][kv, ids].cpu().numpy())
+        byt = raw(c.pages)[layer][kv, ids].cpu().numpy().swapaxes(-3, -2).reshape(len(ids), c.H, c.page, c.D)
+        sc = c.scales[layer][kv, ids].cpu().numpy()
+        for i, per_head in enumerate(model_pages(x, c.page)):
+            for h, (val, E) in enumerate(per_head):
+                assert sc[i, h] == np.float32(2.0 ** E), (i, h)
+                assert np.array_equal(got[i, h, :len(val)], val), (i, h)
+                assert (byt[i, h, len(val):] == NAN_BYTE).all()  # not reached by any token: untouched
+
+
+@pytest.mark.parametrize("page", [16, 32, 64, 128])
+@pytest.mark.parametrize("D,H", [(64, 3), (128, 2)])
+def test_append_matches_the_definition_for_every_split(page, D, H):
+    lens = [1, page - 1, page, page + 1, 3 * page + 5]
+    parts = {r: (tokens(10 * page + r, n, H, D), tokens(10 * page + r + 5, n, H, D)) for r, n in enumerate(lens)}
+    states = []
+    for cuts in ("whole", "single", "odd"):
+        c = Cache(len(lens), 5, 24, H, D, page)
+        at = [0] * len(lens)
+        step = 0
+        while any(a < n for a, n in zip(at, lens)):
+            take = [n - a if cuts == "whole" else min(n - a, 1 if cuts == "single" else 1 + (7 * step + 3 * r) % (page + 9))
+                    for r, (a, n) in enumerate(zip(at, lens))]
+            rows = [r for r in reversed(range(len(lens))) if take[r]]
+            n = [take[r] for r in rows]
+            start = c.extend(rows, n)
+            k = torch.cat([parts[r][0][at[r]:at[r] + take[r]] for r in rows])
+            v = torch.cat([parts[r][1][at[r]:at[r] + take[r]] for r in rows])
+            c.append(k, v, start, n, rows, packed=cuts != "single")
+            at = [a + t for a, t in zip(at, take)]
+            step += 1
+        assert tbik.get_error() == tbik.TBIK_OK
+        for r in range(len(lens)):
+            check_written(c, r, *parts[r])
+        states.append(c)
+
+
+def test_append_takes_values_that_are_not_finite():
+    c = Cache(1, 2, 3, 2, 64, 16)
+    k, v = tokens(1, 3, 2, 64, False), tokens(2, 3, 2, 64, False)
+    k[0, 0, 3], k[1, 1, 5], v[2, 0, 0], v[2, 1, 7] = float("inf"), float("-inf"), float("nan"), float("inf")
+    c.append(k, v, c.extend([0], [3]), [3], [0])
+    assert tbik.get_error() == tbik.TBIK_ERR_VALUE
+    check_written(c, 0, k, v)
+    k2 = torch.full_like(k[:1], float("inf"))  # nothing finite: the smallest scale
+    c2 = Cache(1, 2, 3, 2, 64, 16)
+    c2.append(k2, v[:1], c2.extend([0], [1]), [1], [0])
+    check_written(c2, 0, k2, v[:1])
+    assert tbik.get_error() == tbik.TBIK_ERR_VALUE
+    big = torch.full((1, 2, 64), float(torch.finfo(torch.bfloat16).max), device=DEV).to(torch.bfloat16)
+    c3 = Cache(1, 2, 3, 2, 64, 16)
+    c3.append(big, -big, c3.extend([0], [1]), [1], [0])
+    check_written(c3, 0, big, -big)
+    assert tbik.get_error() == tbik.TBIK_OK
+
+
+@pytest.mark.parametrize("packed", [True, False])
+def test_append_refuses_pages_it_must_not_write(packed):
+    H, D, page = 2, 64, 16
+    c = Cache(4, 2, 8, H, D, page)
+    start = c.extend([0, 1, 2, 3], [1, 1, 1, 1])
+    before, sc = raw(c.pages).clone(), c.scales.clone()
+    k, v = tokens(1, 4, H, D), tokens(2, 4, H, D)
+
+    def attempt(rows, start, code):
+        c.append(k[:len(rows)], v[:len(rows)], start, [1] * len(rows), rows, packed=packed)
+        assert tbik.get_error() == code
+        same = torch.equal(raw(c.pages), before) and torch.equal(c.scales, sc)
+        return same
+
+    assert attempt([0], i32([-1]), tbik.TBIK_OK)                 # not granted: nothing to do
+    assert attempt([4], i32([0]), tbik.TBIK_ERR_PAGE)            # no such slot
+    assert attempt([-1], i32([0]), tbik.TBIK_ERR_PAGE)
+    assert attempt([0], i32([2 * page]), tbik.TBIK_ERR_PAGE)     # behind the table's row
+    assert attempt([0], i32([page]), tbik.TBIK_ERR_PAGE)         # a page that the sequence does not have
+    assert attempt([1, 1], i32([0, 0]), tbik.TBIK_ERR_PAGE)      # the same slot twice
+    c.refs[c.table[2, 0].long()] = 2
+    assert attempt([2], i32([0]), tbik.TBIK_ERR_PAGE)            # a shared page
+    c.table[3, 0] = 8
+    assert attempt([3], i32([0]), tbik.TBIK_ERR_PAGE)            # outside the pool
+    assert not attempt([0], start[:1].contiguous(), tbik.TBIK_OK)
+
+
+# ---------------------------------------------------------------- attention
+
+def filled(ctx, H, D, page, seed, slots=None, spare=3):
+    """A cache whose sequences hold ctx tokens each, written in one call, rows in a mixed order."""
+    rows = list(np.random.RandomState(seed).permutation(slots or len(ctx))[:len(ctx)])
+    rows = [int(r) for r in rows]
+    used = sum(-(-n // page) for n in ctx)
+    c = Cache(slots or len(ctx), max(-(-n // page) for n in ctx) + 1, used + spare, H, D, page)
+    # the pool's pages in a mixed order: one page each in turn
+    left = list(ctx)
+    while any(left):
+        live = [i for i in range(len(ctx)) if left[i]]
+        n = [min(left[i], page) for i in live]
+        c.extend([rows[i] for i in live], n)
+        for i, m in zip(live, n):
+            left[i] -= m
+    g = torch.Generator(device=DEV).manual_seed(seed)
+    k = (torch.randn(sum(ctx), H, D, device=DEV, generator=g) * (1 + 3 * (torch.rand(H, D, device=DEV, generator=g) < .05))).to(torch.bfloat16)
+    v = torch.randn(sum(ctx), H, D, device=DEV, generator=g).to(torch.bfloat16)
+    c.append(k, v, i32([0] * len(ctx)), ctx, rows)
+    assert tbik.get_error() == tbik.TBIK_OK
+    return c, rows
+
+
+def reference(c, q, rows, start, n):
+    """float64 attention over what the device holds, and the largest |v| that each query could see."""
+    q = q.double().cpu().numpy()
+    T, NH, D = q.shape
+    G = NH // c.H
+    out, top, at = np.zeros(q.shape), np.zeros((T, NH)), 0
+    for r, s, m in zip(rows, start, n):
+        if m == 0:
+            continue
+        kv = c.stored(r, s + m)
+        for h in range(NH):
+            k, v = kv[0, h // G], kv[1, h // G]
+            a = q[at:at + m, h] @ k.T / np.sqrt(D)
+            a[np.arange(s + m)[None] > s + np.arange(m)[:, None]] = -np.inf
+            a = np.exp(a - a.max(1, keepdims=True))
+            out[at:at + m, h] = (a @ v) / a.sum(1, keepdims=True)
+            top[at:at + m, h] = np.abs(v).max()
+        at += m
+    return out, top
+
+
+def bound(ref, top):
+    """The weights are rounded to about 8 significant bits (2^-8 each, in the weights and in their sum: 2^-7 of the
+    largest value) with a floor of 2^-18 of the leaf's largest weight (128 keys of it: 2^-11), the scores are off by
+    less than 2^-13 (fp32 sums and hardware exponential at |s| < 100), and the output is rounded once (2^-8)."""
+    return (2.0 ** -7 + 2.0 ** -11 + 2.0 ** -12) * top[..., None] + 2.0 ** -8 * np.abs(ref)
+
+
+CASES = [
+    # H, heads, D, page, contexts before the call, new tokens
+    (1, 1, 128, 16, [0], [1]),
+    (1, 1, 64, 16, [0, 1, 126, 127, 128], [1, 1, 1, 1, 1]),
+    (2, 8, 128, 64, [0, 15, 63, 64, 127, 128, 129, 1000], [1] * 8),
+    (2, 10, 64, 32, [300, 5, 2000], [1, 1, 1]),
+    (3, 3, 128, 128, [255, 256, 4100], [1, 1, 1]),
+    (2, 8, 128, 16, [0, 100, 120, 500], [5, 1, 30, 0]),
+    (1, 16, 128, 32, [10, 0], [3, 140]),
+    (2, 2, 64, 64, [0, 700, 1], [300, 17, 129]),
+    (1, 64, 128, 64, [130], [2]),
+    (2, 12, 64, 128, [1, 3000, 250], [9, 8, 10]),
+    (4, 32, 128, 64, [900, 77], [64, 200]),
+]
+
+
+@pytest.mark.parametrize("H,heads,D,page,before,n", CASES)
+def test_attention_matches_binary64(H, heads, D, page, before, n):
+    c, rows = filled([b + m for b, m in zip(before, n)], H, D, page, seed=len(before) + page + D, slots=len(before) + 2)
+    T = sum(n)
+    g = torch.Generator(device=DEV).manual_seed(5)
+    q = (torch.randn(T + 2, heads, D, device=DEV, generator=g) * 2).to(torch.bfloat16)
+    out = torch.full_like(q, 7.0)
+    # two rows behind the last sequence stay as they are
+    got = tbik.cache_attention(q, c.pages[0], c.scales[0], c.table, i32(before), cu=cu_of(n), rows=i32(rows), out=out,
+                               max_q=max(n), max_keys=max(b + m for b, m in zip(before, n)))
+    assert tbik.get_error() == tbik.TBIK_OK
+    assert (got[T:] == 7.0).all()
+    ref, top = reference(c, q[:T], rows, before, n)
+    err = np.abs(got[:T].double().cpu().numpy() - ref)
+    assert (err <= bound(ref, top)).all(), float((err / bound(ref, top)).max())
+    if all(m == 1 for m in n):  # the form without cu, bounds left to their defaults, in place
+        one = q[:T].clone()
+        tbik.cache_attention(one, c.pages[0], c.scales[0], c.table, i32(before), rows=i32(rows), out=one)
+        assert torch.equal(one, got[:T])
+
+
+def test_attention_bits_do_not_depend_on_batch_split_or_pages():
+    H, heads, D = 2, 8, 128
+    before, n = [0, 60, 127, 500, 2600, 1023, 9000], [1, 80, 2, 33, 40, 1, 5]
+    outs = []
+    g = torch.Generator(device=DEV).manual_seed(11)
+    q = torch.randn(sum(n), heads, D, device=DEV, generator=g).to(torch.bfloat16)
+    for page in (16, 64):
+        # equal contents need equal scales: one scale for all pages
+        c, rows = filled([b + m for b, m in zip(before, n)], H, D, page, seed=3)
+        gen = torch.Generator().manual_seed(1)
+        vals = torch.randn(2, H, max(b + m for b, m in zip(before, n)) + 128, D, generator=gen).mul(60).clamp(-448, 448)
+        byts = vals.to(torch.float8_e4m3fn).view(torch.uint8).to(DEV)
+        for r, b, m in zip(rows, before, n):
+            for j in range(-(-(b + m) // page)):
+                x = byts[:, :, j * page:(j + 1) * page].reshape(2, H, page // 8, 8, D // 16, 16).transpose(3, 4)
+                raw(c.pages)[0][:, int(c.book.table[r, j])] = x
+        c.scales.fill_(2.0 ** -6)
+        whole = c.attend(q, i32(before), n, rows)
+        outs.append(whole)
+        # one query at a time, one sequence at a time
+        at = 0
+        for r, b, m in zip(rows, before, n):
+            part = q[at:at + m].contiguous()
+            assert torch.equal(c.attend(part, i32([b]), [m], [r]), whole[at:at + m])
+            pick = sorted({0, m // 2, m - 1})
+            single = c.attend(part[pick].contiguous(), i32([b + t for t in pick]), [1] * len(pick), [r] * len(pick), packed=False)
+            assert torch.equal(single, whole[at:at + m][pick])
+            at += m
+        # a large batch of the same sequence: another split of the work
+        many = 40
+        qq = q[-1:].repeat(many, 1, 1).contiguous()
+        res = c.attend(qq, i32([before[-1] + n[-1] - 1] * many), [1] * many, [rows[-1]] * many, packed=False)
+        assert torch.equal(res, whole[-1:].expand_as(res))
+        # heads by themselves: the same bits for any split of the heads
+        for h in range(H):
+            one = tbik.cache_attention(q[:, h * 4:h * 4 + 4].contiguous(), c.pages[0][:, :, h:h + 1].contiguous(),
+                                       c.scales[0][:, :, h:h + 1].contiguous(), c.table, i32(before), cu=cu_of(n), rows=i32(rows))
+            assert torch.equal(one, whole[:, h * 4:h * 4 + 4])
+    assert torch.equal(outs[0], outs[1])
+    assert tbik.get_error() == tbik.TBIK_OK
+
+
+def test_attention_with_page_scales_far_apart():
+    """Neighbouring pages whose scales differ by many binades, and keys so large that one weight takes all."""
+    H, D, page = 1, 128, 16
+    c = Cache(1, 20, 24, H, D, page)
+    n = 300
+    start = c.extend([0], [n])
+    g = torch.Generator(device=DEV).manual_seed(2)
+    size = torch.exp2(torch.randint(-14, 4, (n // page + 1,), device=DEV, generator=g).float()).repeat_interleave(page)[:n, None, None]
+    k = (torch.randn(n, H, D, device=DEV, generator=g) * size).to(torch.bfloat16)
+    v = (torch.randn(n, H, D, device=DEV, generator=g) * size.flip(0)).to(torch.bfloat16)
+    c.append(k, v, start, [n], [0])
+    q = (torch.randn(3, 4, D, device=DEV, generator=g)).to(torch.bfloat16)
+    q[1] *= 2.0 ** -20
+    got = c.attend(q, i32([n - 3]), [3], [0]).double().cpu().numpy()
+    ref, top = reference(c, q, [0], [n - 3], [3])
+    # |s| reaches a few thousand here: an fp32 score is off by up to 2^-22 |s| < 2^-9, and so is its weight
+    assert (np.abs(got - ref) <= bound(ref, top) + 2.0 ** -8 * top[..., None]).all()
+
+
+def test_attention_refuses_or_marks_what_cannot_be():
+    H, D, page = 2, 64, 32
+    c, rows = filled([40, 200, 70], H, D, page, seed=1)
+    q = torch.randn(3, 4, D, device=DEV).to(torch.bfloat16)
+    good = c.attend(q, i32([39, 199, 69]), [1, 1, 1], rows, packed=False)
+
+    def bad(start, rws, code, which, **kw):
+        got = c.attend(q, i32(start), [1, 1, 1], rws, packed=False, **kw)
+        assert tbik.get_error() == code
+        nan = torch.isnan(got).all(-1).all(-1).tolist()
+        assert nan == [b in which for b in range(3)]
+        for b in range(3):
+            assert b in which or torch.equal(got[b], good[b])
+
+    bad([39, -1, 69], rows, tbik.TBIK_OK, {1})                                  # not granted
+    bad([39, 199, 69], [rows[0], 3, -1], tbik.TBIK_ERR_PAGE, {1, 2})            # no such slots
+    bad([39, 199, 69], rows, tbik.TBIK_ERR_PAGE, {1}, max_keys=199)             # beyond the bound
+    bad([39, c.table.shape[1] * page, 69], rows, tbik.TBIK_ERR_PAGE, {1})       # beyond the table
+    saved = c.table.clone()
+    c.table[rows[1], 2] = c.refs.numel()                                        # a page outside the pool
+    bad([39, 199, 69], rows, tbik.TBIK_ERR_PAGE, {1})
+    c.table[rows[1], 2] = -1
+    bad([39, 199, 69], rows, tbik.TBIK_ERR_PAGE, {1})
+    c.table.copy_(saved)
+    with pytest.raises(ValueError):
+        c.attend(q[:2].contiguous(), i32([39, 199, 69]), [1, 1, 1], rows, packed=False)
+    with pytest.raises(ValueError):
+        c.attend(q[:, :, :32].contiguous(), i32([39, 199, 69]), [1, 1, 1], rows, packed=False)
+    with pytest.raises(ValueError):
+        c.attend(q[:, ::2], i32([39, 199, 69]), [1, 1, 1], rows, packed=False)
+    with pytest.raises(tbik.TbikError):
+        c.attend(torch.zeros(3, 3, D, dtype=torch.bfloat16, device=DEV), i32([39, 199, 69]), [1, 1, 1], rows, packed=False)
+    with pytest.raises(tbik.TbikError):  # a workspace that is too small
+        need = tbik.cache_attention_workspace(3, 3, 1, 224, 4, H, D, page)
+        if need == 0:
+            raise tbik.TbikError(tbik.TBIK_ERR_WORKSPACE, "none needed")
+        c.attend(q, i32([39, 199, 69]), [1, 1, 1], rows, packed=False, workspace=torch.empty(16, dtype=torch.uint8, device=DEV))
+    assert c.attend(q[:0].contiguous(), i32([]), [], [], packed=False).shape == (0, 4, D)
+
+
+def test_attention_on_other_streams_and_in_graphs():
+    """Two captured graphs that share a workspace, replayed in turn, a call on a side stream, and the eager call give
+    the same bits."""
+    H, heads, D, page = 2, 8, 128, 16
+    c, rows = filled([3000, 40, 700], H, D, page, seed=9)
+    q = [torch.randn(3, heads, D, device=DEV).to(torch.bfloat16) for _ in range(2)]
+    start = i32([2999, 39, 699])
+    args = (c.pages[0], c.scales[0], c.table, start)
+    kw = dict(rows=i32(rows), max_keys=3000)
+    need = tbik.cache_attention_workspace(3, 3, 1, 3000, heads, H, D, page)
+    ws = torch.empty(max(need, 16), dtype=torch.uint8, device=DEV)
+    eager = [tbik.cache_attention(x, *args, **kw) for x in q]
+    outs = [torch.zeros_like(x) for x in q]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    graphs = []
+    with torch.cuda.stream(side):
+        res = tbik.cache_attention(q[0], *args, **kw)
+        for x, o in zip(q, outs):
+            g = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(g, stream=side):
+                tbik.cache_attention(x, *args, out=o, workspace=ws, **kw)
+            graphs.append(g)
+    torch.cuda.current_stream().wait_stream(side)
+    ws.fill_(255)
+    for _ in range(3):
+        for g in graphs:
+            g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(res, eager[0]) and all(torch.equal(a, b) for a, b in zip(outs, eager))
+    assert tbik.get_error() == tbik.TBIK_OK
+
+
+# ---------------------------------------------------------- page operations
+
+def stamp(c):
+    """Every page's bytes name it."""
+    L, _, N = c.pages.shape[:3]
+    g = torch.Generator(device=DEV).manual_seed(4)
+    raw(c.pages).copy_(torch.randint(0, 127, c.pages.shape, dtype=torch.uint8, device=DEV, generator=g))
+    c.scales.copy_(torch.exp2(torch.randint(-9, 9, c.scales.shape, device=DEV, generator=g).float()))
+    return raw(c.pages).clone(), c.scales.clone()
+
+
+def check_moves(c, before, moves):
+    ref, sc = before
+    for a, b in moves:
+        ref[:, :, b], sc[:, :, b] = ref[:, :, a].clone(), sc[:, :, a].clone()
+    assert torch.equal(raw(c.pages), ref) and torch.equal(c.scales, sc)
+
+
+@pytest.mark.parametrize("seed,slots,max_pages,num_pages,page,H,D,layers", [
+    (0, 6, 5, 17, 16, 1, 64, 1), (1, 40, 9, 203, 32, 3, 128, 2), (2, 5, 3, 7, 128, 2, 64, 3),
+    (3, 300, 4, 4500, 16, 1, 64, 1)])
+def test_random_life_of_pages(seed, slots, max_pages, num_pages, page, H, D, layers):
+    r = np.random.RandomState(seed)
+    c = Cache(slots, max_pages, num_pages, H, D, page, layers)
+    refused = 0
+    for step in range(40):
+        before = stamp(c)
+        op = r.choice(["extend", "extend", "fork", "free", "compact"])
+        moves = []
+        if op == "extend":
+            rows = r.permutation(slots)[:r.randint(1, min(slots, 40) + 1)].tolist()
+            n = r.randint(0, 2 * page, len(rows)).tolist()
+            refused += c.extend(rows, n)[0].item() == -1
+        elif op == "fork":
+            empty = np.flatnonzero(c.book.lens == 0)
+            children = r.permutation(empty)[:r.randint(0, 6)].tolist()
+            parents = r.choice([x for x in range(slots) if x not in children], len(children)).tolist()
+            tbik.cache_fork(c.pages, c.scales, c.table, c.lens, c.refs, i32(parents), i32(children))
+            moves = c.book.fork(parents, children)
+            refused += moves is None
+            moves = moves or []
+        elif op == "free":
+            rows = r.randint(0, slots, r.randint(0, 5)).tolist()  # a slot may come twice
+            tbik.cache_free(c.table, c.lens, c.refs, i32(rows), page=page)
+            c.book.free(rows)
+        else:
+            live = tbik.cache_compact(c.pages, c.scales, c.table, c.lens, c.refs)
+            n, moves = c.book.compact()
+            assert live.item() == n
+        c.check()
+        check_moves(c, before, moves)
+        tbik.get_error()
+    assert refused or seed in (1, 3)
+
+
+def test_page_operations_refuse_without_a_trace():
+    c = Cache(4, 3, 6, 2, 64, 16)
+    c.extend([0, 1], [20, 16])
+    before = stamp(c)
+
+    def refused(f):
+        f()
+        assert tbik.get_error() == tbik.TBIK_ERR_PAGE
+        c.check()
+        check_moves(c, before, [])
+
+    ext = lambda rows, n: (lambda: c.extend(rows, n))  # noqa: E731
+    fork = lambda p, ch: (lambda: tbik.cache_fork(c.pages, c.scales, c.table, c.lens, c.refs, i32(p), i32(ch)))  # noqa: E731
+    copy = lambda a, b: (lambda: tbik.cache_copy(c.pages, c.scales, i32(a), i32(b)))  # noqa: E731
+    for f in (ext([0, 4], [1, 1]), ext([-1], [1]), ext([2, 2], [1, 1]), ext([2], [-1]), ext([2], [49]),
+              ext([0, 1, 2], [28, 32, 1]),  # one page more than there are
+              fork([0], [1]), fork([0, 0], [2, 2]), fork([4], [2]), fork([0], [4]), fork([2], [2]), fork([0, 2], [2, 3]),
+              copy([0], [6]), copy([-1], [1]), copy([0, 1], [2, 2]), copy([0, 1], [1, 3])):
+        refused(f)
+    refused(lambda: tbik.cache_free(c.table, c.lens, c.refs, i32([9]), page=16))
+    tbik.cache_copy(c.pages, c.scales, i32([0, 0, 1]), i32([5, 3, 4]))
+    check_moves(c, before, [(0, 5), (0, 3), (1, 4)])
+    c.extend([0, 1, 2], [28, 16, 0])  # exactly what is left
+    assert tbik.get_error() == tbik.TBIK_OK
+    for f in (lambda: tbik.cache_extend(c.table, c.lens, c.refs, i32([1, 1]), page=16, rows=i32([0])),
+              lambda: tbik.cache_extend(c.table, c.lens, c.refs[:5].float(), i32([1]), page=16),
+              lambda: tbik.cache_fork(c.pages[0], c.scales[0], c.table, c.lens, c.refs, i32([0]), i32([3])),
+              lambda: tbik.cache_compact(c.pages, c.scales, c.table, c.lens, c.refs[:4].clone())):
+        with pytest.raises((ValueError, TypeError)):
+            f()
+    for f in (lambda: tbik.cache_extend(c.table, c.lens, c.refs, i32([1]), page=24),
+              lambda: tbik.cache_copy(c.pages, c.scales, i32([0]), i32([1]), workspace=torch.empty(8, dtype=torch.uint8, device=DEV)),
+              lambda: tbik.cache_extend(c.table, c.lens, c.refs, i32([1] * 5), page=16)):
+        with pytest.raises(tbik.TbikError):
+            f()
+
+
+def test_a_large_pool():
+    """Page numbers over many scan steps, and page bytes behind 2^32."""
+    H, D, page, num = 8, 128, 128, 20000  # 5.2 GB
+    c = Cache(3, 19990, num, H, D, page)
+    c.extend([0], [19980 * page])
+    start = c.extend([1], [page + 3])
+    k, v = tokens(1, page + 3, H, D), tokens(2, page + 3, H, D)
+    c.append(k, v, start, [page + 3], [1])
+    check_written(c, 1, k, v)
+    q = torch.randn(1, H, D, device=DEV).to(torch.bfloat16)
+    got = c.attend(q, i32([page + 2]), [1], [1], packed=False, max_keys=page + 3).double().cpu().numpy()
+    ref, top = reference(c, q, [1], [page + 2], [1])
+    assert (np.abs(got - ref) <= bound(ref, top)).all()
+    tbik.cache_free(c.table, c.lens, c.refs, i32([0]), page=page)
+    c.book.free([0])
+    live = tbik.cache_compact(c.pages, c.scales, c.table, c.lens, c.refs)
+    assert c.book.compact()[0] == live.item() == 2
+    c.check()
+    check_written(c, 1, k, v)
+    assert torch.equal(c.attend(q, i32([page + 2]), [1], [1], packed=False, max_keys=page + 3).double().cpu(), torch.from_numpy(got))
+    assert tbik.get_error() == tbik.TBIK_OK

@@ -1,0 +1,196 @@
+"""Sampling against its definition in binary64: every filter and their combinations, odd vocabularies, masks, ties,
+infinities and NaN, and the independence of a row's token from the batch."""
+import numpy as np
+import pytest
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+
+import invariant_tree_ordered_b200 as tbik  # noqa: E402
+
+DEV = "cuda"
+
+
+def ref_row(z, u, temp, k, p, mp):
+    """(token, kept [V], its slack): the definition in binary64; -1 when there is nothing to choose."""
+    z = z.astype(np.float64)
+    V = len(z)
+    if np.isnan(z).any() or z.max() == -np.inf:
+        return -1, np.zeros(V, bool), None
+    m = z.max()
+    order = np.lexsort((np.arange(V), -z))
+    if not temp > 0 or k == 1:
+        return int(order[0]), z == z[order[0]], None
+    with np.errstate(over="ignore", invalid="ignore"):
+        w = np.where(z == m, 1.0, np.exp((z - m) / temp))
+    w[z == -np.inf] = 0
+    if np.isinf(m):
+        w = (z == m).astype(float)
+    keep = np.zeros(V, bool)
+    keep[order[:k] if 0 < k < V else order] = True
+    if p < 1:
+        ws = (w * keep)[order]
+        before = np.cumsum(ws) - ws
+        sel = before < p * ws.sum()
+        sel[0] = True
+        keep[order] &= sel
+    keep &= (w >= mp) | (z == m)
+    c = np.cumsum(w * keep)
+    tok = int(np.searchsorted(c, u * c[-1], side="right"))
+    return min(tok, int(np.flatnonzero(w * keep)[-1])), keep, (w, c)
+
+
+def check(logits, u, temp=None, k=None, p=None, mp=None):
+    B, V = logits.shape
+    f = lambda x, dt: None if x is None else torch.tensor(np.broadcast_to(x, B).copy(), dtype=dt, device=DEV)  # noqa: E731
+    ut = torch.tensor(np.broadcast_to(u, B).copy(), dtype=torch.float32, device=DEV)
+    args = dict(temperature=f(temp, torch.float32), top_k=f(k, torch.int32), top_p=f(p, torch.float32), min_p=f(mp, torch.float32))
+    got = tbik.sample(logits, ut, **args)
+    again = tbik.sample(logits, ut, **args)
+    assert torch.equal(got, again)
+    z = logits.float().cpu().numpy()
+    val = lambda t, d, b: d if t is None else float(t[b])  # noqa: E731
+    got = got.cpu().numpy()
+    for b in range(B):
+        tok, keep, more = ref_row(z[b], float(ut[b]), val(args["temperature"], 1.0, b), int(val(args["top_k"], 0, b)),
+                                  val(args["top_p"], 1.0, b), val(args["min_p"], 0.0, b))
+        if got[b] == tok:
+            continue
+        # a border between two tokens may move by the weights' own precision: fp32 weights and their units of 2^-32
+        # (sums off by less than 2^-20 of the total), nothing else
+        assert more is not None and 0 <= got[b] < V, (b, got[b], tok)
+        w, c = more
+        x, slack = float(ut[b]) * c[-1], 2.0 ** -20 * c[-1]
+        assert c[got[b]] - w[got[b]] - slack <= x <= c[got[b]] + slack and w[got[b]] > 0, (b, got[b], tok)
+    return got
+
+
+def rows(seed, B, V, std=2.5, half=False, peaks=True):
+    g = torch.Generator(device=DEV).manual_seed(seed)
+    x = torch.randn(B, V, device=DEV, generator=g) * std
+    if peaks and V > 20:
+        x.scatter_add_(1, torch.randint(0, V, (B, 8), device=DEV, generator=g), torch.rand(B, 8, device=DEV, generator=g) * 9)
+    return x.to(torch.bfloat16) if half else x
+
+
+def uni(seed, B):
+    return np.random.RandomState(seed).rand(B).astype(np.float32)
+
+
+@pytest.mark.parametrize("half", [False, True])
+@pytest.mark.parametrize("V", [1, 2, 15, 17, 511, 1000, 4097, 32000, 50257, 151936, 393216])
+def test_every_filter(V, half):
+    B = 12 if V < 100000 else 6
+    z = rows(V, B, V, half=half)
+    check(z, uni(1, B))
+    check(z, uni(2, B), temp=np.linspace(0.2, 2.0, B))
+    check(z, uni(3, B), k=np.resize([1, 2, 50, 1000, V, 0], B))
+    check(z, uni(4, B), p=np.resize([0.9, 0.5, 0.999, 1.0, 0.01, 0.0], B))
+    check(z, uni(5, B), mp=np.resize([0.0, 0.1, 0.5, 1.0], B))
+    check(z, uni(6, B), temp=np.resize([0.0, 0.7, 1.0, 3.0], B), k=np.resize([0, 40, 3, 2000, 5], B),
+          p=np.resize([0.95, 1.0, 0.6], B), mp=np.resize([0.0, 0.05], B))
+    assert tbik.get_error() == tbik.TBIK_OK
+
+
+@pytest.mark.parametrize("V", [300, 40000, 151936])
+def test_flat_rows_and_large_k(V):
+    """Almost flat and exactly flat rows: a border with thousands of tokens."""
+    B = 6
+    check(rows(1, B, V, std=0.01, peaks=False), uni(1, B), p=np.resize([0.9, 0.3], B), k=np.resize([0, V // 2, V - 1], B))
+    check(rows(2, B, V, std=0.01, peaks=False, half=True), uni(2, B), p=np.resize([0.9, 0.3], B), k=np.resize([0, V // 3, V - 1], B))
+    flat = torch.full((B, V), -3.5, device=DEV)
+    check(flat, uni(3, B), k=np.resize([0, 7, V // 2], B), p=np.resize([1.0, 0.25], B))
+    lowest = torch.full((B, V), torch.finfo(torch.float32).min, device=DEV)
+    check(lowest, uni(4, B), k=np.resize([0, 9], B), p=0.5)
+    check(rows(5, B, V, std=1e-30, peaks=False), uni(5, B), k=np.resize([3, V // 2], B), p=0.7)
+    check(rows(6, B, V, std=50), uni(6, B), temp=np.resize([1e-3, 100.0, 1e4], B), k=np.resize([0, V // 2, 5000], B), p=0.99)
+
+
+def test_equal_logits_keep_the_lower_indices():
+    V = 5000
+    z = torch.zeros(4, V, device=DEV)
+    z[:, 1000:] = 1.0
+    z[:, 4321] = 2.0
+    # the top 11: token 4321 and the ten lowest indices of the next level
+    got = check(z, [0.0, 0.999999, 0.3, 0.9], k=11)
+    assert got[0] == 1000 and got[1] == 4321
+    # signed zeros are equal
+    s = torch.zeros(1, 64, device=DEV)
+    s[0, ::2] = -0.0
+    assert check(s, [0.0], temp=0.0)[0] == 0
+    assert check(s, [0.999999], k=3)[0] == 2
+
+
+def test_masked_and_broken_rows():
+    V = 3000
+    z = rows(1, 8, V)
+    z[0, :-1] = float("-inf")                       # one token left
+    z[1, :] = float("-inf")                         # nothing left
+    z[2, 5:] = torch.finfo(torch.float32).min       # a mask of the type's lowest value
+    z[3, 17] = float("inf")
+    z[4, 3], z[4, 9] = float("inf"), float("inf")
+    z[5, 100:] = float("-inf")
+    for kw in ({}, {"k": 50}, {"p": 0.9}, {"k": 20, "p": 0.5, "mp": 0.1}, {"temp": 0.0}, {"temp": 1e-40}, {"k": 200}):
+        got = check(z, uni(3, 8), **kw)
+        assert got[0] == V - 1 and got[1] == -1 and got[3] == 17 and got[4] in (3, 9) and got[5] < 100
+    assert tbik.get_error() == tbik.TBIK_OK
+    z[6, 2999] = float("nan")
+    got = check(z, uni(4, 8), k=5)
+    assert got[6] == -1 and got[7] >= 0
+    assert tbik.get_error() == tbik.TBIK_ERR_VALUE
+
+
+def test_the_ends_of_u():
+    z = rows(5, 6, 777)
+    check(z, [0.0, 1.0 - 2.0 ** -24, 2.0 ** -149, 0.5, 1e-10, 0.25], k=30)
+    u = torch.tensor([1.0, -1.0, float("nan"), 7.0, 0.0, 0.5], device=DEV)  # outside [0, 1): the nearest token there is
+    got = tbik.sample(z, u).cpu().numpy()
+    order = [int(np.flatnonzero(np.isfinite(z[b].cpu().numpy()))[i]) for b, i in ((1, 0), (2, 0), (4, 0))]
+    assert got[1] == order[0] and got[2] == order[1] and got[4] == order[2]
+    assert (got >= 0).all() and (got < 777).all()
+
+
+def test_a_row_does_not_depend_on_its_batch():
+    V = 60001  # rows that start at odd addresses
+    for half in (False, True):
+        z = rows(7, 300, V, half=half)
+        u = torch.from_numpy(uni(8, 300)).to(DEV)
+        t = torch.from_numpy(np.resize([0.5, 1.0, 1.5], 300).astype(np.float32)).to(DEV)
+        k = torch.from_numpy(np.resize([0, 40, 5000], 300).astype(np.int32)).to(DEV)
+        p = torch.from_numpy(np.resize([0.9, 1.0], 300).astype(np.float32)).to(DEV)
+        whole = tbik.sample(z, u, temperature=t, top_k=k, top_p=p)
+        for a, b in ((0, 1), (1, 3), (17, 40), (299, 300)):
+            part = tbik.sample(z[a:b].clone(), u[a:b].clone(), temperature=t[a:b].clone(), top_k=k[a:b].clone(), top_p=p[a:b].clone())
+            assert torch.equal(part, whole[a:b])
+        perm = torch.randperm(300, generator=torch.Generator().manual_seed(1)).to(DEV)
+        assert torch.equal(tbik.sample(z[perm], u[perm], temperature=t[perm], top_k=k[perm], top_p=p[perm]), whole[perm])
+
+
+def test_streams_graphs_and_refusals():
+    z, u = rows(9, 5, 32000), torch.from_numpy(uni(9, 5)).to(DEV)
+    eager = tbik.sample(z, u)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    out = torch.zeros(5, dtype=torch.int32, device=DEV)
+    with torch.cuda.stream(side):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=side):
+            tbik.sample(z, u, out=out)
+    torch.cuda.current_stream().wait_stream(side)
+    g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, eager)
+    for f in (lambda: tbik.sample(z[:, ::2], u), lambda: tbik.sample(z, u[:4]), lambda: tbik.sample(z[0], u),
+              lambda: tbik.sample(z, u, out=torch.zeros(4, dtype=torch.int32, device=DEV)),
+              lambda: tbik.sample(z, u, temperature=u[:2])):
+        with pytest.raises(ValueError):
+            f()
+    for f in (lambda: tbik.sample(z.half(), u), lambda: tbik.sample(z, u.double()), lambda: tbik.sample(z, u, top_k=u)):
+        with pytest.raises(TypeError):
+            f()
+    with pytest.raises(tbik.TbikError):
+        tbik.sample(torch.zeros(1, 393217, device=DEV), u[:1])
+    with pytest.raises(tbik.TbikError):
+        tbik.sample(torch.zeros(8 * 5 + 1, device=DEV)[1:].view(5, 8), u)
+    assert tbik.sample(z[:0], u[:0]).shape == (0,)
