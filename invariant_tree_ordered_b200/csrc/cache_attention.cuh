@@ -4,14 +4,41 @@
 // in the other attentions of the library: leaves of 128 consecutive positions, each a (max, sum, weighted value sum)
 // summary, combined by the halving tree over the ceil((i + 1) / 128) leaves, so a row's bits depend only on its
 // query and the cache's contents, never on the batch or on how the work is split.
+//
+// The bytes of a page go to the tensor cores as they lie in the cache (tcgen05 kind::f8f6f4, unswizzled operands), so
+// nothing is ever widened.  What is not 8 bits wide is given to them as two e4m3 terms of 4 significant bits:
+//   query   q 2^x = h + l / 32, x such that the row's largest |q| 2^x lies in [128, 256): exact down to 2^-14 of it;
+//   weight  256 f p = h + l, rounded at 2^-9 relative or 2^-18 of the leaf's largest (f below).
+// With keys as the 128 rows of an MMA and queries as its columns, few queries waste few columns, which suits a decode
+// step (G query heads of one token share a kv head):
+//   S^T = K [h | l]     M = 128 keys, N = 2 rows, K = head_dim
+//   a_j = (S_h + S_l / 32) kscale_j;  m = max over the leaf's visible keys;  p_j = 2^((a_j - m) c), c = 2^-x log2(e) / sqrt(D)
+//   f_j = vscale_j / (largest vscale among the row's visible pages of the leaf), a power of two
+//   s = sum of p_j in fp32: within 32 keys by halves (16 apart first), then (w0 + w1) + (w2 + w3)
+//   O^T = V^T [256 f p] M = 128 dims, N = rows, K = 128 keys, h and l one after the other
+// Combining two summaries: M = max, e = 2^(m - M) (1 for the side that holds M), s = fma(s', e', s e), o likewise.
+//
+// One CTA works on tiles of R = RW * NWG rows (query, head) that share a kv head and a 128-position block, hence the
+// number of leaves.  Warp 0 copies pages to shared memory (cp.async.bulk, one copy per page and operand), warp 1 issues
+// the MMAs, and each group of 4 warps has RW rows: a thread is a key for the scores and a dim for the values, so its
+// summaries' value parts live in its TMEM lane (pending ones too).
+//
+// Split: the work is cut into units (tile, tree node of at most T leaves) and each CTA takes a contiguous run of them
+// by weight; T is chosen on the device such that a CTA has about CATT_UNITS units.  A tile whose tree is cut leaves its
+// nodes' summaries in the workspace, and a second kernel evaluates the tree above them.  Nodes are subtrees of the row's
+// own tree, so the bits do not depend on the cut.
 #pragma once
+
+#include <cuda_fp16.h>
 
 #include "cache.cuh"
 
 namespace tbik {
 
 constexpr int CATT_LEAF = 128;
-constexpr int CATT_MAX_LEVELS = 20;
+constexpr int CATT_UNITS = 6;       // units per CTA that the split aims at
+constexpr int CATT_MAX_NODE = 64;   // leaves of a unit: six pending summaries
+constexpr int CATT_PENDING = 6;
 
 struct CacheAttParams {
     const uint16_t* q;
@@ -23,104 +50,1081 @@ struct CacheAttParams {
     const int32_t* rows;
     uint16_t* out;
     int tokens, batch, slots, max_pages, num_pages, heads, kv_heads, page, max_q, max_keys;
-    float scale;  // log2(e) / sqrt(head_dim)
+    int group;       // heads / kv_heads
+    int blocks;      // 128-position blocks that a sequence's new tokens can touch
+    float scale;     // log2(e) / sqrt(head_dim)
+    // workspace: number of cut tiles, their descriptors, and the nodes' summaries
+    int* count;
+    int4* tiles;     // [max_slots / 2][2]
+    float2* ms;      // [max_slots][R]
+    float* o;        // [max_slots][R][D]
+    int max_slots;
+    unsigned long long wait_cycles;
+    unsigned debug;
 };
 
-__device__ __forceinline__ float e4m3_f32(uint32_t b) {
-    const uint32_t m = b & 7u, f = (b >> 3) & 15u;
-    float v = f ? __uint_as_float(((f + 120u) << 23) | (m << 20)) : (float)m * 0x1p-9f;
-    if ((b & 0x7Fu) == 0x7Fu) v = __uint_as_float(0x7fc00000u);
-    return (b & 0x80u) ? -v : v;
+template <int D_, int RW_, int NWG_>
+struct CattCfg {
+    static constexpr int D = D_, RW = RW_, NWG = NWG_, R = RW * NWG;
+    static constexpr int NQ = 2 * RW;                // columns of S
+    static constexpr int NP = RW < 16 ? 16 : RW;     // columns of O (an MMA of 128 rows has at least 16)
+    static constexpr int SBUF = RW == 32 ? 1 : 2, OBUF = RW == 32 ? 1 : 2;
+    static constexpr int TPEND = RW == 32 ? 5 : 6;   // pending summaries in TMEM; the largest one may be in shared memory
+    static constexpr int S_COL = 0, O_COL = SBUF * NQ, ST_COL = O_COL + OBUF * NP;
+    static constexpr int WG_COLS = ST_COL + TPEND * RW;
+    static constexpr int COLS = NWG * WG_COLS <= 128 ? 128 : NWG * WG_COLS <= 256 ? 256 : 512;
+    static constexpr int CTAS = RW == 8 ? 3 : NWG == 1 ? 2 : 1;
+    static constexpr int THREADS = 64 + 128 * NWG;
+    static constexpr int TILE = 128 * D;             // bytes of a leaf's keys or values
+    static constexpr int STAGES = NWG == 2 ? 4 : RW == 16 && D == 128 ? 3 : D == 64 ? 4 : 2;
+    static constexpr int OFF_K = 0, OFF_V = STAGES * TILE, OFF_Q = 2 * STAGES * TILE;
+    static constexpr int QB = NQ * D, PB = 2 * 128 * NP;
+    static constexpr int OFF_P = OFF_Q + NWG * QB;
+    static constexpr int OFF_ST = OFF_P + NWG * PB;                          // the pending summary that TMEM has no room for
+    static constexpr int OFF_BAR = OFF_ST + (TPEND < CATT_PENDING ? NWG * RW * 128 * 4 : 0);
+    static constexpr int OFF_X = OFF_BAR + 512;
+    // per group of 4 warps, in floats: maxima [2][4][RW], sums [2][4][RW], constants [2][RW], value scales [2][8],
+    // and per warp: factors [3][RW], pending (m, s) [6][2][RW]
+    static constexpr int X_MAX = 0, X_SUM = 8 * RW, X_CST = 16 * RW, X_PV = 18 * RW, X_WARP = X_PV + 16;
+    static constexpr int X_PER_WARP = 3 * RW + CATT_PENDING * 2 * RW;
+    static constexpr int X_FLOATS = X_WARP + 4 * X_PER_WARP;
+    static constexpr int SMEM = OFF_X + NWG * X_FLOATS * 4;
+};
+
+__device__ __forceinline__ uint64_t smem_desc_flat(uint32_t saddr, uint32_t lbo, uint32_t sbo) {
+    return (uint64_t)((saddr & 0x3FFFFu) >> 4) | (uint64_t)((lbo >> 4) & 0x3FFFu) << 16 |
+           (uint64_t)((sbo >> 4) & 0x3FFFu) << 32 | (uint64_t)1 << 46;
+}
+__device__ __forceinline__ void tc_mma_f8(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+// e4m3 operands (format 0), fp32 accumulator; both operands K-major, or both MN-major.
+__host__ __device__ constexpr uint32_t idesc_e4m3_f32(int M, int N, int mn_major) {
+    return (1u << 4) | ((uint32_t)mn_major << 15) | ((uint32_t)mn_major << 16) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst), "l"(src),
+                 "r"(bytes), "r"(bar)
+                 : "memory");
+}
+__device__ __forceinline__ uint32_t pack_e4m3(float lo, float hi) {
+    uint16_t d;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(d) : "f"(hi), "f"(lo));
+    return d;
+}
+__device__ __forceinline__ float2 unpack_e4m3(uint32_t v) {
+    uint32_t h;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)v));
+    return __half22float2(*reinterpret_cast<__half2*>(&h));
+}
+__device__ __forceinline__ float warp_max_f32(float x) {
+    float r;
+    asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(x));
+    return r;
 }
 
-// One block of 128 threads per (packed token, head): a thread is a key for the scores and a dim for the values.
+template <int N>
+__device__ __forceinline__ void catt_ld(uint32_t addr, uint32_t (&r)[N]);
+template <int N>
+__device__ __forceinline__ void catt_st(uint32_t addr, const float (&v)[N]);
+template <>
+__device__ __forceinline__ void catt_ld<8>(uint32_t addr, uint32_t (&r)[8]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+        : "r"(addr)
+        : "memory");
+}
+template <>
+__device__ __forceinline__ void catt_ld<16>(uint32_t addr, uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(addr)
+        : "memory");
+}
+template <>
+__device__ __forceinline__ void catt_ld<32>(uint32_t addr, uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(addr)
+        : "memory");
+}
+template <>
+__device__ __forceinline__ void catt_ld<64>(uint32_t addr, uint32_t (&r)[64]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x64.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32, %33, %34, %35, %36, %37, %38, %39, %40, %41, %42, %43, %44, %45, %46, %47, %48, %49, %50, %51, %52, %53, %54, %55, %56, %57, %58, %59, %60, %61, %62, %63}, [%64];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31]), "=r"(r[32]), "=r"(r[33]), "=r"(r[34]), "=r"(r[35]), "=r"(r[36]), "=r"(r[37]), "=r"(r[38]), "=r"(r[39]), "=r"(r[40]), "=r"(r[41]), "=r"(r[42]), "=r"(r[43]), "=r"(r[44]), "=r"(r[45]), "=r"(r[46]), "=r"(r[47]), "=r"(r[48]), "=r"(r[49]), "=r"(r[50]), "=r"(r[51]), "=r"(r[52]), "=r"(r[53]), "=r"(r[54]), "=r"(r[55]), "=r"(r[56]), "=r"(r[57]), "=r"(r[58]), "=r"(r[59]), "=r"(r[60]), "=r"(r[61]), "=r"(r[62]), "=r"(r[63])
+        : "r"(addr)
+        : "memory");
+}
+template <>
+__device__ __forceinline__ void catt_st<8>(uint32_t addr, const float (&v)[8]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};\n\t"
+        "tcgen05.wait::st.sync.aligned;" ::"r"(addr),
+        "r"(__float_as_uint(v[0])), "r"(__float_as_uint(v[1])), "r"(__float_as_uint(v[2])), "r"(__float_as_uint(v[3])), "r"(__float_as_uint(v[4])), "r"(__float_as_uint(v[5])), "r"(__float_as_uint(v[6])), "r"(__float_as_uint(v[7]))
+        : "memory");
+}
+template <>
+__device__ __forceinline__ void catt_st<16>(uint32_t addr, const float (&v)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};\n\t"
+        "tcgen05.wait::st.sync.aligned;" ::"r"(addr),
+        "r"(__float_as_uint(v[0])), "r"(__float_as_uint(v[1])), "r"(__float_as_uint(v[2])), "r"(__float_as_uint(v[3])), "r"(__float_as_uint(v[4])), "r"(__float_as_uint(v[5])), "r"(__float_as_uint(v[6])), "r"(__float_as_uint(v[7])), "r"(__float_as_uint(v[8])), "r"(__float_as_uint(v[9])), "r"(__float_as_uint(v[10])), "r"(__float_as_uint(v[11])), "r"(__float_as_uint(v[12])), "r"(__float_as_uint(v[13])), "r"(__float_as_uint(v[14])), "r"(__float_as_uint(v[15]))
+        : "memory");
+}
+template <>
+__device__ __forceinline__ void catt_st<32>(uint32_t addr, const float (&v)[32]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};\n\t"
+        "tcgen05.wait::st.sync.aligned;" ::"r"(addr),
+        "r"(__float_as_uint(v[0])), "r"(__float_as_uint(v[1])), "r"(__float_as_uint(v[2])), "r"(__float_as_uint(v[3])), "r"(__float_as_uint(v[4])), "r"(__float_as_uint(v[5])), "r"(__float_as_uint(v[6])), "r"(__float_as_uint(v[7])), "r"(__float_as_uint(v[8])), "r"(__float_as_uint(v[9])), "r"(__float_as_uint(v[10])), "r"(__float_as_uint(v[11])), "r"(__float_as_uint(v[12])), "r"(__float_as_uint(v[13])), "r"(__float_as_uint(v[14])), "r"(__float_as_uint(v[15])), "r"(__float_as_uint(v[16])), "r"(__float_as_uint(v[17])), "r"(__float_as_uint(v[18])), "r"(__float_as_uint(v[19])), "r"(__float_as_uint(v[20])), "r"(__float_as_uint(v[21])), "r"(__float_as_uint(v[22])), "r"(__float_as_uint(v[23])), "r"(__float_as_uint(v[24])), "r"(__float_as_uint(v[25])), "r"(__float_as_uint(v[26])), "r"(__float_as_uint(v[27])), "r"(__float_as_uint(v[28])), "r"(__float_as_uint(v[29])), "r"(__float_as_uint(v[30])), "r"(__float_as_uint(v[31]))
+        : "memory");
+}
+
+// ------------------------------------------------------------------ the split
+
+// Leaves [lo, lo + size) of node v (of 2^d, left to right) at depth d of the tree over L leaves; size may be 0 where a
+// single leaf cannot be cut any further.
+__host__ __device__ __forceinline__ void catt_node(int L, int d, int v, int& lo, int& size) {
+    lo = 0;
+    size = L;
+    for (int k = d - 1; k >= 0; --k) {
+        const int h = (size + 1) >> 1;
+        if ((v >> k) & 1) {
+            lo += h;
+            size -= h;
+        } else {
+            size = h;
+        }
+    }
+}
+__host__ __device__ __forceinline__ int catt_depth(int L, int T) {
+    int d = 0;
+    while (((L + (1 << d) - 1) >> d) > T) ++d;
+    return d;
+}
+// Number of nodes that leaf j of a tree over n leaves closes.
+__host__ __device__ __forceinline__ int catt_pops(int n, int j) {
+    int pops = 0;
+    while (n > 1) {
+        if (j == n - 1) ++pops;
+        else pops = 0;
+        const int h = (n + 1) >> 1;
+        if (j < h) {
+            n = h;
+        } else {
+            j -= h;
+            n -= h;
+        }
+    }
+    return pops;
+}
+
+// The new tokens of a sequence within one block of 128 positions.
+struct CattItem {
+    int b, slot;    // sequence, table row
+    int tok0, i0;   // its first token (packed) and that token's position
+    int rows, L;    // (token, head) rows per kv head (0: nothing to do), leaves
+};
+
+// Sequence b's first packed token and their number (0 if cu makes no sense).
+__device__ __forceinline__ int catt_tokens(const CacheAttParams& p, int b, int& n) {
+    if (!p.cu) {
+        n = 1;
+        return b;
+    }
+    const int a = p.cu[b], e = p.cu[b + 1];
+    n = (a < 0 || e < a || e > p.tokens) ? 0 : e - a;
+    return a;
+}
+// How many of a sequence's n tokens (from its first on) have an answer.
+__device__ __forceinline__ int catt_usable(const CacheAttParams& p, int s, int slot, int n) {
+    if (s < 0 || slot < 0 || slot >= p.slots) return 0;
+    long long lim = min((long long)p.max_keys, (long long)p.max_pages * p.page) - s;
+    lim = min(min(lim, (long long)n), (long long)p.max_q);
+    return lim > 0 ? (int)lim : 0;
+}
+__device__ __forceinline__ CattItem catt_item(const CacheAttParams& p, int i, bool& bad) {
+    CattItem t;
+    int n;
+    t.b = i / p.blocks;
+    const int kb = i - t.b * p.blocks;
+    const int first = catt_tokens(p, t.b, n);
+    const int s = p.start[t.b];
+    t.slot = p.rows ? p.rows[t.b] : t.b;
+    const int use = catt_usable(p, s, t.slot, n);
+    bad |= use < n || (p.cu && n == 0 && (first < 0 || p.cu[t.b + 1] < first || p.cu[t.b + 1] > p.tokens));
+    const int blk = (use > 0 ? s >> 7 : 0) + kb;
+    const int lo = max(0, blk * CATT_LEAF - s), hi = (int)min((long long)use, (long long)(blk + 1) * CATT_LEAF - s);
+    t.L = blk + 1;
+    t.tok0 = first + lo;
+    t.i0 = s + lo;
+    t.rows = use > 0 && hi > lo ? (hi - lo) * p.group : 0;
+    return t;
+}
+
+// Where a CTA begins: set by the whole block, read by every role.
+struct CattPlan {
+    long long x0, x1, at;  // the CTA's run of the weight axis, and the weight before its first item
+    int item, slot_base, tile_base, T;
+};
+
+// A unit: node v of tile `tau` of kv head h of an item.
+template <int R>
+struct CattUnits {
+    CattItem it;
+    int item, h, tau, tiles, d, v, lo, size;
+    int slot_base, tile_base, T;
+    long long at, end;
+
+    __device__ __forceinline__ void enter(const CacheAttParams& p) {
+        bool bad = false;
+        it = catt_item(p, item, bad);
+        tiles = (it.rows + R - 1) / R;
+        d = catt_depth(it.L, T);
+    }
+    __device__ __forceinline__ int slot() const { return slot_base + ((h * tiles + tau) << d) + v; }
+    // The first unit that starts at or behind x0.
+    __device__ __forceinline__ bool first(const CacheAttParams& p, const CattPlan& pl) {
+        item = pl.item;
+        slot_base = pl.slot_base;
+        tile_base = pl.tile_base;
+        T = pl.T;
+        end = pl.x1;
+        if (item < 0 || pl.x0 >= pl.x1) return false;
+        enter(p);
+        const long long ht = (long long)p.kv_heads * tiles, y = pl.x0 - pl.at;
+        int a = 0, b = (1 << d) - 1;
+        while (a < b) {  // the last node whose units start at or before y
+            const int m = (a + b + 1) >> 1;
+            catt_node(it.L, d, m, lo, size);
+            if ((long long)(lo + min(m, lo)) * ht <= y) a = m;
+            else b = m - 1;
+        }
+        v = a;
+        catt_node(it.L, d, v, lo, size);
+        const long long base = (long long)(lo + min(v, lo)) * ht;
+        long long k = size ? (y - base + size) / (size + 1) : ht;
+        if (k >= ht) {
+            h = p.kv_heads - 1;
+            tau = tiles - 1;
+            at = pl.at + base + (size ? (ht - 1) * (size + 1) : 0);
+            return next(p);
+        }
+        h = (int)(k / tiles);
+        tau = (int)(k - (long long)h * tiles);
+        at = pl.at + base + k * (size + 1);
+        return at < end;
+    }
+    __device__ __forceinline__ bool next(const CacheAttParams& p) {
+        if (size) at += size + 1;
+        if (at >= end) return false;
+        if (++tau < tiles) return true;
+        tau = 0;
+        if (++h < p.kv_heads) return true;
+        h = 0;
+        while (++v < (1 << d)) {
+            catt_node(it.L, d, v, lo, size);
+            if (size) return true;
+        }
+        if (d > 0) {
+            slot_base += (p.kv_heads * tiles) << d;
+            tile_base += p.kv_heads * tiles;
+        }
+        do {
+            if (++item >= p.batch * p.blocks) return false;
+            enter(p);
+        } while (it.rows == 0);
+        v = 0;
+        catt_node(it.L, d, 0, lo, size);
+        return true;
+    }
+};
+
+// Sum over the block; every thread gets it.  `buf`: 32 values.
+__device__ __forceinline__ long long catt_block_sum(long long v, long long* buf) {
+#pragma unroll
+    for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    __syncthreads();
+    if ((threadIdx.x & 31) == 0) buf[threadIdx.x >> 5] = v;
+    __syncthreads();
+    v = 0;
+    for (int w = 0; w < (int)blockDim.x / 32; ++w) v += buf[w];
+    return v;
+}
+// Sum of the values of lower threads; `total` over the block.
+__device__ __forceinline__ long long catt_block_before(long long v, long long* buf, long long& total) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    long long s = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long y = __shfl_up_sync(0xffffffffu, s, o);
+        if (lane >= o) s += y;
+    }
+    __syncthreads();
+    if (lane == 31) buf[warp] = s;
+    __syncthreads();
+    long long b = 0;
+    total = 0;
+    for (int w = 0; w < (int)blockDim.x / 32; ++w) {
+        if (w < warp) b += buf[w];
+        total += buf[w];
+    }
+    return b + s - v;
+}
+
+// Fills `pl`; true if some token of the call has no answer.
+template <int R>
+__device__ __forceinline__ bool catt_plan(const CacheAttParams& p, CattPlan* pl, long long* buf) {
+    const int items = p.batch * p.blocks, tid = threadIdx.x, nt = blockDim.x;
+    bool bad = false;
+    long long leaves = 0;
+    for (int i = tid; i < items; i += nt) {
+        const CattItem t = catt_item(p, i, bad);
+        if (t.rows) leaves += (long long)t.L * p.kv_heads * ((t.rows + R - 1) / R);
+    }
+    leaves = catt_block_sum(leaves, buf);
+    const long long aim = (long long)gridDim.x * CATT_UNITS;
+    const int T = (int)min((long long)CATT_MAX_NODE, max(1ll, (leaves + aim - 1) / aim));
+    // weight of a unit: its leaves and one for its start
+    long long total = 0;
+    for (int i = tid; i < items; i += nt) {
+        const CattItem t = catt_item(p, i, bad);
+        if (t.rows) total += (long long)(t.L + min(t.L, 1 << catt_depth(t.L, T))) * p.kv_heads * ((t.rows + R - 1) / R);
+    }
+    total = catt_block_sum(total, buf);
+    const long long x0 = total / gridDim.x * blockIdx.x + total % gridDim.x * blockIdx.x / gridDim.x;
+    const long long x1 = total / gridDim.x * (blockIdx.x + 1) + total % gridDim.x * (blockIdx.x + 1) / gridDim.x;
+    if (tid == 0) {
+        pl->x0 = x0;
+        pl->x1 = x1;
+        pl->item = -1;
+        pl->T = T;
+    }
+    __syncthreads();
+    long long at = 0, cut = 0;  // cut: (slots << 32) + tiles of the cut ones
+    for (int base = 0; base < items; base += nt) {
+        const int i = base + tid;
+        long long w = 0, c = 0;
+        if (i < items) {
+            const CattItem t = catt_item(p, i, bad);
+            if (t.rows) {
+                const long long ht = (long long)p.kv_heads * ((t.rows + R - 1) / R);
+                const int d = catt_depth(t.L, T);
+                w = (long long)(t.L + min(t.L, 1 << d)) * ht;
+                if (d) c = ((ht << d) << 32) + ht;
+            }
+        }
+        long long wt, ct;
+        const long long wb = at + catt_block_before(w, buf, wt), cb = cut + catt_block_before(c, buf, ct);
+        if (w && wb <= x0 && x0 < wb + w) {
+            pl->item = i;
+            pl->at = wb;
+            pl->slot_base = (int)(cb >> 32);
+            pl->tile_base = (int)(cb & 0xffffffff);
+        }
+        at += wt;
+        cut += ct;
+    }
+    // cu that lets sequences overlap can ask for more slots than there are
+    if (blockIdx.x == 0 && tid == 0 && p.max_slots) *p.count = (cut >> 32) > p.max_slots ? 0 : (int)(cut & 0xffffffff);
+    return __syncthreads_or(bad);
+}
+
+// Tokens without an answer: NaN, and an error unless the sequence was not granted (start < 0).
 template <int D>
-__global__ void __launch_bounds__(128) cache_attention_simple_kernel(const CacheAttParams p) {
-    __shared__ float qs[D], ps[128], red[4], vs[128];
-    __shared__ int ids[128];
-    const int tid = threadIdx.x, tok = blockIdx.x, head = blockIdx.y, kvh = head / (p.heads / p.kv_heads);
-    int b = tok, t = 0;
-    if (p.cu) {
-        int lo = 0, hi = p.batch - 1;
-        while (lo < hi) {
-            const int mid = (lo + hi + 1) >> 1;
-            if (p.cu[mid] <= tok) lo = mid; else hi = mid - 1;
+__device__ __noinline__ void catt_mark(const CacheAttParams& p) {
+    for (int b = blockIdx.x; b < p.batch; b += gridDim.x) {
+        int n;
+        const int first = catt_tokens(p, b, n), s = p.start[b];
+        if (n == 0 && p.cu && p.cu[b + 1] != first) {
+            if (threadIdx.x == 0) set_error(TBIK_ERR_POSITION);
+            continue;
         }
-        b = lo;
-        t = tok - p.cu[b];
-        if (t < 0 || tok >= p.cu[b + 1]) return;  // before the first or behind the last sequence
+        const int use = catt_usable(p, s, p.rows ? p.rows[b] : b, n);
+        if (use >= n) continue;
+        if (s >= 0 && threadIdx.x == 0) set_error(TBIK_ERR_PAGE);
+        uint4* o = reinterpret_cast<uint4*>(p.out + (size_t)(first + use) * p.heads * D);
+        const size_t m = (size_t)(n - use) * p.heads * (D / 8);
+        for (size_t k = threadIdx.x; k < m; k += blockDim.x) o[k] = make_uint4(0x7fc07fc0u, 0x7fc07fc0u, 0x7fc07fc0u, 0x7fc07fc0u);
     }
-    uint16_t* out = p.out + ((size_t)tok * p.heads + head) * D;
-    const int s = p.start[b], row = p.rows ? p.rows[b] : b;
-    const long long n = (long long)s + t + 1;
-    bool bad = row < 0 || row >= p.slots || n > p.max_keys || n > (long long)p.max_pages * p.page || t >= p.max_q;
-    if (s < 0 || bad) {
-        if (tid < D) out[tid] = 0x7fc0;
-        if (bad && tid == 0) set_error(TBIK_ERR_PAGE);
-        return;
+}
+
+// ------------------------------------------------------------------ the kernel
+
+// Factors of two summaries' parts: 1 for the side that holds the maximum.
+__device__ __forceinline__ void catt_factors(float am, float bm, float& M, float& ea, float& eb) {
+    M = fmaxf(am, bm);
+    ea = am == M ? 1.0f : ex2_hw(am - M);
+    eb = bm == M ? 1.0f : ex2_hw(bm - M);
+}
+
+template <int D, int RW, int NWG>
+__global__ void __launch_bounds__(CattCfg<D, RW, NWG>::THREADS, CattCfg<D, RW, NWG>::CTAS) cache_attention_kernel(const __grid_constant__ CacheAttParams p) {
+    using C = CattCfg<D, RW, NWG>;
+    constexpr int R = C::R, ST = C::STAGES;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    __shared__ CattPlan plan;
+    __shared__ long long scan_buf[32];
+    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
+    uint64_t *kf = bars, *ke = bars + ST, *vf = bars + 2 * ST, *ve = bars + 3 * ST;  // [ST] landed, MMAs retired
+    uint64_t* wb = bars + 4 * ST;  // per group: s_full[2] s_empty[2] o_full[2] o_empty[2] p_full q_full
+    uint64_t* done = wb + 10 * NWG;
+    uint64_t* clean = done + 1;  // values behind the last key zeroed by every group
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(clean + 1);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+    static_assert((4 * ST + 10 * NWG + 3) * 8 <= 512, "barriers");
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint64_t lim = p.wait_cycles;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < 4 * ST; ++i) mbar_init(&bars[i], 1);
+        for (int w = 0; w < NWG; ++w)
+            for (int i = 0; i < 10; ++i) {
+                const bool by_warps = i == 2 || i == 3 || i >= 6;
+                mbar_init(&wb[10 * w + i], by_warps ? 4 : 1);
+            }
+        mbar_init(done, 1);
+        mbar_init(clean, 4 * NWG);
+        *abort_flag = 0;
+        fence_barrier_init();
     }
-    if (tid < D) qs[tid] = bf2f(p.q[((size_t)tok * p.heads + head) * D + tid]);
-    const int L = (int)((n + CATT_LEAF - 1) / CATT_LEAF);
-    float sm[CATT_MAX_LEVELS], ss[CATT_MAX_LEVELS], so[CATT_MAX_LEVELS];
-    int depth = 0;
-    for (int leaf = 0; leaf < L; ++leaf) {
-        const int j = leaf * CATT_LEAF + tid;
-        __syncthreads();
-        float sc = -INFINITY;
-        int id = -1;
-        if (j < n) {
-            id = p.table[(size_t)row * p.max_pages + j / p.page];
-            if (id < 0 || id >= p.num_pages) {
-                bad = true;
-                id = -1;
+    if (warp == 1) {
+        tmem_alloc(tmem_slot, C::COLS);
+        tmem_relinquish();
+    }
+    // the columns of P that no row has stay zero
+    if (RW < 16)
+        for (int i = threadIdx.x; i < NWG * C::PB / 16; i += C::THREADS) reinterpret_cast<uint4*>(smem + C::OFF_P)[i] = make_uint4(0, 0, 0, 0);
+    const bool marks = catt_plan<R>(p, &plan, scan_buf);
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    CattUnits<R> u;
+    const bool any = u.first(p, plan);
+
+    if (warp == 0) {
+        // ---------------------------------------------------- page copies
+        const int npl = CATT_LEAF / p.page;
+        const uint32_t pbytes = (uint32_t)p.page * D;
+        const size_t vplane = (size_t)p.num_pages * p.kv_heads * pbytes;
+        uint32_t g = 0, gv = 0;  // leaves whose keys, values were requested
+        bool ok = true;
+        for (bool more = any; more && ok; more = u.next(p)) {
+            const int32_t* row = p.table + (size_t)u.it.slot * p.max_pages;
+            const int last_row = min(u.it.rows, (u.tau + 1) * R) - 1;
+            const int imax = u.it.i0 + last_row / p.group;  // the last key that the tile sees
+            const int pages = imax / p.page + 1;
+            int pg = u.lo * npl + lane;
+            int id = lane < npl && pg < pages ? row[pg] : 0;
+            for (int l = 0; l < u.size; ++l) {
+                const int here = min(npl, pages - (u.lo + l) * npl);
+                const int pn = pg + npl;
+                const int idn = l + 1 < u.size && lane < npl && pn < pages ? row[pn] : 0;
+                if (id < 0 || id >= p.num_pages) id = 0;  // its keys are marked where the scores are taken
+                const uint8_t* src = p.pages + ((size_t)id * p.kv_heads + u.h) * pbytes;
+                const int st = g % ST;
+                const uint32_t ph = (g / ST) & 1;
+                ok = g < ST || mbar_wait(&ke[st], ph ^ 1, abort_flag, lim);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+                if (lane == 0) mbar_arrive_expect_tx(&kf[st], here * pbytes);
+                __syncwarp();
+                if (lane < here) bulk_load(smem_u32(smem + C::OFF_K + st * C::TILE) + lane * pbytes, src, pbytes, smem_u32(&kf[st]));
+                ok = g++ < ST || mbar_wait(&ve[st], ph ^ 1, abort_flag, lim);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+                if (lane == 0) mbar_arrive_expect_tx(&vf[st], here * pbytes);
+                __syncwarp();
+                if (lane < here) bulk_load(smem_u32(smem + C::OFF_V + st * C::TILE) + lane * pbytes, src + vplane, pbytes, smem_u32(&vf[st]));
+                ++gv;
+                pg = pn;
+                id = idn;
             }
         }
-        if (id >= 0) {
-            const size_t ph = (size_t)id * p.kv_heads + kvh;
-            const int o = j % p.page;
-            const uint8_t* k = p.pages + ph * ((size_t)p.page * D) + (o >> 3) * (D * 8) + (o & 7) * 16;
-            float a = 0.0f;
-            for (int g = 0; g < D / 16; ++g)
-                for (int e = 0; e < 16; ++e) a = __fmaf_rn(e4m3_f32(k[g * 128 + e]), qs[g * 16 + e], a);
-            sc = a * p.scales[ph] * p.scale;
-            vs[tid] = p.scales[(size_t)p.num_pages * p.kv_heads + ph];
+        if (lane == 0) {
+            // what is in flight has to land before the CTA can exit
+            for (uint32_t x = g > (uint32_t)ST ? g - ST : 0; x < g; ++x) mbar_drain(&kf[x % ST], (x / ST) & 1, lim);
+            for (uint32_t x = gv > (uint32_t)ST ? gv - ST : 0; x < gv; ++x) mbar_drain(&vf[x % ST], (x / ST) & 1, lim);
         }
-        ids[tid] = id;
-        float m = sc;
-        for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-        if ((tid & 31) == 0) red[tid >> 5] = m;
-        __syncthreads();
-        m = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
-        ps[tid] = id >= 0 ? ex2_hw(sc - m) : 0.0f;
-        __syncthreads();
-        float sum = 0.0f, o = 0.0f;
-        const int cnt = n - (long long)leaf * CATT_LEAF < CATT_LEAF ? (int)(n - (long long)leaf * CATT_LEAF) : CATT_LEAF;
-        for (int c = 0; c < cnt; ++c) {
-            sum += ps[c];
-            if (tid < D && ids[c] >= 0) {
-                const int pos = (leaf * CATT_LEAF + c) % p.page;
-                const uint8_t* v = p.pages + (((size_t)p.num_pages + ids[c]) * p.kv_heads + kvh) * ((size_t)p.page * D);
-                o = __fmaf_rn(ps[c] * vs[c], e4m3_f32(v[(pos >> 3) * (D * 8) + (tid >> 4) * 128 + (pos & 7) * 16 + (tid & 15)]), o);
+        __syncwarp();
+    } else if (warp == 1) {
+        // ---------------------------------------------------- MMA issue
+        if (lane == 0) {
+            constexpr uint32_t id_s = idesc_e4m3_f32(128, C::NQ, 0), id_o = idesc_e4m3_f32(128, C::NP, 1);
+            uint32_t g = 0, nu = 0;
+            // O^T of leaf x; D = 64 leaves lanes 64..127 with what lies behind (not read)
+            auto values = [&](uint32_t x) -> bool {
+                const int st = x % ST;
+                if (!mbar_wait(&vf[st], (x / ST) & 1, abort_flag, lim)) return false;
+                for (int w = 0; w < NWG; ++w) {
+                    uint64_t* b = wb + 10 * w;
+                    const uint32_t ob = x % C::OBUF, use = x / C::OBUF;
+                    if (!mbar_wait(&b[8], x & 1, abort_flag, lim)) return false;
+                    if (use > 0 && !mbar_wait(&b[6 + ob], (use - 1) & 1, abort_flag, lim)) return false;
+                    tc_fence_after();
+                    const uint32_t pa = smem_u32(smem + C::OFF_P + w * C::PB);
+#pragma unroll
+                    for (int part = 0; part < 2; ++part)
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            tc_mma_f8(tmem + w * C::WG_COLS + C::O_COL + ob * C::NP,
+                                      smem_desc_flat(smem_u32(smem + C::OFF_V + st * C::TILE) + k * 32 * D, D * 8, 128),
+                                      smem_desc_flat(pa + part * 128 * C::NP + k * 32 * C::NP, 8 * C::NP, 128), id_o, (part | k) ? 1u : 0u);
+                    tc_commit(&b[4 + ob]);
+                }
+                tc_commit(&ve[st]);
+                return true;
+            };
+            for (bool more = any; more; more = u.next(p), ++nu) {
+                for (int l = 0; l < u.size; ++l, ++g) {
+                    const int st = g % ST;
+                    if (!mbar_wait(&kf[st], (g / ST) & 1, abort_flag, lim)) goto mma_out;
+                    for (int w = 0; w < NWG; ++w) {
+                        uint64_t* b = wb + 10 * w;
+                        const uint32_t sb = g % C::SBUF, use = g / C::SBUF;
+                        if (l == 0 && !mbar_wait(&b[9], nu & 1, abort_flag, lim)) goto mma_out;
+                        if (use > 0 && !mbar_wait(&b[2 + sb], (use - 1) & 1, abort_flag, lim)) goto mma_out;
+                        tc_fence_after();
+                        const uint32_t qa = smem_u32(smem + C::OFF_Q + w * C::QB), ka = smem_u32(smem + C::OFF_K + st * C::TILE);
+#pragma unroll
+                        for (int k = 0; k < D / 32; ++k)
+                            tc_mma_f8(tmem + w * C::WG_COLS + C::S_COL + sb * C::NQ, smem_desc_flat(ka + k * 256, 128, D * 8),
+                                      smem_desc_flat(qa + k * 256, 128, D * 8), id_s, k ? 1u : 0u);
+                        tc_commit(&b[0 + sb]);
+                    }
+                    tc_commit(&ke[st]);
+                    if (g > 0 && !values(g - 1)) goto mma_out;
+                }
+            }
+            if (g > 0) values(g - 1);
+        mma_out:
+            tc_commit(done);  // every MMA retires before TMEM is released
+            mbar_drain(done, 0, lim);
+        }
+        __syncwarp();
+    } else {
+        // ---------------------------------------------------- scores, weights, summaries
+        const int wg = (warp - 2) >> 2, qd = warp & 3, tid = qd * 32 + lane;  // tid: TMEM lane = key = dim
+        uint64_t* b = wb + 10 * wg;
+        float* x = reinterpret_cast<float*>(smem + C::OFF_X) + wg * C::X_FLOATS;
+        float* xw = x + C::X_WARP + qd * C::X_PER_WARP;   // this warp's own
+        float2* fac = reinterpret_cast<float2*>(xw);      // [RW]
+        float* ofac = xw + 2 * RW;                        // [RW]
+        float2* pend = reinterpret_cast<float2*>(xw + 3 * RW);  // [6][RW] (m, s)
+        const uint32_t tm = tmem + wg * C::WG_COLS + ((uint32_t)(qd * 32) << 16);
+        uint8_t* qs = smem + C::OFF_Q + wg * C::QB;
+        uint8_t* ps = smem + C::OFF_P + wg * C::PB;
+        float* overflow = reinterpret_cast<float*>(smem + C::OFF_ST) + (size_t)wg * RW * 128 + tid;  // [RW][128]
+        const bool has_dim = tid < D;
+        const int bar = 1 + wg;
+        bool ab = false;
+
+        // Queries of a unit's rows as two e4m3 terms each, and their constants c.
+        auto load_q = [&](const CattUnits<R>& un, uint32_t nu) {
+            constexpr int TPR = D / 8, RPP = 128 / TPR;  // threads per row, rows per pass
+            float* cst = x + C::X_CST + (nu & 1) * RW;
+            const int part = tid % TPR;
+#pragma unroll
+            for (int r0 = 0; r0 < RW; r0 += RPP) {
+                const int r = r0 + tid / TPR;
+                const int fr = un.tau * R + wg * RW + r;
+                const bool live = r < RW && fr < un.it.rows;
+                uint4 w = make_uint4(0, 0, 0, 0);
+                if (live) {
+                    const int t = fr / p.group, hd = un.h * p.group + fr - t * p.group;
+                    w = *reinterpret_cast<const uint4*>(p.q + ((size_t)(un.it.tok0 + t) * p.heads + hd) * D + part * 8);
+                }
+                const uint32_t a[4] = {w.x, w.y, w.z, w.w};
+                uint32_t top = 0;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) top = max(top, max(a[k] & 0x7fffu, (a[k] >> 16) & 0x7fffu));
+#pragma unroll
+                for (int o = TPR / 2; o; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+                // exponents below -119 would take the scale out of range; such a row's scores are zero anyway
+                const int e = max((int)(top >> 7) - 127, -119);
+                const float sc = cache_pow2(7 - e);
+                float f[8];
+                unpack8(w, f);
+                uint32_t hi[4], lo[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const float y0 = __fmul_rn(f[2 * k], sc), y1 = __fmul_rn(f[2 * k + 1], sc);
+                    hi[k] = pack_e4m3(y0, y1);
+                    const float2 z = unpack_e4m3(hi[k]);
+                    lo[k] = pack_e4m3(__fmul_rn(__fsub_rn(y0, z.x), 32.0f), __fmul_rn(__fsub_rn(y1, z.y), 32.0f));
+                    if (top >= 0x7f80u) hi[k] = 0x7f7fu;  // not finite: the row's result is NaN
+                }
+                if (r < RW) {
+                    const int at = (r & 7) * 16 + (part >> 1) * 128 + (part & 1) * 8;
+                    *reinterpret_cast<uint2*>(qs + (r >> 3) * (D * 8) + at) = make_uint2(hi[0] | hi[1] << 16, hi[2] | hi[3] << 16);
+                    *reinterpret_cast<uint2*>(qs + ((RW + r) >> 3) * (D * 8) + at) = make_uint2(lo[0] | lo[1] << 16, lo[2] | lo[3] << 16);
+                    if (part == 0) cst[r] = top >= 0x7f80u ? 1.0f : __fmul_rn(cache_pow2(e - 7), p.scale);
+                }
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&b[9]);
+        };
+        // This thread's key in leaf l of a unit: its page (-1: not seen by the tile, -2: no such page).
+        auto key_page = [&](const CattUnits<R>& un, int l) -> int {
+            const int last_row = min(un.it.rows, (un.tau + 1) * R) - 1;
+            const int imax = un.it.i0 + last_row / p.group;
+            const int pos = (un.lo + l) * CATT_LEAF + tid;
+            if (pos > imax) return -1;
+            const int id = p.table[(size_t)un.it.slot * p.max_pages + pos / p.page];
+            return id < 0 || id >= p.num_pages ? -2 : id;
+        };
+        auto key_scales = [&](const CattUnits<R>& un, int id, float& k, float& v) {
+            k = v = 0.0f;
+            if (id >= 0) {
+                const size_t ph = (size_t)id * p.kv_heads + un.h;
+                k = p.scales[ph];
+                v = p.scales[(size_t)p.num_pages * p.kv_heads + ph];
+            }
+        };
+
+        uint32_t g = 0, nu = 0, cleaned = 0;
+        CattUnits<R> prev = u;          // the unit of the previous leaf
+        int prev_l = 0;
+        float prev_m = 0.0f, prev_o = 0.0f;  // lane = row: its maximum and the scale of its O
+        int depth = 0;
+        float cks = 0.0f, cvs = 0.0f;
+        int cid = -1;
+        if (any) {
+            cid = key_page(u, 0);
+            load_q(u, 0);
+            key_scales(u, cid, cks, cvs);
+        }
+
+        // The summary of leaf g1 of unit `prev` enters the tree.
+        auto tree_step = [&](uint32_t g1) {
+            const uint32_t ob = g1 % C::OBUF;
+            float* sums = x + C::X_SUM + (g1 & 1) * 4 * RW;
+            const int row = lane % RW;
+            float m = prev_m;
+            float s = __fadd_rn(__fadd_rn(sums[row], sums[RW + row]), __fadd_rn(sums[2 * RW + row], sums[3 * RW + row]));
+            if (lane < RW) ofac[lane] = prev_o;
+            __syncwarp();
+            float o[RW];
+            if (has_dim) {
+                uint32_t raw[RW];
+                catt_ld<RW>(tm + C::O_COL + ob * C::NP, raw);
+#pragma unroll
+                for (int r = 0; r < RW; r += 4) {
+                    const float4 f = *reinterpret_cast<const float4*>(ofac + r);
+                    upk2(mul2(pk2(__uint_as_float(raw[r]), __uint_as_float(raw[r + 1])), pk2(f.x, f.y)), o[r], o[r + 1]);
+                    upk2(mul2(pk2(__uint_as_float(raw[r + 2]), __uint_as_float(raw[r + 3])), pk2(f.z, f.w)), o[r + 2], o[r + 3]);
+                }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&b[6 + ob]);
+            const bool last = prev_l + 1 == prev.size;
+            if (prev_l == 0) depth = CATT_PENDING - (32 - __clz(max(prev.size - 1, 0)));  // small trees stay in TMEM
+            for (int c = catt_pops(prev.size, prev_l); c > 0; --c) {
+                --depth;
+                const float2 a = pend[depth * RW + row];
+                float M, ea, eb;
+                catt_factors(a.x, m, M, ea, eb);
+                s = __fmaf_rn(s, eb, __fmul_rn(a.y, ea));
+                m = M;
+                __syncwarp();
+                if (lane < RW) fac[lane] = make_float2(ea, eb);
+                __syncwarp();
+                if (has_dim) {
+                    uint32_t raw[RW];
+                    if (depth < CATT_PENDING - C::TPEND) {
+#pragma unroll
+                        for (int r = 0; r < RW; ++r) raw[r] = __float_as_uint(overflow[r * 128]);
+                    } else {
+                        catt_ld<RW>(tm + C::ST_COL + (depth - (CATT_PENDING - C::TPEND)) * RW, raw);
+                    }
+#pragma unroll
+                    for (int r = 0; r < RW; r += 2) {
+                        const float4 f = *reinterpret_cast<const float4*>(fac + r);
+                        upk2(fma2(pk2(o[r], o[r + 1]), pk2(f.y, f.w),
+                                  mul2(pk2(__uint_as_float(raw[r]), __uint_as_float(raw[r + 1])), pk2(f.x, f.z))),
+                             o[r], o[r + 1]);
+                    }
+                }
+            }
+            __syncwarp();
+            if (!last) {
+                if (lane < RW) pend[depth * RW + lane] = make_float2(m, s);
+                if (has_dim) {
+                    if (depth < CATT_PENDING - C::TPEND) {
+#pragma unroll
+                        for (int r = 0; r < RW; ++r) overflow[r * 128] = o[r];
+                    } else {
+                        catt_st<RW>(tm + C::ST_COL + (depth - (CATT_PENDING - C::TPEND)) * RW, o);
+                    }
+                }
+                ++depth;
+                __syncwarp();
+                return;
+            }
+            const int fr0 = prev.tau * R + wg * RW, live = min(RW, prev.it.rows - fr0);
+            if (prev.d == 0) {
+                if (lane < RW) ofac[lane] = __frcp_rn(s);
+                __syncwarp();
+                if (has_dim) {
+                    int t = fr0 / p.group, hd = fr0 - t * p.group;
+                    uint16_t* op = p.out + ((size_t)(prev.it.tok0 + t) * p.heads + prev.h * p.group) * D + tid;
+#pragma unroll
+                    for (int r = 0; r < RW; ++r) {
+                        if (r < live) op[hd * D] = f2bf(__fmul_rn(o[r], ofac[r]));
+                        if (++hd == p.group) {
+                            hd = 0;
+                            op += (size_t)p.heads * D;
+                        }
+                    }
+                }
+            } else {
+                const int slot = prev.slot();
+                if ((unsigned)slot >= (unsigned)p.max_slots) {
+                    set_error(TBIK_ERR_WORKSPACE);
+                } else {
+                    if (qd == 0 && lane < RW) p.ms[(size_t)slot * R + wg * RW + lane] = make_float2(m, s);
+                    if (has_dim) {
+                        float* op = p.o + ((size_t)slot * R + wg * RW) * D + tid;
+#pragma unroll
+                        for (int r = 0; r < RW; ++r)
+                            if (r < live) op[r * D] = o[r];
+                    }
+                    if (prev.v == 0 && wg == 0 && tid == 0) {
+                        int4* t = p.tiles + 2 * (size_t)(prev.tile_base + prev.h * prev.tiles + prev.tau);
+                        t[0] = make_int4(slot, prev.d, prev.it.L, min(R, prev.it.rows - prev.tau * R));
+                        t[1] = make_int4(prev.it.tok0, prev.tau * R, prev.h, 0);
+                    }
+                }
+            }
+            __syncwarp();
+        };
+
+        for (bool more = any; more; ++nu) {
+            CattUnits<R> nxt = u;
+            const bool has_next = nxt.next(p);
+            for (int l = 0; l < u.size; ++l, ++g) {
+                const bool last = l + 1 == u.size;
+                const uint32_t sb = g % C::SBUF;
+                if (!ab) ab = !mbar_wait(&b[0 + sb], (g / C::SBUF) & 1, abort_flag, lim);
+                ab = __any_sync(0xffffffffu, ab);
+                float a[RW];
+                float* mx = x + C::X_MAX + (g & 1) * 4 * RW;
+                float* pv = x + C::X_PV + (g & 1) * 8;
+                const bool diag = u.lo + l == u.it.L - 1;
+                const int fr0 = u.tau * R + wg * RW;
+                // the key of the next leaf
+                int nid = -1;
+                if (!last) nid = key_page(u, l + 1);
+                else if (has_next) nid = key_page(nxt, 0);
+                if (!ab) {
+                    tc_fence_after();
+                    uint32_t raw[C::NQ];
+                    catt_ld<C::NQ>(tm + C::S_COL + sb * C::NQ, raw);
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&b[2 + sb]);
+                    const f2x k2 = pk2(cks, cks), i32 = pk2(0.03125f, 0.03125f);
+#pragma unroll
+                    for (int r = 0; r < RW; r += 2)
+                        upk2(mul2(fma2(pk2(__uint_as_float(raw[RW + r]), __uint_as_float(raw[RW + r + 1])), i32,
+                                       pk2(__uint_as_float(raw[r]), __uint_as_float(raw[r + 1]))), k2), a[r], a[r + 1]);
+                    if (cid == -2) {
+#pragma unroll
+                        for (int r = 0; r < RW; ++r) a[r] = __uint_as_float(0x7fc00000u);
+                        set_error(TBIK_ERR_PAGE);
+                    }
+                    if (diag) {
+                        int t = fr0 / p.group, hd = fr0 - t * p.group, i = (u.it.i0 + t) & 127;
+#pragma unroll
+                        for (int r = 0; r < RW; ++r) {
+                            if (tid > i) a[r] = -INFINITY;
+                            if (++hd == p.group) {
+                                hd = 0;
+                                ++i;
+                            }
+                        }
+                    }
+#pragma unroll
+                    for (int r = 0; r < RW; r += 4) {
+                        float4 m4;
+                        m4.x = warp_max_f32(a[r]);
+                        m4.y = warp_max_f32(a[r + 1]);
+                        m4.z = warp_max_f32(a[r + 2]);
+                        m4.w = warp_max_f32(a[r + 3]);
+                        if (lane == 0) *reinterpret_cast<float4*>(mx + qd * RW + r) = m4;
+                    }
+                    if (tid % p.page == 0) pv[tid / p.page] = cvs;
+                }
+                if (named_barrier_or(bar, 128, ab)) goto epi_out;
+                // scales of the next leaf's key
+                float nks, nvs;
+                key_scales(last ? nxt : u, nid, nks, nvs);
+                if (last && has_next) load_q(nxt, nu + 1);
+                const float* cst = x + C::X_CST + (nu & 1) * RW;
+                const int npl = CATT_LEAF / p.page;
+                // the largest value scale among a row's visible pages of the leaf
+                auto vmax = [&](int i) {
+                    float v = pv[0];
+                    for (int k = 1; k < npl; ++k)
+                        if (k * p.page <= i) v = fmaxf(v, pv[k]);
+                    return v;
+                };
+                const float vm = diag ? 1.0f : vmax(127);
+                float f = 0.0f;
+                if (!diag) f = __fmul_rn(cvs, __fmul_rn(256.0f, __frcp_rn(vm)));
+                float w[RW];  // 256 f p
+                {
+                    int t = fr0 / p.group, hd = fr0 - t * p.group, i = (u.it.i0 + t) & 127;
+#pragma unroll
+                    for (int r = 0; r < RW; r += 4) {
+                        const float4 m0 = *reinterpret_cast<const float4*>(mx + r), m1 = *reinterpret_cast<const float4*>(mx + RW + r);
+                        const float4 m2 = *reinterpret_cast<const float4*>(mx + 2 * RW + r), m3 = *reinterpret_cast<const float4*>(mx + 3 * RW + r);
+                        const float4 c4 = *reinterpret_cast<const float4*>(cst + r);
+                        const float mm[4] = {fmaxf(fmax3(m0.x, m1.x, m2.x), m3.x), fmaxf(fmax3(m0.y, m1.y, m2.y), m3.y),
+                                             fmaxf(fmax3(m0.z, m1.z, m2.z), m3.z), fmaxf(fmax3(m0.w, m1.w, m2.w), m3.w)};
+                        const float cc[4] = {c4.x, c4.y, c4.z, c4.w};
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            a[r + k] = ex2_hw(__fmul_rn(__fsub_rn(a[r + k], mm[k]), cc[k]));
+                            float fk = f;
+                            if (diag) {
+                                fk = tid <= i ? __fmul_rn(cvs, __fmul_rn(256.0f, __frcp_rn(vmax(i)))) : 0.0f;
+                                if (++hd == p.group) {
+                                    hd = 0;
+                                    ++i;
+                                }
+                            }
+                            w[r + k] = __fmul_rn(a[r + k], fk);
+                        }
+                    }
+                }
+                // this warp's view of row `lane`: its maximum and O's scale
+                float nm, no;
+                {
+                    const int row = lane % RW;
+                    nm = __fmul_rn(fmaxf(fmax3(mx[row], mx[RW + row], mx[2 * RW + row]), mx[3 * RW + row]), cst[row]);
+                    const int i = (u.it.i0 + (fr0 + row) / p.group) & 127;
+                    no = __fmul_rn(diag ? vmax(i) : vm, 0.00390625f);
+                }
+                // P of the previous leaf is read until its O is there
+                if (g > 0 && !ab) {
+                    const uint32_t g1 = g - 1;
+                    ab = !mbar_wait(&b[4 + g1 % C::OBUF], (g1 / C::OBUF) & 1, abort_flag, lim);
+                    ab = __any_sync(0xffffffffu, ab);
+                }
+                if (!ab) {
+                    uint32_t hi[RW / 4], lo[RW / 4];
+#pragma unroll
+                    for (int r = 0; r < RW; r += 4) {
+                        const uint32_t h0 = pack_e4m3(w[r], w[r + 1]), h1 = pack_e4m3(w[r + 2], w[r + 3]);
+                        const float2 z0 = unpack_e4m3(h0), z1 = unpack_e4m3(h1);
+                        hi[r / 4] = h0 | h1 << 16;
+                        lo[r / 4] = pack_e4m3(__fsub_rn(w[r], z0.x), __fsub_rn(w[r + 1], z0.y)) |
+                                    pack_e4m3(__fsub_rn(w[r + 2], z1.x), __fsub_rn(w[r + 3], z1.y)) << 16;
+                    }
+                    uint8_t* dst = ps + (tid >> 3) * (8 * C::NP) + (tid & 7) * 16;
+                    if constexpr (RW == 8) {
+                        *reinterpret_cast<uint2*>(dst) = make_uint2(hi[0], hi[1]);
+                        *reinterpret_cast<uint2*>(dst + 128 * C::NP) = make_uint2(lo[0], lo[1]);
+                    } else {
+#pragma unroll
+                        for (int k = 0; k < RW / 16; ++k) {
+                            *reinterpret_cast<uint4*>(dst + k * 128) = make_uint4(hi[4 * k], hi[4 * k + 1], hi[4 * k + 2], hi[4 * k + 3]);
+                            *reinterpret_cast<uint4*>(dst + 128 * C::NP + k * 128) = make_uint4(lo[4 * k], lo[4 * k + 1], lo[4 * k + 2], lo[4 * k + 3]);
+                        }
+                    }
+                }
+                if (diag) {
+                    // values that no row sees must be finite (0 x NaN): zero behind the tile's last key, and NaN bytes
+                    // between its first row's key and that
+                    const int st = g % ST;
+                    if (!ab) ab = !mbar_wait(&vf[st], (g / ST) & 1, abort_flag, lim);
+                    ab = __any_sync(0xffffffffu, ab);
+                    if (!ab) {
+                        const int r0 = u.tau * R, r1 = min(u.it.rows, r0 + R) - 1;
+                        const int imin = (u.it.i0 + r0 / p.group) & 127, imax = (u.it.i0 + r1 / p.group) & 127;
+                        if (tid > imin) {
+                            uint8_t* vt = smem + C::OFF_V + st * C::TILE + (tid >> 3) * (D * 8) + (tid & 7) * 16;
+                            for (int k = wg; k < D / 16; k += NWG) {
+                                uint4* at = reinterpret_cast<uint4*>(vt + k * 128);
+                                if (tid > imax || cid < 0) {
+                                    *at = make_uint4(0, 0, 0, 0);
+                                } else {
+                                    const uint4 y = *at;
+                                    const uint32_t z[4] = {y.x, y.y, y.z, y.w};
+                                    uint32_t o[4];
+#pragma unroll
+                                    for (int e = 0; e < 4; ++e) o[e] = z[e] & ~__vcmpeq4(z[e] & 0x7f7f7f7fu, 0x7f7f7f7fu);
+                                    *at = make_uint4(o[0], o[1], o[2], o[3]);
+                                }
+                            }
+                        }
+                    }
+                    if (NWG > 1 && !ab) {  // each group has cleaned its share of the dims
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(clean);
+                        ab = !mbar_wait(clean, cleaned++ & 1, abort_flag, lim);
+                        ab = __any_sync(0xffffffffu, ab);
+                    }
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0 && !ab && !(p.debug & TBIK_DEBUG_WITHHOLD_ACC_ARRIVE)) mbar_arrive(&b[8]);
+                // sums over the warp's 32 keys: halves 16, 8, 4, 2, 1 apart; the rows are dealt out on the way
+                {
+                    int n = RW;
+#pragma unroll
+                    for (int o = 16; o; o >>= 1) {
+                        if (n > 1) {
+                            n >>= 1;
+#pragma unroll
+                            for (int k = 0; k < RW / 2; ++k)
+                                if (k < n) {
+                                    const float keep = (lane & o) ? a[k + n] : a[k], send = (lane & o) ? a[k] : a[k + n];
+                                    a[k] = __fadd_rn(keep, __shfl_xor_sync(0xffffffffu, send, o));
+                                }
+                        } else {
+                            a[0] = __fadd_rn(a[0], __shfl_xor_sync(0xffffffffu, a[0], o));
+                        }
+                    }
+                    if (lane % (32 / RW) == 0) x[C::X_SUM + (g & 1) * 4 * RW + qd * RW + lane / (32 / RW)] = a[0];
+                }
+                if (g > 0 && !ab) {
+                    tc_fence_after();
+                    tree_step(g - 1);
+                }
+                prev = u;
+                prev_l = l;
+                prev_m = nm;
+                prev_o = no;
+                cid = nid;
+                cks = nks;
+                cvs = nvs;
+            }
+            u = nxt;
+            more = has_next;
+        }
+        if (named_barrier_or(bar, 128, ab)) goto epi_out;
+        if (g > 0) {
+            const uint32_t g1 = g - 1;
+            ab = !mbar_wait(&b[4 + g1 % C::OBUF], (g1 / C::OBUF) & 1, abort_flag, lim);
+            if (!__any_sync(0xffffffffu, ab)) {
+                tc_fence_after();
+                tree_step(g1);
             }
         }
-        // close the nodes whose last leaf this is, deepest first
-        const LeafOps ops = leaf_ops(L, leaf);
-        for (int c = leaf_pops(ops); c > 0; --c) {
-            --depth;
-            const float M = fmaxf(sm[depth], m);
-            const float ea = sm[depth] == M ? 1.0f : ex2_hw(sm[depth] - M), eb = m == M ? 1.0f : ex2_hw(m - M);
-            sum = __fmaf_rn(sum, eb, __fmul_rn(ss[depth], ea));
-            o = __fmaf_rn(o, eb, __fmul_rn(so[depth], ea));
-            m = M;
-        }
-        sm[depth] = m;
-        ss[depth] = sum;
-        so[depth] = o;
-        ++depth;
+    epi_out:;
     }
-    bad = __syncthreads_or(bad);
-    if (bad && tid == 0) set_error(TBIK_ERR_PAGE);
-    if (tid < D) out[tid] = bad ? (uint16_t)0x7fc0 : f2bf(__fmul_rn(so[0], __fdiv_rn(1.0f, ss[0])));
+    if (marks) catt_mark<D>(p);
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem, C::COLS);
+    }
+}
+
+// ------------------------------------------------------------------ the tree above the units
+//
+// One block per cut tile's row, a thread per dim in each of eight groups; a group evaluates one of the subtrees three
+// levels below the root, one thread's values of eight nodes in flight at a time.  Empty nodes are passed over.
+
+constexpr int CATT_JOIN_GROUPS = 8;
+
+struct CattSum {
+    float m, s, o;
+    bool any;
+};
+__device__ __forceinline__ CattSum catt_join(const CattSum& a, const CattSum& b) {
+    if (!b.any) return a;
+    if (!a.any) return b;
+    CattSum r;
+    float ea, eb;
+    catt_factors(a.m, b.m, r.m, ea, eb);
+    r.s = __fmaf_rn(b.s, eb, __fmul_rn(a.s, ea));
+    r.o = __fmaf_rn(b.o, eb, __fmul_rn(a.o, ea));
+    r.any = true;
+    return r;
+}
+
+template <int D, int R>
+__global__ void __launch_bounds__(D* CATT_JOIN_GROUPS) cache_attention_join_kernel(const __grid_constant__ CacheAttParams p) {
+    __shared__ CattSum part[CATT_JOIN_GROUPS][D];
+    const int dim = threadIdx.x % D, grp = threadIdx.x / D;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int count = *p.count;
+    for (int w = blockIdx.x; w < count * R; w += gridDim.x) {
+        const int4 t0 = p.tiles[2 * (size_t)(w / R)], t1 = p.tiles[2 * (size_t)(w / R) + 1];
+        const int row = w % R, d = t0.y, L = t0.z;
+        if (row >= t0.w || t0.x + (1 << d) > p.max_slots) continue;  // the same for the whole block
+        const int top = min(d, 3);
+        CattSum r;
+        r.any = false;
+        if (grp < (1 << top)) {
+            const int per = 1 << (d - top), v0 = grp * per;  // this group's nodes
+            CattSum st[20];
+            int depth = 0;
+            const int step = min(per, 8);
+            for (int v = 0; v < per; v += step) {
+                CattSum x[8];
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    x[k].any = false;
+                    if (k < step) {
+                        int lo, size;
+                        catt_node(L, d, v0 + v + k, lo, size);
+                        if (size) {
+                            const size_t at = (size_t)(t0.x + v0 + v + k) * R + row;
+                            const float2 ms = p.ms[at];
+                            x[k].m = ms.x;
+                            x[k].s = ms.y;
+                            x[k].o = p.o[at * D + dim];
+                            x[k].any = true;
+                        }
+                    }
+                }
+#pragma unroll
+                for (int h = 1; h < 8; h <<= 1)
+                    if (h < step)
+#pragma unroll
+                        for (int k = 0; k + h < 8; k += 2 * h) x[k] = catt_join(x[k], x[k + h]);
+                r = x[0];
+                for (int c = v / step; c & 1; c >>= 1) r = catt_join(st[--depth], r);
+                st[depth++] = r;
+            }
+        }
+        __syncthreads();
+        part[grp][dim] = r;
+        __syncthreads();
+        if (grp == 0) {
+            CattSum x[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) x[k] = part[k][dim];  // groups behind the last are empty
+#pragma unroll
+            for (int h = 1; h < 8; h <<= 1)
+#pragma unroll
+                for (int k = 0; k + h < 8; k += 2 * h) x[k] = catt_join(x[k], x[k + h]);
+            const int fr = t1.y + row, t = fr / p.group, hd = t1.z * p.group + fr - t * p.group;
+            p.out[((size_t)(t1.x + t) * p.heads + hd) * D + dim] = f2bf(__fmul_rn(x[0].o, __frcp_rn(x[0].s)));
+        }
+    }
 }
 
 }  // namespace tbik

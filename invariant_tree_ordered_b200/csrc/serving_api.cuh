@@ -71,6 +71,85 @@ tbik_status check_attention(int tokens, int batch, int max_q, int max_keys, int 
     return check_meta(batch, 1, 1, 1, page);
 }
 
+// Rows of a tile, grid and workspace of an attention call.
+struct CattSplit {
+    int rows;    // rows per tile: 8, 16, 32 or 64
+    int blocks, grid, slots;
+    size_t off_tiles, off_ms, off_o, bytes;
+};
+
+tbik_status plan_cache_attention(int tokens, int batch, int max_q, int max_keys, int heads, int kv_heads, int head_dim,
+                                 int sms, CattSplit& c) {
+    memset(&c, 0, sizeof(c));
+    if (tokens == 0 || batch == 0) return TBIK_OK;
+    const int group = heads / kv_heads;
+    const long long most = (long long)(max_q < tokens ? max_q : tokens) * group;  // rows of a sequence that share a kv head
+    c.rows = most <= 8 ? 8 : most <= 16 ? 16 : most <= 32 ? 32 : 64;
+    c.blocks = ((max_q < tokens ? max_q : tokens) + 126) / 128 + 1;
+    const long long items = (long long)batch * c.blocks;
+    if (items > (1 << 30)) return TBIK_ERR_SHAPE;
+    const int ctas = c.rows == 8 ? 3 : c.rows == 64 ? 1 : 2;
+    const long long leaves = (max_keys + CATT_LEAF - 1) / CATT_LEAF;
+    const long long tiles = (long long)kv_heads * ((long long)tokens * group / c.rows + (items < tokens ? items : tokens));
+    const long long work = tiles * leaves;
+    const long long full = (long long)sms * ctas;
+    c.grid = (int)(work < full ? work : full);
+    if (leaves > 1) {
+        // a cut tile of L leaves has fewer than 2 L / T nodes, T >= all leaves / (grid * CATT_UNITS) or the cap
+        const long long by_grid = 2ll * c.grid * CATT_UNITS, by_cap = 2 * work / CATT_MAX_NODE;
+        long long slots = by_grid > by_cap ? by_grid : by_cap;
+        if (slots > 2 * work) slots = 2 * work;
+        slots += 2;
+        if (slots * c.rows > (1ll << 30)) return TBIK_ERR_SHAPE;
+        c.slots = (int)slots;
+        c.off_tiles = 256;
+        c.off_ms = c.off_tiles + (size_t)(slots / 2) * 32;
+        c.off_o = (c.off_ms + (size_t)slots * c.rows * 8 + 255) / 256 * 256;
+        c.bytes = c.off_o + (size_t)slots * c.rows * head_dim * 4;
+    }
+    return TBIK_OK;
+}
+
+template <int D, int RW, int NWG>
+tbik_status launch_cache_attention(const CacheAttParams& p, const CattSplit& c, const DeviceInfo* info, int dev, cudaStream_t s) {
+    using C = CattCfg<D, RW, NWG>;
+    static bool ready[kMaxDevices];
+    {
+        std::lock_guard<std::mutex> lk(g_mu);
+        if (!ready[dev]) {
+            if (cudaFuncSetAttribute(cache_attention_kernel<D, RW, NWG>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) != cudaSuccess)
+                return TBIK_ERR_CUDA;
+            ready[dev] = true;
+        }
+    }
+    cache_attention_kernel<D, RW, NWG><<<c.grid, C::THREADS, C::SMEM, s>>>(p);
+    tbik_status st = launch_status();
+    if (st != TBIK_OK || !c.slots) return st;
+    // the second kernel's blocks may be set up while the first one ends; they wait for its results themselves
+    cudaLaunchConfig_t cfg = {};
+    const long long rows = (long long)(c.slots / 2) * c.rows, full = (long long)info->sms * 2;
+    cfg.gridDim = dim3((unsigned)(rows < full ? rows : full));
+    cfg.blockDim = dim3(D * CATT_JOIN_GROUPS);
+    cfg.stream = s;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, cache_attention_join_kernel<D, C::R>, p) != cudaSuccess) return TBIK_ERR_CUDA;
+    return launch_status();
+}
+
+template <int D>
+tbik_status dispatch_cache_attention(const CacheAttParams& p, const CattSplit& c, const DeviceInfo* info, int dev, cudaStream_t s) {
+    switch (c.rows) {
+        case 8: return launch_cache_attention<D, 8, 1>(p, c, info, dev, s);
+        case 16: return launch_cache_attention<D, 16, 1>(p, c, info, dev, s);
+        case 32: return launch_cache_attention<D, 32, 1>(p, c, info, dev, s);
+        default: return launch_cache_attention<D, 32, 2>(p, c, info, dev, s);
+    }
+}
+
 template <typename T>
 tbik_status launch_sample(SampleParams& p, const DeviceInfo* info, int dev, cudaStream_t s) {
     // Blocks per row: as few as hold the row in 48 KB each, more (up to 8) while the device has room for them and a
@@ -254,7 +333,9 @@ size_t tbik_cache_attention_workspace(int tokens, int batch, int max_q, int max_
     DeviceInfo* info;
     if (device_info(dev, info) != TBIK_OK) return (size_t)-1;
     if (check_attention(tokens, batch, max_q, max_keys, heads, kv_heads, head_dim, page) != TBIK_OK) return (size_t)-1;
-    return 0;
+    CattSplit c;
+    if (plan_cache_attention(tokens, batch, max_q, max_keys, heads, kv_heads, head_dim, info->sms, c) != TBIK_OK) return (size_t)-1;
+    return c.bytes;
 }
 
 tbik_status tbik_cache_attention(const uint16_t* q, const uint8_t* pages, const float* scales, const int32_t* table,
@@ -268,20 +349,33 @@ tbik_status tbik_cache_attention(const uint16_t* q, const uint8_t* pages, const 
     if ((st = check_attention(tokens, batch, max_q, max_keys, heads, kv_heads, head_dim, page)) != TBIK_OK) return st;
     if ((st = check_meta(batch, slots, max_pages, num_pages, page)) != TBIK_OK) return st;
     if ((!cu && tokens != batch) || (!rows && batch > slots)) return TBIK_ERR_SHAPE;
+    CattSplit c;
+    if ((st = plan_cache_attention(tokens, batch, max_q, max_keys, heads, kv_heads, head_dim, info->sms, c)) != TBIK_OK) return st;
     if (tokens == 0 || batch == 0) return TBIK_OK;
     if (!q || !pages || !scales || !table || !start || !out) return TBIK_ERR_ARG;
     if (!aligned16(q) || !aligned16(pages) || !aligned16(scales) || !aligned16(out)) return TBIK_ERR_ALIGN;
+    if (c.bytes && (!ws || ws_bytes < c.bytes)) return TBIK_ERR_WORKSPACE;
+    if (c.bytes && !aligned16(ws)) return TBIK_ERR_ALIGN;
     CacheAttParams p;
+    memset(&p, 0, sizeof(p));
     p.q = q, p.pages = pages, p.scales = scales, p.table = table, p.start = start, p.cu = cu, p.rows = rows, p.out = out;
     p.tokens = tokens, p.batch = batch, p.slots = slots, p.max_pages = max_pages, p.num_pages = num_pages;
     p.heads = heads, p.kv_heads = kv_heads, p.page = page, p.max_q = max_q, p.max_keys = max_keys;
+    p.group = heads / kv_heads;
+    p.blocks = c.blocks;
     p.scale = (float)(1.4426950408889634 / std::sqrt((double)head_dim));
+    if (c.slots) {
+        uint8_t* w = reinterpret_cast<uint8_t*>(ws);
+        p.count = reinterpret_cast<int*>(w);
+        p.tiles = reinterpret_cast<int4*>(w + c.off_tiles);
+        p.ms = reinterpret_cast<float2*>(w + c.off_ms);
+        p.o = reinterpret_cast<float*>(w + c.off_o);
+        p.max_slots = c.slots;
+    }
+    p.wait_cycles = wait_cycles(info);
+    p.debug = g_debug_flags;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    if (head_dim == 128)
-        cache_attention_simple_kernel<128><<<dim3(tokens, heads), 128, 0, s>>>(p);
-    else
-        cache_attention_simple_kernel<64><<<dim3(tokens, heads), 128, 0, s>>>(p);
-    return launch_status();
+    return head_dim == 128 ? dispatch_cache_attention<128>(p, c, info, dev, s) : dispatch_cache_attention<64>(p, c, info, dev, s);
 }
 
 tbik_status tbik_sample(const void* logits, const float* u, const float* temperature, const int32_t* top_k,
