@@ -39,6 +39,7 @@ constexpr int CATT_LEAF = 128;
 constexpr int CATT_UNITS = 6;       // units per CTA that the split aims at
 constexpr int CATT_MAX_NODE = 64;   // leaves of a unit: six pending summaries
 constexpr int CATT_PENDING = 6;
+constexpr int CATT_JOIN_DEPTH = 4;  // levels above the units that one thread of the second kernel evaluates alone
 
 struct CacheAttParams {
     const uint16_t* q;
@@ -51,10 +52,12 @@ struct CacheAttParams {
     uint16_t* out;
     int tokens, batch, slots, max_pages, num_pages, heads, kv_heads, page, max_q, max_keys;
     int group;       // heads / kv_heads
+    int page_shift;  // log2(page)
+    uint32_t group_inv;  // ceil(2^31 / group)
     int blocks;      // 128-position blocks that a sequence's new tokens can touch
     float scale;     // log2(e) / sqrt(head_dim)
     // workspace: number of cut tiles, their descriptors, and the nodes' summaries
-    int* count;
+    int* count;      // [2]: cut tiles, whether a tree was cut deeper than CATT_JOIN_DEPTH
     int4* tiles;     // [max_slots / 2][2]
     float2* ms;      // [max_slots][R]
     float* o;        // [max_slots][R][D]
@@ -84,9 +87,9 @@ struct CattCfg {
     static constexpr int OFF_BAR = OFF_ST + (TPEND < CATT_PENDING ? NWG * RW * 128 * 4 : 0);
     static constexpr int OFF_X = OFF_BAR + 512;
     // per group of 4 warps, in floats: maxima [2][4][RW], sums [2][4][RW], constants [2][RW], value scales [2][8],
-    // and per warp: factors [3][RW], pending (m, s) [6][2][RW]
+    // and per warp: factors and rows [4][RW], pending (m, s) [6][2][RW]
     static constexpr int X_MAX = 0, X_SUM = 8 * RW, X_CST = 16 * RW, X_PV = 18 * RW, X_WARP = X_PV + 16;
-    static constexpr int X_PER_WARP = 3 * RW + CATT_PENDING * 2 * RW;
+    static constexpr int X_PER_WARP = 4 * RW + CATT_PENDING * 2 * RW;
     static constexpr int X_FLOATS = X_WARP + 4 * X_PER_WARP;
     static constexpr int SMEM = OFF_X + NWG * X_FLOATS * 4;
 };
@@ -193,31 +196,59 @@ __device__ __forceinline__ void catt_st<32>(uint32_t addr, const float (&v)[32])
         : "memory");
 }
 
-// ------------------------------------------------------------------ the split
-
-// Leaves [lo, lo + size) of node v (of 2^d, left to right) at depth d of the tree over L leaves; size may be 0 where a
-// single leaf cannot be cut any further.
-__host__ __device__ __forceinline__ void catt_node(int L, int d, int v, int& lo, int& size) {
-    lo = 0;
-    size = L;
-    for (int k = d - 1; k >= 0; --k) {
-        const int h = (size + 1) >> 1;
-        if ((v >> k) & 1) {
-            lo += h;
-            size -= h;
-        } else {
-            size = h;
+// The bounded waits of device_common.cuh with their loops kept small: the softmax warps run through their whole code
+// once per leaf, and unrolled waits (of which there are a dozen) would push it out of the instruction cache
+// (measured: 160 KB of code, a leaf took three times as long).
+__device__ __forceinline__ bool catt_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag, uint64_t limit) {
+    if (mbar_try_wait(bar, parity)) return true;
+    const long long t0 = clock64();
+    bool ok;
+#pragma unroll 1
+    while (!(ok = mbar_try_wait(bar, parity))) {
+        if (*abort_flag) break;
+        if ((uint64_t)(clock64() - t0) > limit) {
+            *abort_flag = 1;
+            set_error(TBIK_ERR_TIMEOUT);
+            break;
+        }
+    }
+    return ok;
+}
+__device__ __forceinline__ void catt_drain(uint64_t* bar, uint32_t parity, uint64_t limit) {
+    const long long t0 = clock64();
+#pragma unroll 1
+    while (!mbar_try_wait(bar, parity)) {
+        if ((uint64_t)(clock64() - t0) > limit) {
+            set_error(TBIK_ERR_TIMEOUT);
+            break;
         }
     }
 }
+
+// ------------------------------------------------------------------ the split
+
+// Leaves of node v (of 2^d, left to right) at depth d of the tree over L leaves.  Halving gives the left part the odd
+// leaf, so the L mod 2^d nodes with one leaf more are those whose index, its d bits reversed, is smallest.  0 where a
+// single leaf cannot be cut any further.
+__host__ __device__ __forceinline__ int catt_node_size(int L, int d, int v) {
+#ifdef __CUDA_ARCH__
+    const uint32_t rev = d ? __brev((uint32_t)v) >> (32 - d) : 0u;
+#else
+    uint32_t rev = 0;
+    for (int k = 0; k < d; ++k) rev |= (uint32_t)(v >> k & 1) << (d - 1 - k);
+#endif
+    return (int)(((uint32_t)L + (1u << d) - 1u - rev) >> d);
+}
+// The smallest depth whose nodes have at most T leaves.
 __host__ __device__ __forceinline__ int catt_depth(int L, int T) {
     int d = 0;
-    while (((L + (1 << d) - 1) >> d) > T) ++d;
+    for (int x = (L + T - 1) / T; (1 << d) < x;) ++d;
     return d;
 }
 // Number of nodes that leaf j of a tree over n leaves closes.
 __host__ __device__ __forceinline__ int catt_pops(int n, int j) {
     int pops = 0;
+#pragma unroll 1
     while (n > 1) {
         if (j == n - 1) ++pops;
         else pops = 0;
@@ -231,6 +262,9 @@ __host__ __device__ __forceinline__ int catt_pops(int n, int j) {
     }
     return pops;
 }
+
+// x / group for x < 2^16 (group <= 64: the error x / 2^31 is below 1 / group).
+__device__ __forceinline__ int catt_div(const CacheAttParams& p, int x) { return (int)((uint64_t)(uint32_t)x * p.group_inv >> 31); }
 
 // The new tokens of a sequence within one block of 128 positions.
 struct CattItem {
@@ -259,7 +293,7 @@ __device__ __forceinline__ int catt_usable(const CacheAttParams& p, int s, int s
 __device__ __forceinline__ CattItem catt_item(const CacheAttParams& p, int i, bool& bad) {
     CattItem t;
     int n;
-    t.b = i / p.blocks;
+    t.b = p.blocks == 1 ? i : i / p.blocks;
     const int kb = i - t.b * p.blocks;
     const int first = catt_tokens(p, t.b, n);
     const int s = p.start[t.b];
@@ -295,6 +329,9 @@ struct CattUnits {
         tiles = (it.rows + R - 1) / R;
         d = catt_depth(it.L, T);
     }
+    // Positions of the tile's first and last query.
+    __device__ __forceinline__ int imin(const CacheAttParams& p) const { return it.i0 + catt_div(p, tau * R); }
+    __device__ __forceinline__ int imax(const CacheAttParams& p) const { return it.i0 + catt_div(p, min(it.rows, (tau + 1) * R) - 1); }
     __device__ __forceinline__ int slot() const { return slot_base + ((h * tiles + tau) << d) + v; }
     // The first unit that starts at or behind x0.
     __device__ __forceinline__ bool first(const CacheAttParams& p, const CattPlan& pl) {
@@ -306,15 +343,21 @@ struct CattUnits {
         if (item < 0 || pl.x0 >= pl.x1) return false;
         enter(p);
         const long long ht = (long long)p.kv_heads * tiles, y = pl.x0 - pl.at;
-        int a = 0, b = (1 << d) - 1;
-        while (a < b) {  // the last node whose units start at or before y
-            const int m = (a + b + 1) >> 1;
-            catt_node(it.L, d, m, lo, size);
-            if ((long long)(lo + min(m, lo)) * ht <= y) a = m;
-            else b = m - 1;
+        // down to the last node whose units start at or before y: nodes before v weigh their leaves and one for each
+        // that is not empty, lo + min(v, lo) in all
+        v = lo = 0;
+        size = it.L;
+#pragma unroll 1
+        for (int k = d - 1; k >= 0; --k) {
+            const int h = (size + 1) >> 1, r = lo + h;
+            if ((long long)(r + min(v + (1 << k), r)) * ht <= y) {
+                v += 1 << k;
+                lo = r;
+                size -= h;
+            } else {
+                size = h;
+            }
         }
-        v = a;
-        catt_node(it.L, d, v, lo, size);
         const long long base = (long long)(lo + min(v, lo)) * ht;
         long long k = size ? (y - base + size) / (size + 1) : ht;
         if (k >= ht) {
@@ -335,20 +378,23 @@ struct CattUnits {
         tau = 0;
         if (++h < p.kv_heads) return true;
         h = 0;
+        lo += size;
+#pragma unroll 1
         while (++v < (1 << d)) {
-            catt_node(it.L, d, v, lo, size);
+            size = catt_node_size(it.L, d, v);
             if (size) return true;
         }
         if (d > 0) {
             slot_base += (p.kv_heads * tiles) << d;
             tile_base += p.kv_heads * tiles;
         }
+#pragma unroll 1
         do {
             if (++item >= p.batch * p.blocks) return false;
             enter(p);
         } while (it.rows == 0);
-        v = 0;
-        catt_node(it.L, d, 0, lo, size);
+        v = lo = 0;
+        size = catt_node_size(it.L, d, 0);
         return true;
     }
 };
@@ -361,6 +407,7 @@ __device__ __forceinline__ long long catt_block_sum(long long v, long long* buf)
     if ((threadIdx.x & 31) == 0) buf[threadIdx.x >> 5] = v;
     __syncthreads();
     v = 0;
+#pragma unroll 1
     for (int w = 0; w < (int)blockDim.x / 32; ++w) v += buf[w];
     return v;
 }
@@ -378,6 +425,7 @@ __device__ __forceinline__ long long catt_block_before(long long v, long long* b
     __syncthreads();
     long long b = 0;
     total = 0;
+#pragma unroll 1
     for (int w = 0; w < (int)blockDim.x / 32; ++w) {
         if (w < warp) b += buf[w];
         total += buf[w];
@@ -391,6 +439,7 @@ __device__ __forceinline__ bool catt_plan(const CacheAttParams& p, CattPlan* pl,
     const int items = p.batch * p.blocks, tid = threadIdx.x, nt = blockDim.x;
     bool bad = false;
     long long leaves = 0;
+#pragma unroll 1
     for (int i = tid; i < items; i += nt) {
         const CattItem t = catt_item(p, i, bad);
         if (t.rows) leaves += (long long)t.L * p.kv_heads * ((t.rows + R - 1) / R);
@@ -400,6 +449,7 @@ __device__ __forceinline__ bool catt_plan(const CacheAttParams& p, CattPlan* pl,
     const int T = (int)min((long long)CATT_MAX_NODE, max(1ll, (leaves + aim - 1) / aim));
     // weight of a unit: its leaves and one for its start
     long long total = 0;
+#pragma unroll 1
     for (int i = tid; i < items; i += nt) {
         const CattItem t = catt_item(p, i, bad);
         if (t.rows) total += (long long)(t.L + min(t.L, 1 << catt_depth(t.L, T))) * p.kv_heads * ((t.rows + R - 1) / R);
@@ -414,7 +464,9 @@ __device__ __forceinline__ bool catt_plan(const CacheAttParams& p, CattPlan* pl,
         pl->T = T;
     }
     __syncthreads();
+    bool deep = false;
     long long at = 0, cut = 0;  // cut: (slots << 32) + tiles of the cut ones
+#pragma unroll 1
     for (int base = 0; base < items; base += nt) {
         const int i = base + tid;
         long long w = 0, c = 0;
@@ -425,6 +477,7 @@ __device__ __forceinline__ bool catt_plan(const CacheAttParams& p, CattPlan* pl,
                 const int d = catt_depth(t.L, T);
                 w = (long long)(t.L + min(t.L, 1 << d)) * ht;
                 if (d) c = ((ht << d) << 32) + ht;
+                deep |= d > CATT_JOIN_DEPTH;
             }
         }
         long long wt, ct;
@@ -439,13 +492,18 @@ __device__ __forceinline__ bool catt_plan(const CacheAttParams& p, CattPlan* pl,
         cut += ct;
     }
     // cu that lets sequences overlap can ask for more slots than there are
-    if (blockIdx.x == 0 && tid == 0 && p.max_slots) *p.count = (cut >> 32) > p.max_slots ? 0 : (int)(cut & 0xffffffff);
+    deep = __syncthreads_or(deep);
+    if (blockIdx.x == 0 && tid == 0 && p.max_slots) {
+        p.count[0] = (cut >> 32) > p.max_slots ? 0 : (int)(cut & 0xffffffff);
+        p.count[1] = deep;
+    }
     return __syncthreads_or(bad);
 }
 
 // Tokens without an answer: NaN, and an error unless the sequence was not granted (start < 0).
 template <int D>
 __device__ __noinline__ void catt_mark(const CacheAttParams& p) {
+#pragma unroll 1
     for (int b = blockIdx.x; b < p.batch; b += gridDim.x) {
         int n;
         const int first = catt_tokens(p, b, n), s = p.start[b];
@@ -458,6 +516,7 @@ __device__ __noinline__ void catt_mark(const CacheAttParams& p) {
         if (s >= 0 && threadIdx.x == 0) set_error(TBIK_ERR_PAGE);
         uint4* o = reinterpret_cast<uint4*>(p.out + (size_t)(first + use) * p.heads * D);
         const size_t m = (size_t)(n - use) * p.heads * (D / 8);
+#pragma unroll 1
         for (size_t k = threadIdx.x; k < m; k += blockDim.x) o[k] = make_uint4(0x7fc07fc0u, 0x7fc07fc0u, 0x7fc07fc0u, 0x7fc07fc0u);
     }
 }
@@ -489,8 +548,11 @@ __global__ void __launch_bounds__(CattCfg<D, RW, NWG>::THREADS, CattCfg<D, RW, N
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint64_t lim = p.wait_cycles;
     if (threadIdx.x == 0) {
+#pragma unroll 1
         for (int i = 0; i < 4 * ST; ++i) mbar_init(&bars[i], 1);
+#pragma unroll 1
         for (int w = 0; w < NWG; ++w)
+#pragma unroll 1
             for (int i = 0; i < 10; ++i) {
                 const bool by_warps = i == 2 || i == 3 || i >= 6;
                 mbar_init(&wb[10 * w + i], by_warps ? 4 : 1);
@@ -506,6 +568,7 @@ __global__ void __launch_bounds__(CattCfg<D, RW, NWG>::THREADS, CattCfg<D, RW, N
     }
     // the columns of P that no row has stay zero
     if (RW < 16)
+#pragma unroll 1
         for (int i = threadIdx.x; i < NWG * C::PB / 16; i += C::THREADS) reinterpret_cast<uint4*>(smem + C::OFF_P)[i] = make_uint4(0, 0, 0, 0);
     const bool marks = catt_plan<R>(p, &plan, scan_buf);
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -518,18 +581,18 @@ __global__ void __launch_bounds__(CattCfg<D, RW, NWG>::THREADS, CattCfg<D, RW, N
 
     if (warp == 0) {
         // ---------------------------------------------------- page copies
-        const int npl = CATT_LEAF / p.page;
+        const int npl = CATT_LEAF >> p.page_shift;
         const uint32_t pbytes = (uint32_t)p.page * D;
         const size_t vplane = (size_t)p.num_pages * p.kv_heads * pbytes;
         uint32_t g = 0, gv = 0;  // leaves whose keys, values were requested
         bool ok = true;
+#pragma unroll 1
         for (bool more = any; more && ok; more = u.next(p)) {
             const int32_t* row = p.table + (size_t)u.it.slot * p.max_pages;
-            const int last_row = min(u.it.rows, (u.tau + 1) * R) - 1;
-            const int imax = u.it.i0 + last_row / p.group;  // the last key that the tile sees
-            const int pages = imax / p.page + 1;
+            const int pages = (u.imax(p) >> p.page_shift) + 1;  // that the tile sees
             int pg = u.lo * npl + lane;
             int id = lane < npl && pg < pages ? row[pg] : 0;
+#pragma unroll 1
             for (int l = 0; l < u.size; ++l) {
                 const int here = min(npl, pages - (u.lo + l) * npl);
                 const int pn = pg + npl;
@@ -538,13 +601,13 @@ __global__ void __launch_bounds__(CattCfg<D, RW, NWG>::THREADS, CattCfg<D, RW, N
                 const uint8_t* src = p.pages + ((size_t)id * p.kv_heads + u.h) * pbytes;
                 const int st = g % ST;
                 const uint32_t ph = (g / ST) & 1;
-                ok = g < ST || mbar_wait(&ke[st], ph ^ 1, abort_flag, lim);
+                ok = g < ST || catt_wait(&ke[st], ph ^ 1, abort_flag, lim);
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
                 if (lane == 0) mbar_arrive_expect_tx(&kf[st], here * pbytes);
                 __syncwarp();
                 if (lane < here) bulk_load(smem_u32(smem + C::OFF_K + st * C::TILE) + lane * pbytes, src, pbytes, smem_u32(&kf[st]));
-                ok = g++ < ST || mbar_wait(&ve[st], ph ^ 1, abort_flag, lim);
+                ok = g++ < ST || catt_wait(&ve[st], ph ^ 1, abort_flag, lim);
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
                 if (lane == 0) mbar_arrive_expect_tx(&vf[st], here * pbytes);
@@ -557,8 +620,10 @@ __global__ void __launch_bounds__(CattCfg<D, RW, NWG>::THREADS, CattCfg<D, RW, N
         }
         if (lane == 0) {
             // what is in flight has to land before the CTA can exit
-            for (uint32_t x = g > (uint32_t)ST ? g - ST : 0; x < g; ++x) mbar_drain(&kf[x % ST], (x / ST) & 1, lim);
-            for (uint32_t x = gv > (uint32_t)ST ? gv - ST : 0; x < gv; ++x) mbar_drain(&vf[x % ST], (x / ST) & 1, lim);
+#pragma unroll 1
+            for (uint32_t x = g > (uint32_t)ST ? g - ST : 0; x < g; ++x) catt_drain(&kf[x % ST], (x / ST) & 1, lim);
+#pragma unroll 1
+            for (uint32_t x = gv > (uint32_t)ST ? gv - ST : 0; x < gv; ++x) catt_drain(&vf[x % ST], (x / ST) & 1, lim);
         }
         __syncwarp();
     } else if (warp == 1) {
@@ -569,12 +634,13 @@ __global__ void __launch_bounds__(CattCfg<D, RW, NWG>::THREADS, CattCfg<D, RW, N
             // O^T of leaf x; D = 64 leaves lanes 64..127 with what lies behind (not read)
             auto values = [&](uint32_t x) -> bool {
                 const int st = x % ST;
-                if (!mbar_wait(&vf[st], (x / ST) & 1, abort_flag, lim)) return false;
+                if (!catt_wait(&vf[st], (x / ST) & 1, abort_flag, lim)) return false;
+#pragma unroll 1
                 for (int w = 0; w < NWG; ++w) {
                     uint64_t* b = wb + 10 * w;
                     const uint32_t ob = x % C::OBUF, use = x / C::OBUF;
-                    if (!mbar_wait(&b[8], x & 1, abort_flag, lim)) return false;
-                    if (use > 0 && !mbar_wait(&b[6 + ob], (use - 1) & 1, abort_flag, lim)) return false;
+                    if (!catt_wait(&b[8], x & 1, abort_flag, lim)) return false;
+                    if (use > 0 && !catt_wait(&b[6 + ob], (use - 1) & 1, abort_flag, lim)) return false;
                     tc_fence_after();
                     const uint32_t pa = smem_u32(smem + C::OFF_P + w * C::PB);
 #pragma unroll
@@ -589,15 +655,18 @@ __global__ void __launch_bounds__(CattCfg<D, RW, NWG>::THREADS, CattCfg<D, RW, N
                 tc_commit(&ve[st]);
                 return true;
             };
+#pragma unroll 1
             for (bool more = any; more; more = u.next(p), ++nu) {
+#pragma unroll 1
                 for (int l = 0; l < u.size; ++l, ++g) {
                     const int st = g % ST;
-                    if (!mbar_wait(&kf[st], (g / ST) & 1, abort_flag, lim)) goto mma_out;
+                    if (!catt_wait(&kf[st], (g / ST) & 1, abort_flag, lim)) goto mma_out;
+#pragma unroll 1
                     for (int w = 0; w < NWG; ++w) {
                         uint64_t* b = wb + 10 * w;
                         const uint32_t sb = g % C::SBUF, use = g / C::SBUF;
-                        if (l == 0 && !mbar_wait(&b[9], nu & 1, abort_flag, lim)) goto mma_out;
-                        if (use > 0 && !mbar_wait(&b[2 + sb], (use - 1) & 1, abort_flag, lim)) goto mma_out;
+                        if (l == 0 && !catt_wait(&b[9], nu & 1, abort_flag, lim)) goto mma_out;
+                        if (use > 0 && !catt_wait(&b[2 + sb], (use - 1) & 1, abort_flag, lim)) goto mma_out;
                         tc_fence_after();
                         const uint32_t qa = smem_u32(smem + C::OFF_Q + w * C::QB), ka = smem_u32(smem + C::OFF_K + st * C::TILE);
 #pragma unroll
@@ -613,7 +682,7 @@ __global__ void __launch_bounds__(CattCfg<D, RW, NWG>::THREADS, CattCfg<D, RW, N
             if (g > 0) values(g - 1);
         mma_out:
             tc_commit(done);  // every MMA retires before TMEM is released
-            mbar_drain(done, 0, lim);
+            catt_drain(done, 0, lim);
         }
         __syncwarp();
     } else {
@@ -622,9 +691,9 @@ __global__ void __launch_bounds__(CattCfg<D, RW, NWG>::THREADS, CattCfg<D, RW, N
         uint64_t* b = wb + 10 * wg;
         float* x = reinterpret_cast<float*>(smem + C::OFF_X) + wg * C::X_FLOATS;
         float* xw = x + C::X_WARP + qd * C::X_PER_WARP;   // this warp's own
-        float2* fac = reinterpret_cast<float2*>(xw);      // [RW]
-        float* ofac = xw + 2 * RW;                        // [RW]
-        float2* pend = reinterpret_cast<float2*>(xw + 3 * RW);  // [6][RW] (m, s)
+        float *fac = xw, *ofac = xw + RW;                 // [RW] factors of a step
+        float *rmax = xw + 2 * RW, *rval = xw + 3 * RW;   // [RW] a row's -m c, and 256 / its largest value scale
+        float2* pend = reinterpret_cast<float2*>(xw + 4 * RW);  // [6][RW] (m, s)
         const uint32_t tm = tmem + wg * C::WG_COLS + ((uint32_t)(qd * 32) << 16);
         uint8_t* qs = smem + C::OFF_Q + wg * C::QB;
         uint8_t* ps = smem + C::OFF_P + wg * C::PB;
@@ -645,7 +714,7 @@ __global__ void __launch_bounds__(CattCfg<D, RW, NWG>::THREADS, CattCfg<D, RW, N
                 const bool live = r < RW && fr < un.it.rows;
                 uint4 w = make_uint4(0, 0, 0, 0);
                 if (live) {
-                    const int t = fr / p.group, hd = un.h * p.group + fr - t * p.group;
+                    const int t = catt_div(p, fr), hd = un.h * p.group + fr - t * p.group;
                     w = *reinterpret_cast<const uint4*>(p.q + ((size_t)(un.it.tok0 + t) * p.heads + hd) * D + part * 8);
                 }
                 const uint32_t a[4] = {w.x, w.y, w.z, w.w};
@@ -679,35 +748,35 @@ __global__ void __launch_bounds__(CattCfg<D, RW, NWG>::THREADS, CattCfg<D, RW, N
             __syncwarp();
             if (lane == 0) mbar_arrive(&b[9]);
         };
-        // This thread's key in leaf l of a unit: its page (-1: not seen by the tile, -2: no such page).
-        auto key_page = [&](const CattUnits<R>& un, int l) -> int {
-            const int last_row = min(un.it.rows, (un.tau + 1) * R) - 1;
-            const int imax = un.it.i0 + last_row / p.group;
+        // The page of this thread's key in leaf l of a unit: what the table holds, if some row of the tile sees the key.
+        auto key_page = [&](const CattUnits<R>& un, int imax, int l) -> int {
             const int pos = (un.lo + l) * CATT_LEAF + tid;
-            if (pos > imax) return -1;
-            const int id = p.table[(size_t)un.it.slot * p.max_pages + pos / p.page];
-            return id < 0 || id >= p.num_pages ? -2 : id;
+            return pos <= imax ? p.table[(size_t)un.it.slot * p.max_pages + (pos >> p.page_shift)] : -1;
         };
-        auto key_scales = [&](const CattUnits<R>& un, int id, float& k, float& v) {
+        auto key_scales = [&](int h, int id, float& k, float& v) {
             k = v = 0.0f;
-            if (id >= 0) {
-                const size_t ph = (size_t)id * p.kv_heads + un.h;
-                k = p.scales[ph];
-                v = p.scales[(size_t)p.num_pages * p.kv_heads + ph];
+            if (id >= 0 && id < p.num_pages) {
+                const float* at = p.scales + (size_t)id * p.kv_heads + h;
+                k = at[0];
+                v = at[(size_t)p.num_pages * p.kv_heads];
             }
         };
+        // Lane k: how many nodes leaf k closes (low half), and leaf k + 32 (high half).
+        auto pop_codes = [&](int size) { return catt_pops(size, min(lane, size - 1)) | catt_pops(size, min(lane + 32, size - 1)) << 16; };
 
         uint32_t g = 0, nu = 0, cleaned = 0;
         CattUnits<R> prev = u;          // the unit of the previous leaf
-        int prev_l = 0;
+        int prev_l = 0, prev_codes = 0;
         float prev_m = 0.0f, prev_o = 0.0f;  // lane = row: its maximum and the scale of its O
         int depth = 0;
         float cks = 0.0f, cvs = 0.0f;
-        int cid = -1;
+        int cid = -1, imax = 0, codes = 0;
         if (any) {
-            cid = key_page(u, 0);
+            imax = u.imax(p);
+            cid = key_page(u, imax, 0);
             load_q(u, 0);
-            key_scales(u, cid, cks, cvs);
+            key_scales(u.h, cid, cks, cvs);
+            codes = pop_codes(u.size);
         }
 
         // The summary of leaf g1 of unit `prev` enters the tree.
@@ -717,56 +786,72 @@ __global__ void __launch_bounds__(CattCfg<D, RW, NWG>::THREADS, CattCfg<D, RW, N
             const int row = lane % RW;
             float m = prev_m;
             float s = __fadd_rn(__fadd_rn(sums[row], sums[RW + row]), __fadd_rn(sums[2 * RW + row], sums[3 * RW + row]));
-            if (lane < RW) ofac[lane] = prev_o;
-            __syncwarp();
+            const int code = __shfl_sync(0xffffffffu, prev_codes, prev_l & 31);
+            int pops = prev_l < 32 ? code & 0xffff : code >> 16;
+            const bool last = prev_l + 1 == prev.size;
+            if (prev_l == 0) depth = CATT_PENDING - (32 - __clz(max(prev.size - 1, 0)));  // small trees stay in TMEM
+            // O is in units of prev_o, a power of two: the first step multiplies it in
+            float scale_o = prev_o;
             float o[RW];
             if (has_dim) {
                 uint32_t raw[RW];
                 catt_ld<RW>(tm + C::O_COL + ob * C::NP, raw);
 #pragma unroll
-                for (int r = 0; r < RW; r += 4) {
-                    const float4 f = *reinterpret_cast<const float4*>(ofac + r);
-                    upk2(mul2(pk2(__uint_as_float(raw[r]), __uint_as_float(raw[r + 1])), pk2(f.x, f.y)), o[r], o[r + 1]);
-                    upk2(mul2(pk2(__uint_as_float(raw[r + 2]), __uint_as_float(raw[r + 3])), pk2(f.z, f.w)), o[r + 2], o[r + 3]);
-                }
+                for (int r = 0; r < RW; ++r) o[r] = __uint_as_float(raw[r]);
             }
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&b[6 + ob]);
-            const bool last = prev_l + 1 == prev.size;
-            if (prev_l == 0) depth = CATT_PENDING - (32 - __clz(max(prev.size - 1, 0)));  // small trees stay in TMEM
-            for (int c = catt_pops(prev.size, prev_l); c > 0; --c) {
+            if (pops == 0) {
+                if (lane < RW) ofac[lane] = scale_o;
+                __syncwarp();
+                if (has_dim)
+#pragma unroll
+                    for (int r = 0; r < RW; r += 4) {
+                        const float4 f = *reinterpret_cast<const float4*>(ofac + r);
+                        upk2(mul2(pk2(o[r], o[r + 1]), pk2(f.x, f.y)), o[r], o[r + 1]);
+                        upk2(mul2(pk2(o[r + 2], o[r + 3]), pk2(f.z, f.w)), o[r + 2], o[r + 3]);
+                    }
+            }
+#pragma unroll 1
+            for (; pops > 0; --pops) {
                 --depth;
                 const float2 a = pend[depth * RW + row];
                 float M, ea, eb;
                 catt_factors(a.x, m, M, ea, eb);
                 s = __fmaf_rn(s, eb, __fmul_rn(a.y, ea));
                 m = M;
-                __syncwarp();
-                if (lane < RW) fac[lane] = make_float2(ea, eb);
+                if (lane < RW) {
+                    fac[lane] = ea;
+                    ofac[lane] = __fmul_rn(eb, scale_o);
+                }
+                scale_o = 1.0f;
                 __syncwarp();
                 if (has_dim) {
                     uint32_t raw[RW];
-                    if (depth < CATT_PENDING - C::TPEND) {
+                    if (C::TPEND < CATT_PENDING && depth < CATT_PENDING - C::TPEND) {
 #pragma unroll
                         for (int r = 0; r < RW; ++r) raw[r] = __float_as_uint(overflow[r * 128]);
                     } else {
                         catt_ld<RW>(tm + C::ST_COL + (depth - (CATT_PENDING - C::TPEND)) * RW, raw);
                     }
 #pragma unroll
-                    for (int r = 0; r < RW; r += 2) {
-                        const float4 f = *reinterpret_cast<const float4*>(fac + r);
-                        upk2(fma2(pk2(o[r], o[r + 1]), pk2(f.y, f.w),
-                                  mul2(pk2(__uint_as_float(raw[r]), __uint_as_float(raw[r + 1])), pk2(f.x, f.z))),
+                    for (int r = 0; r < RW; r += 4) {
+                        const float4 fa = *reinterpret_cast<const float4*>(fac + r), fb = *reinterpret_cast<const float4*>(ofac + r);
+                        upk2(fma2(pk2(o[r], o[r + 1]), pk2(fb.x, fb.y),
+                                  mul2(pk2(__uint_as_float(raw[r]), __uint_as_float(raw[r + 1])), pk2(fa.x, fa.y))),
                              o[r], o[r + 1]);
+                        upk2(fma2(pk2(o[r + 2], o[r + 3]), pk2(fb.z, fb.w),
+                                  mul2(pk2(__uint_as_float(raw[r + 2]), __uint_as_float(raw[r + 3])), pk2(fa.z, fa.w))),
+                             o[r + 2], o[r + 3]);
                     }
                 }
+                __syncwarp();
             }
-            __syncwarp();
             if (!last) {
                 if (lane < RW) pend[depth * RW + lane] = make_float2(m, s);
                 if (has_dim) {
-                    if (depth < CATT_PENDING - C::TPEND) {
+                    if (C::TPEND < CATT_PENDING && depth < CATT_PENDING - C::TPEND) {
 #pragma unroll
                         for (int r = 0; r < RW; ++r) overflow[r * 128] = o[r];
                     } else {
@@ -782,7 +867,7 @@ __global__ void __launch_bounds__(CattCfg<D, RW, NWG>::THREADS, CattCfg<D, RW, N
                 if (lane < RW) ofac[lane] = __frcp_rn(s);
                 __syncwarp();
                 if (has_dim) {
-                    int t = fr0 / p.group, hd = fr0 - t * p.group;
+                    int t = catt_div(p, fr0), hd = fr0 - t * p.group;
                     uint16_t* op = p.out + ((size_t)(prev.it.tok0 + t) * p.heads + prev.h * p.group) * D + tid;
 #pragma unroll
                     for (int r = 0; r < RW; ++r) {
@@ -815,23 +900,29 @@ __global__ void __launch_bounds__(CattCfg<D, RW, NWG>::THREADS, CattCfg<D, RW, N
             __syncwarp();
         };
 
+#pragma unroll 1
         for (bool more = any; more; ++nu) {
             CattUnits<R> nxt = u;
             const bool has_next = nxt.next(p);
+            const int fr0 = u.tau * R + wg * RW, i0 = u.it.i0 & 127;
+            const int nmax = has_next ? nxt.imax(p) : 0;
+            const int row_i = (i0 + catt_div(p, fr0 + lane % RW)) & 127;  // lane = row: its position in the block
+            const float* cst = x + C::X_CST + (nu & 1) * RW;
+#pragma unroll 1
             for (int l = 0; l < u.size; ++l, ++g) {
                 const bool last = l + 1 == u.size;
                 const uint32_t sb = g % C::SBUF;
-                if (!ab) ab = !mbar_wait(&b[0 + sb], (g / C::SBUF) & 1, abort_flag, lim);
-                ab = __any_sync(0xffffffffu, ab);
                 float a[RW];
                 float* mx = x + C::X_MAX + (g & 1) * 4 * RW;
                 float* pv = x + C::X_PV + (g & 1) * 8;
                 const bool diag = u.lo + l == u.it.L - 1;
-                const int fr0 = u.tau * R + wg * RW;
-                // the key of the next leaf
+                // the next leaf's key
                 int nid = -1;
-                if (!last) nid = key_page(u, l + 1);
-                else if (has_next) nid = key_page(nxt, 0);
+                if (!last) nid = key_page(u, imax, l + 1);
+                else if (has_next) nid = key_page(nxt, nmax, 0);
+                if (!ab) ab = !catt_wait(&b[0 + sb], (g / C::SBUF) & 1, abort_flag, lim);
+                ab = __any_sync(0xffffffffu, ab);
+                const bool seen = (u.lo + l) * CATT_LEAF + tid <= imax, no_page = seen && (cid < 0 || cid >= p.num_pages);
                 if (!ab) {
                     tc_fence_after();
                     uint32_t raw[C::NQ];
@@ -844,21 +935,20 @@ __global__ void __launch_bounds__(CattCfg<D, RW, NWG>::THREADS, CattCfg<D, RW, N
                     for (int r = 0; r < RW; r += 2)
                         upk2(mul2(fma2(pk2(__uint_as_float(raw[RW + r]), __uint_as_float(raw[RW + r + 1])), i32,
                                        pk2(__uint_as_float(raw[r]), __uint_as_float(raw[r + 1]))), k2), a[r], a[r + 1]);
-                    if (cid == -2) {
+                    if (__any_sync(0xffffffffu, no_page)) {
+                        if (no_page) {
 #pragma unroll
-                        for (int r = 0; r < RW; ++r) a[r] = __uint_as_float(0x7fc00000u);
-                        set_error(TBIK_ERR_PAGE);
+                            for (int r = 0; r < RW; ++r) a[r] = __uint_as_float(0x7fc00000u);
+                            set_error(TBIK_ERR_PAGE);
+                        }
                     }
                     if (diag) {
-                        int t = fr0 / p.group, hd = fr0 - t * p.group, i = (u.it.i0 + t) & 127;
+                        // row r is at block position i0 + (fr0 + r) / group and does not see this key if that is less
+                        // than tid, that is, if fr0 + r < (tid - i0) * group
+                        const int hidden = (tid - i0) * p.group - fr0;
 #pragma unroll
-                        for (int r = 0; r < RW; ++r) {
-                            if (tid > i) a[r] = -INFINITY;
-                            if (++hd == p.group) {
-                                hd = 0;
-                                ++i;
-                            }
-                        }
+                        for (int r = 0; r < RW; ++r)
+                            if (r < hidden) a[r] = -INFINITY;
                     }
 #pragma unroll
                     for (int r = 0; r < RW; r += 4) {
@@ -869,63 +959,57 @@ __global__ void __launch_bounds__(CattCfg<D, RW, NWG>::THREADS, CattCfg<D, RW, N
                         m4.w = warp_max_f32(a[r + 3]);
                         if (lane == 0) *reinterpret_cast<float4*>(mx + qd * RW + r) = m4;
                     }
-                    if (tid % p.page == 0) pv[tid / p.page] = cvs;
+                    if ((tid & (p.page - 1)) == 0) pv[tid >> p.page_shift] = cvs;
                 }
                 if (named_barrier_or(bar, 128, ab)) goto epi_out;
                 // scales of the next leaf's key
                 float nks, nvs;
-                key_scales(last ? nxt : u, nid, nks, nvs);
+                key_scales(last ? nxt.h : u.h, nid, nks, nvs);
                 if (last && has_next) load_q(nxt, nu + 1);
-                const float* cst = x + C::X_CST + (nu & 1) * RW;
-                const int npl = CATT_LEAF / p.page;
-                // the largest value scale among a row's visible pages of the leaf
-                auto vmax = [&](int i) {
-                    float v = pv[0];
-                    for (int k = 1; k < npl; ++k)
-                        if (k * p.page <= i) v = fmaxf(v, pv[k]);
-                    return v;
-                };
-                const float vm = diag ? 1.0f : vmax(127);
-                float f = 0.0f;
-                if (!diag) f = __fmul_rn(cvs, __fmul_rn(256.0f, __frcp_rn(vm)));
-                float w[RW];  // 256 f p
-                {
-                    int t = fr0 / p.group, hd = fr0 - t * p.group, i = (u.it.i0 + t) & 127;
-#pragma unroll
-                    for (int r = 0; r < RW; r += 4) {
-                        const float4 m0 = *reinterpret_cast<const float4*>(mx + r), m1 = *reinterpret_cast<const float4*>(mx + RW + r);
-                        const float4 m2 = *reinterpret_cast<const float4*>(mx + 2 * RW + r), m3 = *reinterpret_cast<const float4*>(mx + 3 * RW + r);
-                        const float4 c4 = *reinterpret_cast<const float4*>(cst + r);
-                        const float mm[4] = {fmaxf(fmax3(m0.x, m1.x, m2.x), m3.x), fmaxf(fmax3(m0.y, m1.y, m2.y), m3.y),
-                                             fmaxf(fmax3(m0.z, m1.z, m2.z), m3.z), fmaxf(fmax3(m0.w, m1.w, m2.w), m3.w)};
-                        const float cc[4] = {c4.x, c4.y, c4.z, c4.w};
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            a[r + k] = ex2_hw(__fmul_rn(__fsub_rn(a[r + k], mm[k]), cc[k]));
-                            float fk = f;
-                            if (diag) {
-                                fk = tid <= i ? __fmul_rn(cvs, __fmul_rn(256.0f, __frcp_rn(vmax(i)))) : 0.0f;
-                                if (++hd == p.group) {
-                                    hd = 0;
-                                    ++i;
-                                }
-                            }
-                            w[r + k] = __fmul_rn(a[r + k], fk);
-                        }
-                    }
-                }
-                // this warp's view of row `lane`: its maximum and O's scale
+                // lane = row: its maximum, and the largest value scale among its visible pages of the leaf
                 float nm, no;
                 {
-                    const int row = lane % RW;
+                    const int row = lane % RW, i = diag ? row_i : 127;
+                    const float4 v0 = *reinterpret_cast<const float4*>(pv), v1 = *reinterpret_cast<const float4*>(pv + 4);
+                    const float v[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
+                    float vm = v[0];
+#pragma unroll
+                    for (int k = 1; k < 8; ++k)
+                        if (k << p.page_shift <= i) vm = fmaxf(vm, v[k]);
                     nm = __fmul_rn(fmaxf(fmax3(mx[row], mx[RW + row], mx[2 * RW + row]), mx[3 * RW + row]), cst[row]);
-                    const int i = (u.it.i0 + (fr0 + row) / p.group) & 127;
-                    no = __fmul_rn(diag ? vmax(i) : vm, 0.00390625f);
+                    no = __fmul_rn(vm, 0.00390625f);
+                    // 256 / vm: scales are powers of two
+                    const float iv = __fmul_rn(256.0f, __uint_as_float((254u << 23) - __float_as_uint(vm)));
+                    if (lane < RW) {
+                        rmax[lane] = -nm;
+                        rval[lane] = iv;
+                    }
+                    __syncwarp();
+                }
+#pragma unroll
+                for (int r = 0; r < RW; r += 4) {
+                    const float4 c4 = *reinterpret_cast<const float4*>(cst + r), m4 = *reinterpret_cast<const float4*>(rmax + r);
+                    float y[4];
+                    upk2(fma2(pk2(a[r], a[r + 1]), pk2(c4.x, c4.y), pk2(m4.x, m4.y)), y[0], y[1]);
+                    upk2(fma2(pk2(a[r + 2], a[r + 3]), pk2(c4.z, c4.w), pk2(m4.z, m4.w)), y[2], y[3]);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) a[r + k] = ex2_hw(y[k]);
+                }
+                float w[RW];  // 256 f p
+                if (!diag) {
+                    const float f = __fmul_rn(cvs, rval[0]);
+                    const f2x f2 = pk2(f, f);
+#pragma unroll
+                    for (int r = 0; r < RW; r += 2) upk2(mul2(pk2(a[r], a[r + 1]), f2), w[r], w[r + 1]);
+                } else {
+                    // f <= 1 for a key that the row sees; for others p is 0
+#pragma unroll
+                    for (int r = 0; r < RW; ++r) w[r] = __fmul_rn(a[r], fminf(__fmul_rn(cvs, rval[r]), 256.0f));
                 }
                 // P of the previous leaf is read until its O is there
                 if (g > 0 && !ab) {
                     const uint32_t g1 = g - 1;
-                    ab = !mbar_wait(&b[4 + g1 % C::OBUF], (g1 / C::OBUF) & 1, abort_flag, lim);
+                    ab = !catt_wait(&b[4 + g1 % C::OBUF], (g1 / C::OBUF) & 1, abort_flag, lim);
                     ab = __any_sync(0xffffffffu, ab);
                 }
                 if (!ab) {
@@ -954,16 +1038,14 @@ __global__ void __launch_bounds__(CattCfg<D, RW, NWG>::THREADS, CattCfg<D, RW, N
                     // values that no row sees must be finite (0 x NaN): zero behind the tile's last key, and NaN bytes
                     // between its first row's key and that
                     const int st = g % ST;
-                    if (!ab) ab = !mbar_wait(&vf[st], (g / ST) & 1, abort_flag, lim);
+                    if (!ab) ab = !catt_wait(&vf[st], (g / ST) & 1, abort_flag, lim);
                     ab = __any_sync(0xffffffffu, ab);
                     if (!ab) {
-                        const int r0 = u.tau * R, r1 = min(u.it.rows, r0 + R) - 1;
-                        const int imin = (u.it.i0 + r0 / p.group) & 127, imax = (u.it.i0 + r1 / p.group) & 127;
-                        if (tid > imin) {
+                        if (tid > (u.imin(p) & 127)) {
                             uint8_t* vt = smem + C::OFF_V + st * C::TILE + (tid >> 3) * (D * 8) + (tid & 7) * 16;
                             for (int k = wg; k < D / 16; k += NWG) {
                                 uint4* at = reinterpret_cast<uint4*>(vt + k * 128);
-                                if (tid > imax || cid < 0) {
+                                if (!seen || no_page) {
                                     *at = make_uint4(0, 0, 0, 0);
                                 } else {
                                     const uint4 y = *at;
@@ -980,7 +1062,7 @@ __global__ void __launch_bounds__(CattCfg<D, RW, NWG>::THREADS, CattCfg<D, RW, N
                         fence_proxy_async_smem();
                         __syncwarp();
                         if (lane == 0) mbar_arrive(clean);
-                        ab = !mbar_wait(clean, cleaned++ & 1, abort_flag, lim);
+                        ab = !catt_wait(clean, cleaned++ & 1, abort_flag, lim);
                         ab = __any_sync(0xffffffffu, ab);
                     }
                 }
@@ -1012,6 +1094,7 @@ __global__ void __launch_bounds__(CattCfg<D, RW, NWG>::THREADS, CattCfg<D, RW, N
                 }
                 prev = u;
                 prev_l = l;
+                prev_codes = codes;
                 prev_m = nm;
                 prev_o = no;
                 cid = nid;
@@ -1020,11 +1103,13 @@ __global__ void __launch_bounds__(CattCfg<D, RW, NWG>::THREADS, CattCfg<D, RW, N
             }
             u = nxt;
             more = has_next;
+            imax = nmax;
+            if (more) codes = pop_codes(u.size);
         }
         if (named_barrier_or(bar, 128, ab)) goto epi_out;
         if (g > 0) {
             const uint32_t g1 = g - 1;
-            ab = !mbar_wait(&b[4 + g1 % C::OBUF], (g1 / C::OBUF) & 1, abort_flag, lim);
+            ab = !catt_wait(&b[4 + g1 % C::OBUF], (g1 / C::OBUF) & 1, abort_flag, lim);
             if (!__any_sync(0xffffffffu, ab)) {
                 tc_fence_after();
                 tree_step(g1);
@@ -1043,8 +1128,9 @@ __global__ void __launch_bounds__(CattCfg<D, RW, NWG>::THREADS, CattCfg<D, RW, N
 
 // ------------------------------------------------------------------ the tree above the units
 //
-// One block per cut tile's row, a thread per dim in each of eight groups; a group evaluates one of the subtrees three
-// levels below the root, one thread's values of eight nodes in flight at a time.  Empty nodes are passed over.
+// A thread per dim.  Trees that are cut a few levels deep go to one group of D threads per row; for deeper ones (few rows
+// over long contexts) the block's eight groups take one subtree each.  Eight nodes' values are in flight at a time.
+// Empty nodes are passed over.
 
 constexpr int CATT_JOIN_GROUPS = 8;
 
@@ -1064,65 +1150,76 @@ __device__ __forceinline__ CattSum catt_join(const CattSum& a, const CattSum& b)
     return r;
 }
 
+// The tree over nodes v0 .. v0 + n - 1 (n a power of two) of a tile's 2^d; PEND: log2(n / 8) at most.
+template <int D, int R, int PEND>
+__device__ __forceinline__ CattSum catt_join_nodes(const CacheAttParams& p, int slot, int L, int d, int v0, int n, int row, int dim) {
+    CattSum st[PEND + 1], r;
+    r.any = false;
+    int depth = 0;
+    const int step = min(n, 8);
+    for (int v = 0; v < n; v += step) {
+        CattSum x[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            x[k].any = false;
+            if (k < step) {
+                if (catt_node_size(L, d, v0 + v + k)) {
+                    const size_t at = (size_t)(slot + v0 + v + k) * R + row;
+                    const float2 ms = p.ms[at];
+                    x[k].m = ms.x;
+                    x[k].s = ms.y;
+                    x[k].o = p.o[at * D + dim];
+                    x[k].any = true;
+                }
+            }
+        }
+#pragma unroll
+        for (int h = 1; h < 8; h <<= 1)
+            if (h < step)
+#pragma unroll
+                for (int k = 0; k + h < 8; k += 2 * h) x[k] = catt_join(x[k], x[k + h]);
+        r = x[0];
+        for (int c = v / step; c & 1; c >>= 1) r = catt_join(st[--depth], r);
+        if (v + step < n) st[depth++] = r;
+    }
+    return r;
+}
+
 template <int D, int R>
 __global__ void __launch_bounds__(D* CATT_JOIN_GROUPS) cache_attention_join_kernel(const __grid_constant__ CacheAttParams p) {
     __shared__ CattSum part[CATT_JOIN_GROUPS][D];
     const int dim = threadIdx.x % D, grp = threadIdx.x / D;
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int count = *p.count;
-    for (int w = blockIdx.x; w < count * R; w += gridDim.x) {
-        const int4 t0 = p.tiles[2 * (size_t)(w / R)], t1 = p.tiles[2 * (size_t)(w / R) + 1];
-        const int row = w % R, d = t0.y, L = t0.z;
-        if (row >= t0.w || t0.x + (1 << d) > p.max_slots) continue;  // the same for the whole block
-        const int top = min(d, 3);
-        CattSum r;
-        r.any = false;
-        if (grp < (1 << top)) {
-            const int per = 1 << (d - top), v0 = grp * per;  // this group's nodes
-            CattSum st[20];
-            int depth = 0;
-            const int step = min(per, 8);
-            for (int v = 0; v < per; v += step) {
-                CattSum x[8];
-#pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    x[k].any = false;
-                    if (k < step) {
-                        int lo, size;
-                        catt_node(L, d, v0 + v + k, lo, size);
-                        if (size) {
-                            const size_t at = (size_t)(t0.x + v0 + v + k) * R + row;
-                            const float2 ms = p.ms[at];
-                            x[k].m = ms.x;
-                            x[k].s = ms.y;
-                            x[k].o = p.o[at * D + dim];
-                            x[k].any = true;
-                        }
-                    }
-                }
-#pragma unroll
-                for (int h = 1; h < 8; h <<= 1)
-                    if (h < step)
-#pragma unroll
-                        for (int k = 0; k + h < 8; k += 2 * h) x[k] = catt_join(x[k], x[k + h]);
-                r = x[0];
-                for (int c = v / step; c & 1; c >>= 1) r = catt_join(st[--depth], r);
-                st[depth++] = r;
-            }
-        }
+    const int count = p.count[0], deep = p.count[1];
+    auto put = [&](const int4& t1, int row, const CattSum& x) {
+        const int fr = t1.y + row, t = catt_div(p, fr), hd = t1.z * p.group + fr - t * p.group;
+        p.out[((size_t)(t1.x + t) * p.heads + hd) * D + dim] = f2bf(__fmul_rn(x.o, __frcp_rn(x.s)));
+    };
+    for (long long w = (long long)blockIdx.x * CATT_JOIN_GROUPS + grp; w < (long long)count * R; w += (long long)gridDim.x * CATT_JOIN_GROUPS) {
+        const int4 t0 = p.tiles[2 * (w / R)], t1 = p.tiles[2 * (w / R) + 1];  // slot, d, L, rows; token, first row, kv head
+        const int row = (int)(w % R);
+        if (row >= t0.w || t0.y > CATT_JOIN_DEPTH) continue;
+        put(t1, row, catt_join_nodes<D, R, 1>(p, t0.x, t0.z, t0.y, 0, 1 << t0.y, row, dim));
+    }
+    if (!deep) return;
+    for (long long w = blockIdx.x; w < (long long)count * R; w += gridDim.x) {
+        const int4 t0 = p.tiles[2 * (w / R)], t1 = p.tiles[2 * (w / R) + 1];
+        const int row = (int)(w % R);
+        if (row >= t0.w || t0.y <= CATT_JOIN_DEPTH) continue;  // the same for the whole block
+        const int per = 1 << (t0.y - 3);
+        const CattSum r = catt_join_nodes<D, R, 14>(p, t0.x, t0.z, t0.y, grp * per, per, row, dim);
         __syncthreads();
         part[grp][dim] = r;
         __syncthreads();
         if (grp == 0) {
             CattSum x[8];
 #pragma unroll
-            for (int k = 0; k < 8; ++k) x[k] = part[k][dim];  // groups behind the last are empty
+            for (int k = 0; k < 8; ++k) x[k] = part[k][dim];
 #pragma unroll
             for (int h = 1; h < 8; h <<= 1)
 #pragma unroll
                 for (int k = 0; k + h < 8; k += 2 * h) x[k] = catt_join(x[k], x[k + h]);
-            const int fr = t1.y + row, t = fr / p.group, hd = t1.z * p.group + fr - t * p.group;
-            p.out[((size_t)(t1.x + t) * p.heads + hd) * D + dim] = f2bf(__fmul_rn(x[0].o, __frcp_rn(x[0].s)));
+            put(t1, row, x[0]);
         }
     }
 }

@@ -362,6 +362,8 @@ tbik_status tbik_cache_attention(const uint16_t* q, const uint8_t* pages, const 
     p.tokens = tokens, p.batch = batch, p.slots = slots, p.max_pages = max_pages, p.num_pages = num_pages;
     p.heads = heads, p.kv_heads = kv_heads, p.page = page, p.max_q = max_q, p.max_keys = max_keys;
     p.group = heads / kv_heads;
+    p.group_inv = ((1u << 31) + (unsigned)p.group - 1) / (unsigned)p.group;
+    p.page_shift = page == 16 ? 4 : page == 32 ? 5 : page == 64 ? 6 : 7;
     p.blocks = c.blocks;
     p.scale = (float)(1.4426950408889634 / std::sqrt((double)head_dim));
     if (c.slots) {
