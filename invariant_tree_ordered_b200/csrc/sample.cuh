@@ -10,9 +10,17 @@
 // nearest at 2^-32 moves a border between tokens by about 2^-32 sqrt(V) of the largest weight.
 //
 // Layout: a cluster of 1..8 blocks holds one row in its shared memory (one read of HBM), every later step runs there.
-// The threshold of top-k and top-p is found by a histogram over linear bins of (max - z) / temperature, whose border
-// bin (usually some tens of tokens) is sorted in one block; a border bin with more tokens is split again on the bits
-// of the logits until it fits or all its logits are equal.
+// What bounds it are the instructions per token, so the common case takes two sweeps over shared memory:
+//   1. a histogram of counts over linear bins of (max - z) / temperature, 32 to a unit (one shared atomic per token);
+//      with top-k the bin of the k-th token is exact, and the tokens up to it (a few more than k) are sorted in one block,
+//      where the rest is decided too;
+//   2. with top-p alone, counts times the bins' middle weights estimate the mass up to a bin to a few 0.1 %, which gives
+//      a bracket of bins around the limit; the second sweep forms the exact sums: the row's mass, the kept mass above the
+//      bracket (per chunk of tokens, for the choice), and a histogram of the tokens inside, whose border bin is sorted.
+//      The estimate only chooses the bracket; whether the limit lies inside is checked with the exact sums.
+// A row that does not fit (the limit outside the bracket, too many tokens in a list, infinite logits, temperatures near
+// 0) takes the general steps: histograms of masses, the border bin split again on the bits of the logits until it
+// fits or all its logits are equal.
 #pragma once
 
 #include "device_common.cuh"
@@ -27,6 +35,10 @@ constexpr int SMP_CHUNK_ROUNDS = 8;    // rounds of SMP_THREADS tokens per parti
 constexpr int SMP_CHUNK = SMP_THREADS * SMP_CHUNK_ROUNDS;
 constexpr int SMP_MAX_SEG = 12 * SMP_CHUNK;  // tokens per block
 constexpr int SMP_MAX_CLUSTER = 8;
+constexpr int SMP_BINS2 = 256;         // of the second histogram
+constexpr int SMP_LIST = 2048;         // tokens of a top-k set that one block sorts; tokens of a bracket per block
+constexpr int SMP_SWEEP = 16;          // tokens per thread and chunk of the second sweep
+constexpr int SMP_SWEEP_CHUNKS = (SMP_MAX_SEG + 16) / (SMP_THREADS * SMP_SWEEP) + 1;
 
 struct SampleParams {
     const void* logits;
@@ -40,20 +52,39 @@ struct SampleParams {
 };
 
 struct SampleShared {
-    unsigned long long csum[SMP_MAX_SEG / SMP_CHUNK][SMP_WARPS];
-    unsigned long long wsum[SMP_CHUNK_ROUNDS][SMP_WARPS];
-    unsigned long long cand[SMP_CAND];  // key << 32 | ~index: descending order is the order of the tokens
+    union {
+        unsigned long long csum[SMP_MAX_SEG / SMP_CHUNK][SMP_WARPS];  // kept mass of each chunk
+        unsigned long long sweep[SMP_SWEEP_CHUNKS][SMP_WARPS];        // and in the two-sweep form
+    };
+    union {
+        unsigned long long wsum[SMP_CHUNK_ROUNDS][SMP_WARPS];  // of the chosen chunk, when the lists are done with
+        unsigned long long cand[SMP_LIST];  // key << 32 | ~index: descending order is the order of the tokens
+        struct {
+            unsigned long long border_list[SMP_CAND];
+            uint32_t loc[SMP_LIST];         // this block's tokens in the bracket
+        };
+    };
+    unsigned long long extra[SMP_SWEEP_CHUNKS];             // and of its tokens in the bracket
+    // what each block of the cluster has pushed to this one
+    struct {
+        unsigned long long total, above, in, kept;
+        float max;
+        uint32_t nan, first, lists;
+    } from[SMP_MAX_CLUSTER];
+    unsigned long long part[3][SMP_WARPS];
+    alignas(16) uint32_t cnt2[SMP_BINS2];
+    uint32_t n_loc;
     unsigned long long scan[SMP_WARPS + 1];
     unsigned long long total;           // this block's kept mass (read by the others)
     unsigned long long mass;            // mass up to and with the last kept token
     unsigned long long base_mass;
-    uint32_t cnt[SMP_BINS], mhi[SMP_BINS], mlo[SMP_BINS];
+    alignas(16) uint32_t cnt[SMP_BINS];
+    alignas(16) uint32_t mhi[SMP_BINS];
+    uint32_t mlo[SMP_BINS];  // directly behind mhi
     uint32_t wmin[SMP_WARPS], wmax[SMP_WARPS];
     uint32_t kmin, kmax;
     uint32_t n_cand;
     uint32_t lkey, lidx;  // the last kept token
-    float bmax;
-    int nan;
     int border, base_cnt, border_cnt;
     int token;
 };
@@ -83,6 +114,12 @@ __device__ __forceinline__ void st_cluster_u64(uint32_t addr, unsigned long long
     asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(addr), "l"(x) : "memory");
 }
 
+__device__ __forceinline__ uint4 ld_cluster_v4(uint32_t addr) {
+    uint4 v;
+    asm volatile("ld.shared::cluster.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
+    return v;
+}
+
 __device__ __forceinline__ unsigned long long warp_sum_u64(unsigned long long v) {
 #pragma unroll
     for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
@@ -95,6 +132,29 @@ template <>
 __device__ __forceinline__ float smp_load<float>(const float* s, int i) { return s[i] + 0.0f; }
 template <>
 __device__ __forceinline__ float smp_load<uint16_t>(const uint16_t* s, int i) { return bf2f(s[i]) + 0.0f; }
+
+template <typename T>
+__device__ __forceinline__ T smp_minus_inf();
+template <>
+__device__ __forceinline__ float smp_minus_inf<float>() { return -INFINITY; }
+template <>
+__device__ __forceinline__ uint16_t smp_minus_inf<uint16_t>() { return 0xff80; }
+
+// The values of a 16-byte piece.
+template <typename T>
+struct SmpPiece;
+template <>
+struct SmpPiece<float> {
+    static constexpr int N = 4;
+    static __device__ __forceinline__ void get(const uint4& w, float (&z)[4]) {
+        z[0] = __uint_as_float(w.x), z[1] = __uint_as_float(w.y), z[2] = __uint_as_float(w.z), z[3] = __uint_as_float(w.w);
+    }
+};
+template <>
+struct SmpPiece<uint16_t> {
+    static constexpr int N = 8;
+    static __device__ __forceinline__ void get(const uint4& w, float (&z)[8]) { unpack8(w, z); }
+};
 
 // What is kept, and with which weight.
 struct SampleFilter {
@@ -212,13 +272,499 @@ __device__ __forceinline__ unsigned long long share_of(float u, unsigned long lo
     return __umul64hi(total << 1, U);
 }
 
+// Descending bitonic sort of n2 (a power of two) values.
+__device__ __forceinline__ void sample_sort(unsigned long long* v, int n2) {
+    for (int size = 2; size <= n2; size <<= 1)
+        for (int stride = size >> 1; stride; stride >>= 1) {
+            for (int i = threadIdx.x; i < n2 / 2; i += SMP_THREADS) {
+                const int a = 2 * i - (i & (stride - 1)), b = a + stride;
+                const unsigned long long x = v[a], y = v[b];
+                if ((x < y) == ((a & size) == 0)) {
+                    v[a] = y;
+                    v[b] = x;
+                }
+            }
+            __syncthreads();
+        }
+}
+
+// Sum over lower threads, `all` over the block.  Two barriers.
+template <typename V>
+__device__ __forceinline__ V sample_before(V v, V* buf, V& all) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    V s = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const V y = __shfl_up_sync(0xffffffffu, s, o);
+        if (lane >= o) s += y;
+    }
+    __syncthreads();
+    if (lane == 31) buf[warp] = s;
+    __syncthreads();
+    V b = 0;
+    all = 0;
+    for (int w = 0; w < SMP_WARPS; ++w) {
+        const V t = buf[w];
+        if (w < warp) b += t;
+        all += t;
+    }
+    return b + s - v;
+}
+
+__device__ __forceinline__ float smp_unkey(uint32_t key) { return __uint_as_float((key & 0x80000000u) ? (key & 0x7fffffffu) : ~key); }
+
+// The two-sweep form; false (for the whole cluster) if the row does not fit it.  All blocks of the cluster leave together.
 template <typename T>
-__global__ void __launch_bounds__(SMP_THREADS) sample_kernel(const SampleParams p) {
+__device__ bool sample_fast(const SampleParams& p, SampleShared& sh, uint8_t* raw, int row, uint32_t rank, uint32_t cl, int len, int mis,
+                            int pieces, SampleFilter f, float scale, bool by_k, bool by_p, int k, float tp) {
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    constexpr int PER = SmpPiece<T>::N, BPT = 4, ROUNDS = SMP_SWEEP / PER;
+    const uint4* img = reinterpret_cast<const uint4*>(raw);
+    const uint32_t at = rank * (uint32_t)p.seg;
+    const float m = f.m;
+
+    if (f.greedy) {  // the lowest index of the largest logit
+        uint32_t best = 0xffffffffu;
+        for (int v = tid; v < pieces; v += SMP_THREADS) {
+            float z[PER];
+            SmpPiece<T>::get(img[v], z);
+#pragma unroll
+            for (int e = 0; e < PER; ++e)
+                if (z[e] == m) best = min(best, at + (uint32_t)(v * PER + e - mis));
+        }
+        best = __reduce_min_sync(0xffffffffu, best);
+        if (lane == 0) sh.wmin[warp] = best;
+        __syncthreads();
+        if (tid == 0) {
+            for (int w = 0; w < SMP_WARPS; ++w) best = min(best, sh.wmin[w]);
+            st_cluster_u32(mapa_shared(smem_u32(&sh.from[rank].first), 0), best);
+        }
+        cluster_sync();
+        if (rank == 0 && tid == 0) {
+            for (uint32_t r = 0; r < cl; ++r) best = min(best, sh.from[r].first);
+            p.out[row] = (int)best;
+        }
+        return true;
+    }
+
+    float above = INFINITY, inside = INFINITY;  // in bins: kept for certain below `above`, to be decided below `inside`
+    const float u = p.u[row];
+    if (by_k || by_p) {
+        // ---- first sweep: counts
+        for (int v = tid; v < pieces; v += SMP_THREADS) {
+            float z[PER];
+            SmpPiece<T>::get(img[v], z);
+#pragma unroll
+            for (int e = 0; e < PER; ++e) {
+                // floor by an addition that rounds toward zero
+                const float y = fminf(__fmul_rn(__fsub_rn(m, z[e]), scale), (float)(SMP_BINS - 1));
+                atomicAdd(&sh.cnt[__float_as_uint(__fadd_rz(y, 0x1p23f)) - 0x4b000000u], 1u);
+            }
+        }
+        cluster_sync();
+        uint32_t cnt[BPT] = {0, 0, 0, 0};  // threads behind the last bin have none
+        if (tid < SMP_BINS / BPT) {
+            const uint32_t a = smem_u32(&sh.cnt[tid * BPT]);
+            uint4 t[SMP_MAX_CLUSTER];
+#pragma unroll
+            for (uint32_t r = 0; r < SMP_MAX_CLUSTER; ++r) t[r] = r < cl ? ld_cluster_v4(mapa_shared(a, r)) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+            for (uint32_t r = 0; r < SMP_MAX_CLUSTER; ++r) cnt[0] += t[r].x, cnt[1] += t[r].y, cnt[2] += t[r].z, cnt[3] += t[r].w;
+        }
+        if (by_k) {
+            uint32_t here = 0, every;
+#pragma unroll
+            for (int x = 0; x < BPT; ++x) here += cnt[x];
+            uint32_t b = sample_before(here, sh.wmin, every);
+#pragma unroll
+            for (int x = 0; x < BPT; ++x) {
+                if (b < (uint32_t)k && (uint32_t)k <= b + cnt[x]) {
+                    sh.border = tid * BPT + x;
+                    sh.border_cnt = (int)(b + cnt[x]);
+                }
+                b += cnt[x];
+            }
+            __syncthreads();
+            const int border = sh.border, most = sh.border_cnt;
+            // the last bin has no lower end, and holds what lies outside the segments
+            if (border == SMP_BINS - 1 || most > SMP_LIST) {
+                cluster_sync();  // everybody has read the counts
+                for (int i = tid; i < SMP_BINS; i += SMP_THREADS) sh.cnt[i] = 0;
+                cluster_sync();
+                return false;
+            }
+            // ---- the tokens up to that bin go to the first block
+            const float limit = (float)(border + 1);
+            const uint32_t list = mapa_shared(smem_u32(sh.cand), 0), num = mapa_shared(smem_u32(&sh.n_cand), 0);
+            for (int v = tid; v < pieces; v += SMP_THREADS) {
+                float z[PER];
+                SmpPiece<T>::get(img[v], z);
+#pragma unroll
+                for (int e = 0; e < PER; ++e)
+                    if (__fmul_rn(__fsub_rn(m, z[e]), scale) < limit) {
+                        const uint32_t slot = atom_add_cluster_u32(num, 1u);
+                        const uint32_t idx = at + (uint32_t)(v * PER + e - mis);
+                        if (slot < SMP_LIST) st_cluster_u64(list + slot * 8, (unsigned long long)smp_key(z[e] + 0.0f) << 32 | (uint32_t)~idx);
+                    }
+            }
+            cluster_sync();
+            if (rank != 0) return true;
+            int n = min((int)sh.n_cand, SMP_LIST), n2 = 32;
+            while (n2 < n) n2 <<= 1;
+            for (int i = n + tid; i < n2; i += SMP_THREADS) sh.cand[i] = 0;
+            __syncthreads();
+            sample_sort(sh.cand, n2);
+            n = min(n, k);
+            constexpr int Q = SMP_LIST / SMP_THREADS;
+            unsigned long long c[Q], q[Q], v = 0, all, dummy;
+#pragma unroll
+            for (int x = 0; x < Q; ++x) {
+                const int i = tid * Q + x;
+                c[x] = q[x] = 0;
+                if (i < n) {
+                    c[x] = sh.cand[i];
+                    q[x] = f.units(smp_unkey((uint32_t)(c[x] >> 32)));
+                }
+                v += q[x];
+            }
+            unsigned long long b4 = sample_before(v, sh.scan, all);
+            if (by_p) {
+                bool rest;
+                unsigned long long lim = share_of(tp > 0.0f ? tp : 0.0f, all, rest);
+                if (rest) ++lim;
+                if (lim < 1) lim = 1;
+#pragma unroll
+                for (int x = 0; x < Q; ++x) {
+                    const unsigned long long e = b4 + q[x];
+                    if (b4 >= lim) q[x] = 0;  // mass before it has reached the share
+                    b4 = e;
+                }
+            }
+            // what stays, by index: index << 32 | units - 1, sorted descending on the complement
+            unsigned long long kept = 0;
+#pragma unroll
+            for (int x = 0; x < Q; ++x) {
+                const int i = tid * Q + x;
+                const float z = smp_unkey((uint32_t)(c[x] >> 32));
+                if (q[x] && z != m && f.weight(z) < f.min_w) q[x] = 0;
+                if (i < n2) sh.cand[i] = q[x] ? (c[x] & 0xffffffffull) << 32 | (q[x] - 1) : 0ull;
+                kept += q[x];
+            }
+            sample_before(kept, sh.scan, all);
+            bool rest;
+            unsigned long long target = share_of(u >= 0.0f ? fminf(u, 1.0f) : 0.0f, all, rest);
+            if (target >= all) target = all - 1;
+            __syncthreads();
+            sample_sort(sh.cand, n2);  // ~index descends: index ascends; empty places come last
+            v = 0;
+#pragma unroll
+            for (int x = 0; x < Q; ++x) {
+                const int i = tid * Q + x;
+                c[x] = i < n2 ? sh.cand[i] : 0ull;
+                q[x] = c[x] ? (c[x] & 0xffffffffull) + 1 : 0ull;
+                v += q[x];
+            }
+            b4 = sample_before(v, sh.scan, dummy);
+#pragma unroll
+            for (int x = 0; x < Q; ++x) {
+                if (b4 <= target && target < b4 + q[x]) p.out[row] = (int)~(uint32_t)(c[x] >> 32);
+                b4 += q[x];
+            }
+            return true;
+        }
+        // ---- top-p alone: a bracket of bins around the limit, from counts and the bins' middle weights
+        float mf[BPT], s1 = 0.0f, s2 = 0.0f, all1, all2;
+#pragma unroll
+        for (int x = 0; x < BPT; ++x) {
+            const float w = ex2_hw(-1.44269504f / 32.0f * ((float)(tid * BPT + x) + 0.5f));
+            mf[x] = __fmul_rn((float)cnt[x], w);
+            s1 += mf[x];
+            s2 += mf[x] * w;
+        }
+        float b = sample_before(s1, reinterpret_cast<float*>(sh.wmin), all1);
+        sample_before(s2, reinterpret_cast<float*>(sh.wmax), all2);
+        // a token's weight is off by up to 1.6 % of it, evenly spread (0.9 % rms): four deviations of the sum, and a
+        // little for weights that change across a bin; twice, for the mass up to the limit and for the row's
+        const float margin = 2.0f * (0.036f * sqrtf(all2) + 0.0005f * all1), want = fmaxf(tp, 0.0f) * all1;
+        if (tid == 0) {
+            sh.border = 0;
+            sh.border_cnt = SMP_BINS - 1;
+        }
+        __syncthreads();
+#pragma unroll
+        for (int x = 0; x < BPT; ++x) {
+            const float e = b + mf[x];
+            if (b < want - margin && e >= want - margin) sh.border = tid * BPT + x;
+            if (b < want + margin && e >= want + margin) sh.border_cnt = tid * BPT + x;
+            b = e;
+        }
+        __syncthreads();
+        above = (float)sh.border;
+        inside = (float)(sh.border_cnt + 1);
+        if (sh.border_cnt >= SMP_BINS - 1) inside = INFINITY;
+    }
+
+    // ---- second sweep: the sums
+    const float spread = (float)(SMP_BINS2 - 1) / (inside - above);  // bins of the second histogram per bin
+    unsigned long long total = 0, sure = 0, in = 0;
+    const int chunks = (pieces + SMP_THREADS * ROUNDS - 1) / (SMP_THREADS * ROUNDS);
+    const T* simg = reinterpret_cast<const T*>(raw);
+    auto bin_of = [&](float z) { return (int)(__fmul_rn(__fsub_rn(__fmul_rn(__fsub_rn(m, z), scale), above), spread)); };
+#pragma unroll 1
+    for (int c = 0; c < chunks; ++c) {
+        // weights below 2^-9: 2^32 w rounds to an integer in the addition of 2^23; 16 of them fit 27 bits.  Larger
+        // ones and those in the bracket (few) are set aside.
+        uint32_t s_all = 0, s_up = 0, s_kept = 0, aside = 0;
+#pragma unroll
+        for (int r = 0; r < ROUNDS; ++r) {
+            const int v = (c * ROUNDS + r) * SMP_THREADS + tid;
+            if (v < pieces) {
+                float z[PER];
+                SmpPiece<T>::get(img[v], z);
+#pragma unroll
+                for (int e = 0; e < PER; ++e) {
+                    const float x = __fsub_rn(z[e], m), w = ex2_hw(__fmul_rn(x, f.c)), y = __fmul_rn(x, -scale);
+                    const uint32_t q = __float_as_uint(__fmaf_rn(w, 0x1p32f, 0x1p23f)) - 0x4b000000u;
+                    const bool up = y < above, big = w >= 0x1p-9f, odd = big || (!up && y < inside);
+                    if (odd) aside |= 1u << (r * PER + e);
+                    if (!odd) s_all += q;
+                    if (up && !big) s_up += q;
+                    if (up && !big && w >= f.min_w) s_kept += q;
+                }
+            }
+        }
+        unsigned long long kept = 0;
+        while (aside) {
+            const int bit = __ffs((int)aside) - 1;
+            aside &= aside - 1;
+            const int j = ((c * ROUNDS + bit / PER) * SMP_THREADS + tid) * PER + bit % PER;
+            const float z = smp_load(simg, j), w = f.weight(z), y = __fmul_rn(__fsub_rn(m, z), scale);
+            const unsigned long long q = __float2ull_rn(__fmul_rn(w, 0x1p32f));
+            total += q;
+            if (y < above) {
+                sure += q;
+                if (w >= f.min_w || z == m) kept += q;
+            } else if (y < inside) {
+                if (q) {
+                    const uint32_t slot = atomicAdd(&sh.n_loc, 1u);
+                    if (slot < SMP_LIST) sh.loc[slot] = (uint32_t)j;
+                    const int bin = bin_of(z);
+                    atomicAdd(&sh.cnt2[bin], 1u);
+                    if (q >> 16) atomicAdd(&sh.mhi[bin], (uint32_t)(q >> 16));
+                    if (q & 0xffffu) atomicAdd(&sh.mlo[bin], (uint32_t)(q & 0xffffu));
+                    in += q;
+                }
+            }
+        }
+        // 32 lanes x 16 values below 2^23: below 2^32
+        unsigned long long t = __reduce_add_sync(0xffffffffu, s_kept);
+        if (__any_sync(0xffffffffu, kept != 0)) t += warp_sum_u64(kept);
+        if (lane == 0) sh.sweep[c][warp] = t;
+        total += s_all;
+        sure += s_up;
+    }
+    SampleFilter g = f;
+    if (by_p) {
+        total = warp_sum_u64(total);
+        sure = warp_sum_u64(sure);
+        in = warp_sum_u64(in);
+        if (lane == 0) {
+            sh.part[0][warp] = total;
+            sh.part[1][warp] = sure;
+            sh.part[2][warp] = in;
+        }
+        __syncthreads();
+        if (warp == 0) {
+            unsigned long long t[3];
+#pragma unroll
+            for (int x = 0; x < 3; ++x) t[x] = warp_sum_u64(lane < SMP_WARPS ? sh.part[x][lane] : 0ull);
+            if (lane < (int)cl) {
+                const uint32_t to = mapa_shared(smem_u32(&sh.from[rank]), lane);
+                st_cluster_u64(to, t[0]);
+                st_cluster_u64(to + 8, t[1]);
+                st_cluster_u64(to + 16, t[2]);
+                st_cluster_u32(mapa_shared(smem_u32(&sh.from[rank].lists), lane), sh.n_loc);
+            }
+        }
+        cluster_sync();
+        total = sure = in = 0;
+        bool fits = true;
+        for (uint32_t r = 0; r < cl; ++r) {
+            total += sh.from[r].total;
+            sure += sh.from[r].above;
+            in += sh.from[r].in;
+            fits &= sh.from[r].lists <= SMP_LIST;
+        }
+        bool rest;
+        unsigned long long limit = share_of(tp > 0.0f ? tp : 0.0f, total, rest);
+        if (rest) ++limit;
+        if (limit < 1) limit = 1;
+        fits &= sure < limit && limit <= sure + in;
+        if (fits) {
+            uint32_t cn[BPT] = {0, 0, 0, 0};
+            unsigned long long ms[BPT] = {0, 0, 0, 0}, all;
+            if (tid < SMP_BINS2 / BPT) {
+                const uint32_t a0 = smem_u32(&sh.cnt2[tid * BPT]), a1 = smem_u32(&sh.mhi[tid * BPT]), a2 = smem_u32(&sh.mlo[tid * BPT]);
+#pragma unroll
+                for (uint32_t r = 0; r < SMP_MAX_CLUSTER; ++r)
+                    if (r < cl) {
+                        const uint4 t0 = ld_cluster_v4(mapa_shared(a0, r)), t1 = ld_cluster_v4(mapa_shared(a1, r)), t2 = ld_cluster_v4(mapa_shared(a2, r));
+                        cn[0] += t0.x, cn[1] += t0.y, cn[2] += t0.z, cn[3] += t0.w;
+                        ms[0] += ((unsigned long long)t1.x << 16) + t2.x, ms[1] += ((unsigned long long)t1.y << 16) + t2.y;
+                        ms[2] += ((unsigned long long)t1.z << 16) + t2.z, ms[3] += ((unsigned long long)t1.w << 16) + t2.w;
+                    }
+            }
+            unsigned long long b = sure + sample_before(ms[0] + ms[1] + ms[2] + ms[3], sh.scan, all);
+#pragma unroll
+            for (int x = 0; x < BPT; ++x) {
+                if (b < limit && limit <= b + ms[x]) {
+                    sh.border = tid * BPT + x;
+                    sh.border_cnt = (int)cn[x];
+                    sh.base_mass = b;
+                }
+                b += ms[x];
+            }
+            __syncthreads();
+            fits = sh.border_cnt <= SMP_CAND;
+        }
+        if (!fits) {  // the same in every block
+            cluster_sync();
+            for (int i = tid; i < SMP_BINS; i += SMP_THREADS) sh.cnt[i] = sh.mhi[i] = sh.mlo[i] = 0;
+            cluster_sync();
+            return false;
+        }
+        // the border bin's tokens, to every block; each finds the last one that stays
+        const int border = sh.border, mine = (int)sh.n_loc;
+        for (int i = tid; i < mine; i += SMP_THREADS) {
+            const float z = smp_load(simg, (int)sh.loc[i]);
+            if (bin_of(z) == border) {
+                const uint32_t idx = at + sh.loc[i] - (uint32_t)mis;
+                for (uint32_t r = 0; r < cl; ++r) {
+                    const uint32_t slot = atom_add_cluster_u32(mapa_shared(smem_u32(&sh.n_cand), r), 1u);
+                    if (slot < SMP_CAND)
+                        st_cluster_u64(mapa_shared(smem_u32(sh.border_list), r) + slot * 8, (unsigned long long)smp_key(z) << 32 | (uint32_t)~idx);
+                }
+            }
+        }
+        cluster_sync();
+        const int n = min((int)sh.n_cand, SMP_CAND);
+        unsigned long long* units = reinterpret_cast<unsigned long long*>(sh.mhi);  // [SMP_CAND]: the bins have been read
+        static_assert(sizeof(sh.mhi) + sizeof(sh.mlo) >= SMP_CAND * 8, "units of the border bin");
+        for (int i = tid; i < n; i += SMP_THREADS) units[i] = f.units(smp_unkey((uint32_t)(sh.border_list[i] >> 32)));
+        __syncthreads();
+        for (int i = tid; i < n; i += SMP_THREADS) {
+            const unsigned long long me = sh.border_list[i];
+            unsigned long long b = sh.base_mass;
+            for (int j = 0; j < n; ++j)
+                if (sh.border_list[j] > me) b += units[j];
+            if (b < limit && limit <= b + units[i]) {
+                sh.lkey = (uint32_t)(me >> 32);
+                sh.lidx = ~(uint32_t)me;
+            }
+        }
+        __syncthreads();
+        g.lkey = sh.lkey;
+        g.lidx = sh.lidx;
+        for (int i = tid; i < mine; i += SMP_THREADS) {
+            const uint32_t j = sh.loc[i];
+            const unsigned long long q = g.kept(smp_load(simg, (int)j), at + j - (uint32_t)mis);
+            if (q) atomicAdd(&sh.extra[j / (SMP_THREADS * SMP_SWEEP)], q);
+        }
+    }
+
+    // ---- the choice: the chunk, the round and warp, the lane, the token
+    __syncthreads();
+    unsigned long long sum = 0;
+    for (int c = warp; c < chunks; c += SMP_WARPS) {
+        const unsigned long long t = warp_sum_u64(lane < SMP_WARPS ? sh.sweep[c][lane] : 0ull) + sh.extra[c];
+        if (lane == 0) sh.extra[c] = t;
+        sum += t;
+    }
+    if (lane == 0) sh.scan[warp] = sum;
+    __syncthreads();
+    if (tid < (int)cl) {
+        sum = 0;
+        for (int w = 0; w < SMP_WARPS; ++w) sum += sh.scan[w];
+        st_cluster_u64(mapa_shared(smem_u32(&sh.from[rank].kept), tid), sum);
+    }
+    cluster_sync();  // the last access to another block's memory lies before this
+    unsigned long long before = 0, all = 0, own = 0;
+    for (uint32_t r = 0; r < cl; ++r) {
+        const unsigned long long t = sh.from[r].kept;
+        if (r < rank) before += t;
+        if (r == rank) own = t;
+        all += t;
+    }
+    bool rest;
+    unsigned long long target = share_of(u >= 0.0f ? fminf(u, 1.0f) : 0.0f, all, rest);
+    if (target >= all) target = all - 1;
+    if (target >= before && target - before < own) {  // the same for the whole block
+        unsigned long long left = target - before;
+        int c = 0;
+        for (; left >= sh.extra[c]; ++c) left -= sh.extra[c];
+        unsigned long long mine[ROUNDS];
+#pragma unroll
+        for (int r = 0; r < ROUNDS; ++r) {
+            const int v = (c * ROUNDS + r) * SMP_THREADS + tid;
+            mine[r] = 0;
+            if (v < pieces) {
+                float z[PER];
+                SmpPiece<T>::get(img[v], z);
+#pragma unroll
+                for (int e = 0; e < PER; ++e) mine[r] += g.kept(z[e] + 0.0f, at + (uint32_t)(v * PER + e - mis));
+            }
+            const unsigned long long t = warp_sum_u64(mine[r]);
+            if (lane == 0) sh.wsum[r][warp] = t;
+        }
+        __syncthreads();
+        int rr = 0, ww = 0;
+        while (left >= sh.wsum[rr][ww]) {
+            left -= sh.wsum[rr][ww];
+            if (++ww == SMP_WARPS) {
+                ww = 0;
+                ++rr;
+            }
+        }
+        if (warp == ww) {
+            unsigned long long x = 0;
+#pragma unroll
+            for (int r = 0; r < ROUNDS; ++r)
+                if (r == rr) x = mine[r];
+            unsigned long long e = x;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const unsigned long long y = __shfl_up_sync(0xffffffffu, e, o);
+                if (lane >= o) e += y;
+            }
+            if (e - x <= left && left < e) {
+                left -= e - x;
+                const int v = (c * ROUNDS + rr) * SMP_THREADS + tid;
+                float z[PER];
+                SmpPiece<T>::get(img[v], z);
+                int token = -1;
+#pragma unroll
+                for (int i = 0; i < PER; ++i) {
+                    const uint32_t idx = at + (uint32_t)(v * PER + i - mis);
+                    const unsigned long long q = g.kept(z[i] + 0.0f, idx);
+                    if (token < 0 && left < q) token = (int)idx;
+                    if (token < 0) left -= q;
+                }
+                p.out[row] = token;
+            }
+        }
+    }
+    return true;
+}
+
+template <typename T>
+__global__ void __launch_bounds__(SMP_THREADS, 2) sample_kernel(const SampleParams p) {
     extern __shared__ __align__(16) uint8_t raw[];
     __shared__ SampleShared sh;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     uint32_t rank = cluster_rank(), cl;
     asm volatile("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(cl));
+    // another block's memory may be written once that block runs: waited for before the first push
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
     const int row = blockIdx.x / cl;
     const long long at = (long long)rank * p.seg;
     const int len = (int)(p.vocab - at < p.seg ? (p.vocab > at ? p.vocab - at : 0) : p.seg);
@@ -229,10 +775,10 @@ __global__ void __launch_bounds__(SMP_THREADS) sample_kernel(const SampleParams 
     const int mis = (int)((reinterpret_cast<uintptr_t>(g) & 15) / sizeof(T));
     T* simg = reinterpret_cast<T*>(raw);
     const T* s = simg + mis;
+    const int pieces = len > 0 ? (mis + len + PER - 1) / PER : 0;
     float m = -INFINITY;
     bool nan = false;
     if (len > 0) {
-        const int pieces = (mis + len + PER - 1) / PER;
         const uint4* ga = reinterpret_cast<const uint4*>(g - mis);
         constexpr int UN = 4;
         for (int base = 0; base < pieces; base += SMP_THREADS * UN) {
@@ -249,21 +795,23 @@ __global__ void __launch_bounds__(SMP_THREADS) sample_kernel(const SampleParams 
                 const int v = base + x * SMP_THREADS + tid;
                 if (whole[x]) {
                     reinterpret_cast<uint4*>(raw)[v] = w[x];
-                } else if (v < pieces) {
+                } else if (v < pieces) {  // what is not of this segment reads as -inf
                     for (int e = 0; e < PER; ++e) {
                         const int i = v * PER + e;
                         if (i >= mis && i < mis + len) simg[i] = g[i - mis];
+                        else simg[i] = smp_minus_inf<T>();
+                    }
+                    w[x] = reinterpret_cast<const uint4*>(raw)[v];
+                }
+                if (v < pieces) {
+                    float z[PER];
+                    SmpPiece<T>::get(w[x], z);
+#pragma unroll
+                    for (int e = 0; e < PER; ++e) {
+                        nan |= z[e] != z[e];
+                        m = fmaxf(m, z[e]);
                     }
                 }
-                if (v < pieces)
-                    for (int e = 0; e < PER; ++e) {
-                        const int i = v * PER + e;
-                        if (i >= mis && i < mis + len) {
-                            const float z = smp_load(simg, i);
-                            nan |= z != z;
-                            m = fmaxf(m, z);
-                        }
-                    }
             }
         }
     }
@@ -272,18 +820,21 @@ __global__ void __launch_bounds__(SMP_THREADS) sample_kernel(const SampleParams 
         for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
         if (lane == 0) sh.wmax[warp] = __float_as_uint(m);
         nan = __syncthreads_or(nan);
-        if (tid == 0) {
-            for (int w = 0; w < SMP_WARPS; ++w) m = fmaxf(m, __uint_as_float(sh.wmax[w]));
-            sh.bmax = m;
-            sh.nan = nan;
-            sh.n_cand = 0;
-        }
+        if (tid == 0) sh.n_cand = sh.n_loc = 0;
         for (int i = tid; i < SMP_BINS; i += SMP_THREADS) sh.cnt[i] = sh.mhi[i] = sh.mlo[i] = 0;
+        if (tid < SMP_BINS2) sh.cnt2[tid] = 0;
+        if (tid < SMP_SWEEP_CHUNKS) sh.extra[tid] = 0;
+        asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+        if (tid < (int)cl) {
+            for (int w = 0; w < SMP_WARPS; ++w) m = fmaxf(m, __uint_as_float(sh.wmax[w]));
+            st_cluster_u32(mapa_shared(smem_u32(&sh.from[rank].max), tid), __float_as_uint(m));
+            st_cluster_u32(mapa_shared(smem_u32(&sh.from[rank].nan), tid), nan);
+        }
         cluster_sync();
         m = -INFINITY;
         for (uint32_t r = 0; r < cl; ++r) {
-            m = fmaxf(m, __uint_as_float(ld_cluster_u32(mapa_shared(smem_u32(&sh.bmax), r))));
-            nan |= ld_cluster_u32(mapa_shared(smem_u32(&sh.nan), r)) != 0;
+            m = fmaxf(m, sh.from[r].max);
+            nan |= sh.from[r].nan != 0;
         }
     }
     if (nan || m == -INFINITY) {  // nothing to choose from
@@ -291,7 +842,6 @@ __global__ void __launch_bounds__(SMP_THREADS) sample_kernel(const SampleParams 
             p.out[row] = -1;
             if (nan) set_error(TBIK_ERR_VALUE);
         }
-        cluster_sync();
         return;
     }
     const float temp = p.temperature ? p.temperature[row] : 1.0f;
@@ -308,8 +858,14 @@ __global__ void __launch_bounds__(SMP_THREADS) sample_kernel(const SampleParams 
     const bool by_k = !f.greedy && k > 0 && k < p.vocab;
     const bool by_p = !f.greedy && tp < 1.0f;
     int token;
+    {
+        const float scale = f.greedy ? 1.0f : __fdiv_rn(32.0f, temp);
+        if (m < INFINITY && scale < 1e30f && scale > 1e-30f &&
+            sample_fast<T>(p, sh, raw, row, rank, cl, len, mis, pieces, f, scale, by_k, by_p, k, tp))
+            return;
+    }
     if (by_k || by_p) {
-        // histogram over linear bins of (m - z) / temperature, 32 of them to a unit
+        // the general steps: histogram over linear bins of (m - z) / temperature, 32 of them to a unit
         const float scale = __fdiv_rn(32.0f, temp);
         auto bin0 = [&](float z) { return min(SMP_BINS - 1, z == m ? 0 : __float2int_rz(__fmul_rn(__fsub_rn(m, z), scale))); };
         auto add = [&](int b, unsigned long long q) {
