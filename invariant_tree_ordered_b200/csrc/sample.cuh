@@ -36,6 +36,7 @@ constexpr int SMP_CHUNK = SMP_THREADS * SMP_CHUNK_ROUNDS;
 constexpr int SMP_MAX_SEG = 12 * SMP_CHUNK;  // tokens per block
 constexpr int SMP_MAX_CLUSTER = 8;
 constexpr int SMP_BINS2 = 256;         // of the second histogram
+constexpr int SMP_BORDER = 128;        // tokens of its border bin, from each block
 constexpr int SMP_LIST = 2048;         // tokens of a top-k set that one block sorts; tokens of a bracket per block
 constexpr int SMP_SWEEP = 16;          // tokens per thread and chunk of the second sweep
 constexpr int SMP_SWEEP_CHUNKS = (SMP_MAX_SEG + 16) / (SMP_THREADS * SMP_SWEEP) + 1;
@@ -60,7 +61,7 @@ struct SampleShared {
         unsigned long long wsum[SMP_CHUNK_ROUNDS][SMP_WARPS];  // of the chosen chunk, when the lists are done with
         unsigned long long cand[SMP_LIST];  // key << 32 | ~index: descending order is the order of the tokens
         struct {
-            unsigned long long border_list[SMP_CAND];
+            unsigned long long border_list[SMP_MAX_CLUSTER][SMP_BORDER];
             uint32_t loc[SMP_LIST];         // this block's tokens in the bracket
         };
     };
@@ -69,10 +70,9 @@ struct SampleShared {
     struct {
         unsigned long long total, above, in, kept;
         float max;
-        uint32_t nan, first, lists;
+        uint32_t nan, first, lists, border;
     } from[SMP_MAX_CLUSTER];
     unsigned long long part[3][SMP_WARPS];
-    alignas(16) uint32_t cnt2[SMP_BINS2];
     uint32_t n_loc;
     unsigned long long scan[SMP_WARPS + 1];
     unsigned long long total;           // this block's kept mass (read by the others)
@@ -265,27 +265,14 @@ __device__ __forceinline__ unsigned long long sample_select(const T* s, int len,
     return all;
 }
 
-// u * total as (floor, whether something is left over), u in [0, 1].
+// u * total as (floor, whether something is left over), u in [0, 1], total < 2^63.
 __device__ __forceinline__ unsigned long long share_of(float u, unsigned long long total, bool& rest) {
-    const unsigned long long U = __double2ull_rz((double)u * 9223372036854775808.0);  // exact
+    const uint32_t bits = __float_as_uint(u);
+    const int shift = (int)(bits >> 23) - 127 + 40;  // U = floor(2^63 u)
+    const unsigned long long mant = (bits & 0x7fffffu) | 0x800000u;
+    const unsigned long long U = shift >= 0 ? mant << shift : shift > -24 ? mant >> -shift : 0ull;
     rest = ((total << 1) * U) != 0;
     return __umul64hi(total << 1, U);
-}
-
-// Descending bitonic sort of n2 (a power of two) values.
-__device__ __forceinline__ void sample_sort(unsigned long long* v, int n2) {
-    for (int size = 2; size <= n2; size <<= 1)
-        for (int stride = size >> 1; stride; stride >>= 1) {
-            for (int i = threadIdx.x; i < n2 / 2; i += SMP_THREADS) {
-                const int a = 2 * i - (i & (stride - 1)), b = a + stride;
-                const unsigned long long x = v[a], y = v[b];
-                if ((x < y) == ((a & size) == 0)) {
-                    v[a] = y;
-                    v[b] = x;
-                }
-            }
-            __syncthreads();
-        }
 }
 
 // Sum over lower threads, `all` over the block.  Two barriers.
@@ -382,6 +369,7 @@ __device__ bool sample_fast(const SampleParams& p, SampleShared& sh, uint8_t* ra
                     sh.border = tid * BPT + x;
                     sh.border_cnt = (int)(b + cnt[x]);
                 }
+                if (tid < SMP_BINS / BPT) sh.mhi[tid * BPT + x] = b;  // the bin's first place
                 b += cnt[x];
             }
             __syncthreads();
@@ -389,34 +377,52 @@ __device__ bool sample_fast(const SampleParams& p, SampleShared& sh, uint8_t* ra
             // the last bin has no lower end, and holds what lies outside the segments
             if (border == SMP_BINS - 1 || most > SMP_LIST) {
                 cluster_sync();  // everybody has read the counts
-                for (int i = tid; i < SMP_BINS; i += SMP_THREADS) sh.cnt[i] = 0;
+                for (int i = tid; i < SMP_BINS; i += SMP_THREADS) sh.cnt[i] = sh.mhi[i] = 0;
                 cluster_sync();
                 return false;
             }
-            // ---- the tokens up to that bin go to the first block
+            // ---- the tokens up to that bin go to the first block, each bin's to its place
             const float limit = (float)(border + 1);
-            const uint32_t list = mapa_shared(smem_u32(sh.cand), 0), num = mapa_shared(smem_u32(&sh.n_cand), 0);
+            const uint32_t list = mapa_shared(smem_u32(sh.cand), 0), num = mapa_shared(smem_u32(sh.mlo), 0);
+            auto bin0 = [&](float z) { return (int)__fmul_rn(__fsub_rn(m, z), scale); };
             for (int v = tid; v < pieces; v += SMP_THREADS) {
                 float z[PER];
                 SmpPiece<T>::get(img[v], z);
 #pragma unroll
                 for (int e = 0; e < PER; ++e)
                     if (__fmul_rn(__fsub_rn(m, z[e]), scale) < limit) {
-                        const uint32_t slot = atom_add_cluster_u32(num, 1u);
+                        const int bin = bin0(z[e]);
+                        const uint32_t slot = sh.mhi[bin] + atom_add_cluster_u32(num + 4 * bin, 1u);
                         const uint32_t idx = at + (uint32_t)(v * PER + e - mis);
                         if (slot < SMP_LIST) st_cluster_u64(list + slot * 8, (unsigned long long)smp_key(z[e] + 0.0f) << 32 | (uint32_t)~idx);
                     }
             }
             cluster_sync();
             if (rank != 0) return true;
-            int n = min((int)sh.n_cand, SMP_LIST), n2 = 32;
-            while (n2 < n) n2 <<= 1;
-            for (int i = n + tid; i < n2; i += SMP_THREADS) sh.cand[i] = 0;
-            __syncthreads();
-            sample_sort(sh.cand, n2);
-            n = min(n, k);
+            // a token's place: its bin's first, and the larger ones in the bin
             constexpr int Q = SMP_LIST / SMP_THREADS;
-            unsigned long long c[Q], q[Q], v = 0, all, dummy;
+            unsigned long long c[Q], q[Q];
+            int place[Q];
+#pragma unroll
+            for (int x = 0; x < Q; ++x) {
+                const int i = x * SMP_THREADS + tid;
+                place[x] = -1;
+                if (i < most) {
+                    c[x] = sh.cand[i];
+                    const int bin = bin0(smp_unkey((uint32_t)(c[x] >> 32)));
+                    const int lo = (int)sh.mhi[bin], hi = lo + (int)sh.mlo[bin];
+                    place[x] = lo;
+                    for (int j = lo; j < hi; ++j) place[x] += sh.cand[j] > c[x];
+                }
+            }
+            __syncthreads();
+#pragma unroll
+            for (int x = 0; x < Q; ++x)
+                if (place[x] >= 0) sh.cand[place[x]] = c[x];
+            for (int i = tid; i < SMP_BINS; i += SMP_THREADS) sh.cnt[i] = sh.mhi[i] = sh.mlo[i] = 0;
+            __syncthreads();
+            const int n = min(most, k);
+            unsigned long long v = 0, all;
 #pragma unroll
             for (int x = 0; x < Q; ++x) {
                 const int i = tid * Q + x;
@@ -440,35 +446,58 @@ __device__ bool sample_fast(const SampleParams& p, SampleShared& sh, uint8_t* ra
                     b4 = e;
                 }
             }
-            // what stays, by index: index << 32 | units - 1, sorted descending on the complement
-            unsigned long long kept = 0;
-#pragma unroll
-            for (int x = 0; x < Q; ++x) {
-                const int i = tid * Q + x;
-                const float z = smp_unkey((uint32_t)(c[x] >> 32));
-                if (q[x] && z != m && f.weight(z) < f.min_w) q[x] = 0;
-                if (i < n2) sh.cand[i] = q[x] ? (c[x] & 0xffffffffull) << 32 | (q[x] - 1) : 0ull;
-                kept += q[x];
-            }
-            sample_before(kept, sh.scan, all);
-            bool rest;
-            unsigned long long target = share_of(u >= 0.0f ? fminf(u, 1.0f) : 0.0f, all, rest);
-            if (target >= all) target = all - 1;
-            __syncthreads();
-            sample_sort(sh.cand, n2);  // ~index descends: index ascends; empty places come last
+            // what stays, in a histogram of masses over the indices
+            int shift = 0;
+            while ((p.vocab - 1) >> shift >= SMP_BINS) ++shift;
             v = 0;
 #pragma unroll
             for (int x = 0; x < Q; ++x) {
-                const int i = tid * Q + x;
-                c[x] = i < n2 ? sh.cand[i] : 0ull;
-                q[x] = c[x] ? (c[x] & 0xffffffffull) + 1 : 0ull;
-                v += q[x];
+                const float z = smp_unkey((uint32_t)(c[x] >> 32));
+                if (q[x] && z != m && f.weight(z) < f.min_w) q[x] = 0;
+                if (q[x]) {
+                    const int bin = (int)(~(uint32_t)c[x] >> shift);
+                    atomicAdd(&sh.mhi[bin], (uint32_t)(q[x] >> 16));
+                    atomicAdd(&sh.mlo[bin], (uint32_t)(q[x] & 0xffffu));
+                }
             }
-            b4 = sample_before(v, sh.scan, dummy);
+            __syncthreads();
+            unsigned long long ms[2];
 #pragma unroll
-            for (int x = 0; x < Q; ++x) {
-                if (b4 <= target && target < b4 + q[x]) p.out[row] = (int)~(uint32_t)(c[x] >> 32);
-                b4 += q[x];
+            for (int x = 0; x < 2; ++x) {
+                ms[x] = ((unsigned long long)sh.mhi[tid * 2 + x] << 16) + sh.mlo[tid * 2 + x];
+                v += ms[x];
+            }
+            b4 = sample_before(v, sh.scan, all);
+            bool rest;
+            unsigned long long target = share_of(u >= 0.0f ? fminf(u, 1.0f) : 0.0f, all, rest);
+            if (target >= all) target = all - 1;
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                if (b4 <= target && target < b4 + ms[x]) {
+                    sh.border = tid * 2 + x;
+                    sh.base_mass = b4;
+                }
+                b4 += ms[x];
+            }
+            __syncthreads();
+            // its tokens, and the one at which the running sum passes the target
+            unsigned long long* units = reinterpret_cast<unsigned long long*>(sh.mhi);  // [SMP_CAND], the bins are read
+            unsigned int* fill = &sh.n_loc;
+#pragma unroll
+            for (int x = 0; x < Q; ++x)
+                if (q[x] && (int)(~(uint32_t)c[x] >> shift) == sh.border) {
+                    const uint32_t slot = atomicAdd(fill, 1u);  // a bin has at most 2^shift tokens: 512
+                    sh.cnt[slot] = ~(uint32_t)c[x];
+                    units[slot] = q[x];
+                }
+            __syncthreads();
+            const int few = (int)sh.n_loc;
+            for (int i = tid; i < few; i += SMP_THREADS) {
+                const uint32_t idx = sh.cnt[i];
+                unsigned long long b = sh.base_mass;
+                for (int j = 0; j < few; ++j)
+                    if (sh.cnt[j] < idx) b += units[j];
+                if (b <= target && target < b + units[i]) p.out[row] = (int)idx;
             }
             return true;
         }
@@ -514,7 +543,7 @@ __device__ bool sample_fast(const SampleParams& p, SampleShared& sh, uint8_t* ra
     for (int c = 0; c < chunks; ++c) {
         // weights below 2^-9: 2^32 w rounds to an integer in the addition of 2^23; 16 of them fit 27 bits.  Larger
         // ones and those in the bracket (few) are set aside.
-        uint32_t s_all = 0, s_up = 0, s_kept = 0, aside = 0;
+        uint32_t s_all = 0, s_up = 0, s_kept = 0, large = 0, between = 0;
 #pragma unroll
         for (int r = 0; r < ROUNDS; ++r) {
             const int v = (c * ROUNDS + r) * SMP_THREADS + tid;
@@ -525,35 +554,44 @@ __device__ bool sample_fast(const SampleParams& p, SampleShared& sh, uint8_t* ra
                 for (int e = 0; e < PER; ++e) {
                     const float x = __fsub_rn(z[e], m), w = ex2_hw(__fmul_rn(x, f.c)), y = __fmul_rn(x, -scale);
                     const uint32_t q = __float_as_uint(__fmaf_rn(w, 0x1p32f, 0x1p23f)) - 0x4b000000u;
-                    const bool up = y < above, big = w >= 0x1p-9f, odd = big || (!up && y < inside);
-                    if (odd) aside |= 1u << (r * PER + e);
-                    if (!odd) s_all += q;
+                    const bool up = y < above, mid = !up && y < inside && q, big = !mid && w >= 0x1p-9f;
+                    if (mid) between |= 1u << (r * PER + e);
+                    if (big) large |= 1u << (r * PER + e);
+                    if (!mid && !big) s_all += q;
                     if (up && !big) s_up += q;
                     if (up && !big && w >= f.min_w) s_kept += q;
                 }
             }
         }
+        auto place = [&](int bit) { return ((c * ROUNDS + bit / PER) * SMP_THREADS + tid) * PER + bit % PER; };
         unsigned long long kept = 0;
-        while (aside) {
-            const int bit = __ffs((int)aside) - 1;
-            aside &= aside - 1;
-            const int j = ((c * ROUNDS + bit / PER) * SMP_THREADS + tid) * PER + bit % PER;
-            const float z = smp_load(simg, j), w = f.weight(z), y = __fmul_rn(__fsub_rn(m, z), scale);
+        while (large) {
+            const int bit = __ffs((int)large) - 1;
+            large &= large - 1;
+            const float z = smp_load(simg, place(bit)), w = f.weight(z);
             const unsigned long long q = __float2ull_rn(__fmul_rn(w, 0x1p32f));
             total += q;
-            if (y < above) {
+            if (__fmul_rn(__fsub_rn(m, z), scale) < above) {
                 sure += q;
                 if (w >= f.min_w || z == m) kept += q;
-            } else if (y < inside) {
-                if (q) {
-                    const uint32_t slot = atomicAdd(&sh.n_loc, 1u);
-                    if (slot < SMP_LIST) sh.loc[slot] = (uint32_t)j;
-                    const int bin = bin_of(z);
-                    atomicAdd(&sh.cnt2[bin], 1u);
-                    if (q >> 16) atomicAdd(&sh.mhi[bin], (uint32_t)(q >> 16));
-                    if (q & 0xffffu) atomicAdd(&sh.mlo[bin], (uint32_t)(q & 0xffffu));
-                    in += q;
-                }
+            }
+        }
+        if (__any_sync(0xffffffffu, between)) {  // one reservation for the warp
+            const uint32_t count = __popc(between);
+            uint32_t upto = count;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const uint32_t y = __shfl_up_sync(0xffffffffu, upto, o);
+                if (lane >= o) upto += y;
+            }
+            uint32_t first = 0;
+            if (lane == 31) first = atomicAdd(&sh.n_loc, upto);
+            first = __shfl_sync(0xffffffffu, first, 31) + upto - count;
+            while (between) {
+                const int bit = __ffs((int)between) - 1;
+                between &= between - 1;
+                if (first < SMP_LIST) sh.loc[first] = (uint32_t)place(bit);
+                ++first;
             }
         }
         // 32 lanes x 16 values below 2^23: below 2^32
@@ -565,6 +603,17 @@ __device__ bool sample_fast(const SampleParams& p, SampleShared& sh, uint8_t* ra
     }
     SampleFilter g = f;
     if (by_p) {
+        __syncthreads();
+        const int mine = min((int)sh.n_loc, SMP_LIST);
+        for (int i = tid; i < mine; i += SMP_THREADS) {
+            const float z = smp_load(simg, (int)sh.loc[i]);
+            const unsigned long long q = f.units(z);
+            const int bin = bin_of(z);
+            if (q >> 16) atomicAdd(&sh.mhi[bin], (uint32_t)(q >> 16));
+            if (q & 0xffffu) atomicAdd(&sh.mlo[bin], (uint32_t)(q & 0xffffu));
+            in += q;
+        }
+        total += in;
         total = warp_sum_u64(total);
         sure = warp_sum_u64(sure);
         in = warp_sum_u64(in);
@@ -601,31 +650,33 @@ __device__ bool sample_fast(const SampleParams& p, SampleShared& sh, uint8_t* ra
         if (limit < 1) limit = 1;
         fits &= sure < limit && limit <= sure + in;
         if (fits) {
-            uint32_t cn[BPT] = {0, 0, 0, 0};
             unsigned long long ms[BPT] = {0, 0, 0, 0}, all;
             if (tid < SMP_BINS2 / BPT) {
-                const uint32_t a0 = smem_u32(&sh.cnt2[tid * BPT]), a1 = smem_u32(&sh.mhi[tid * BPT]), a2 = smem_u32(&sh.mlo[tid * BPT]);
+                const uint32_t a1 = smem_u32(&sh.mhi[tid * BPT]), a2 = smem_u32(&sh.mlo[tid * BPT]);
+                uint4 t[SMP_MAX_CLUSTER];
+                auto pull = [&](uint32_t a) {
 #pragma unroll
-                for (uint32_t r = 0; r < SMP_MAX_CLUSTER; ++r)
-                    if (r < cl) {
-                        const uint4 t0 = ld_cluster_v4(mapa_shared(a0, r)), t1 = ld_cluster_v4(mapa_shared(a1, r)), t2 = ld_cluster_v4(mapa_shared(a2, r));
-                        cn[0] += t0.x, cn[1] += t0.y, cn[2] += t0.z, cn[3] += t0.w;
-                        ms[0] += ((unsigned long long)t1.x << 16) + t2.x, ms[1] += ((unsigned long long)t1.y << 16) + t2.y;
-                        ms[2] += ((unsigned long long)t1.z << 16) + t2.z, ms[3] += ((unsigned long long)t1.w << 16) + t2.w;
-                    }
+                    for (uint32_t r = 0; r < SMP_MAX_CLUSTER; ++r) t[r] = r < cl ? ld_cluster_v4(mapa_shared(a, r)) : make_uint4(0, 0, 0, 0);
+                };
+                pull(a1);
+#pragma unroll
+                for (uint32_t r = 0; r < SMP_MAX_CLUSTER; ++r) ms[0] += t[r].x, ms[1] += t[r].y, ms[2] += t[r].z, ms[3] += t[r].w;
+#pragma unroll
+                for (int x = 0; x < BPT; ++x) ms[x] <<= 16;
+                pull(a2);
+#pragma unroll
+                for (uint32_t r = 0; r < SMP_MAX_CLUSTER; ++r) ms[0] += t[r].x, ms[1] += t[r].y, ms[2] += t[r].z, ms[3] += t[r].w;
             }
             unsigned long long b = sure + sample_before(ms[0] + ms[1] + ms[2] + ms[3], sh.scan, all);
 #pragma unroll
             for (int x = 0; x < BPT; ++x) {
                 if (b < limit && limit <= b + ms[x]) {
                     sh.border = tid * BPT + x;
-                    sh.border_cnt = (int)cn[x];
                     sh.base_mass = b;
                 }
                 b += ms[x];
             }
             __syncthreads();
-            fits = sh.border_cnt <= SMP_CAND;
         }
         if (!fits) {  // the same in every block
             cluster_sync();
@@ -634,29 +685,44 @@ __device__ bool sample_fast(const SampleParams& p, SampleShared& sh, uint8_t* ra
             return false;
         }
         // the border bin's tokens, to every block; each finds the last one that stays
-        const int border = sh.border, mine = (int)sh.n_loc;
+        const int border = sh.border;
+        if (tid == 0) sh.n_cand = 0;
+        __syncthreads();
         for (int i = tid; i < mine; i += SMP_THREADS) {
             const float z = smp_load(simg, (int)sh.loc[i]);
             if (bin_of(z) == border) {
-                const uint32_t idx = at + sh.loc[i] - (uint32_t)mis;
-                for (uint32_t r = 0; r < cl; ++r) {
-                    const uint32_t slot = atom_add_cluster_u32(mapa_shared(smem_u32(&sh.n_cand), r), 1u);
-                    if (slot < SMP_CAND)
-                        st_cluster_u64(mapa_shared(smem_u32(sh.border_list), r) + slot * 8, (unsigned long long)smp_key(z) << 32 | (uint32_t)~idx);
-                }
+                const uint32_t idx = at + sh.loc[i] - (uint32_t)mis, slot = atomicAdd(&sh.n_cand, 1u);
+                if (slot < SMP_BORDER)
+                    for (uint32_t r = 0; r < cl; ++r)
+                        st_cluster_u64(mapa_shared(smem_u32(&sh.border_list[rank][slot]), r), (unsigned long long)smp_key(z) << 32 | (uint32_t)~idx);
             }
         }
-        cluster_sync();
-        const int n = min((int)sh.n_cand, SMP_CAND);
-        unsigned long long* units = reinterpret_cast<unsigned long long*>(sh.mhi);  // [SMP_CAND]: the bins have been read
-        static_assert(sizeof(sh.mhi) + sizeof(sh.mlo) >= SMP_CAND * 8, "units of the border bin");
-        for (int i = tid; i < n; i += SMP_THREADS) units[i] = f.units(smp_unkey((uint32_t)(sh.border_list[i] >> 32)));
         __syncthreads();
-        for (int i = tid; i < n; i += SMP_THREADS) {
-            const unsigned long long me = sh.border_list[i];
+        if (tid < (int)cl) st_cluster_u32(mapa_shared(smem_u32(&sh.from[rank].border), tid), sh.n_cand);
+        cluster_sync();
+        // the lists one behind the other; the bins have been read by everybody
+        unsigned long long* units = reinterpret_cast<unsigned long long*>(sh.mhi);  // [SMP_CAND]
+        static_assert(sizeof(sh.mhi) + sizeof(sh.mlo) >= SMP_MAX_CLUSTER * SMP_BORDER * 8, "units of the border bin");
+        for (int i = tid; i < (int)cl * SMP_BORDER; i += SMP_THREADS) {
+            const uint32_t r = (uint32_t)i / SMP_BORDER, slot = (uint32_t)i % SMP_BORDER;
+            if (slot < sh.from[r].border) units[i] = f.units(smp_unkey((uint32_t)(sh.border_list[r][slot] >> 32)));
+            fits &= sh.from[r].border <= SMP_BORDER;
+        }
+        if (!__syncthreads_and(fits)) {
+            cluster_sync();
+            if (tid == 0) sh.n_cand = 0;
+            for (int i = tid; i < SMP_BINS; i += SMP_THREADS) sh.cnt[i] = sh.mhi[i] = sh.mlo[i] = 0;
+            cluster_sync();
+            return false;
+        }
+        for (int i = tid; i < (int)cl * SMP_BORDER; i += SMP_THREADS) {
+            const uint32_t r = (uint32_t)i / SMP_BORDER, slot = (uint32_t)i % SMP_BORDER;
+            if (slot >= sh.from[r].border) continue;
+            const unsigned long long me = sh.border_list[r][slot];
             unsigned long long b = sh.base_mass;
-            for (int j = 0; j < n; ++j)
-                if (sh.border_list[j] > me) b += units[j];
+            for (uint32_t t = 0; t < cl; ++t)
+                for (uint32_t j = 0; j < sh.from[t].border; ++j)
+                    if (sh.border_list[t][j] > me) b += units[t * SMP_BORDER + j];
             if (b < limit && limit <= b + units[i]) {
                 sh.lkey = (uint32_t)(me >> 32);
                 sh.lidx = ~(uint32_t)me;
@@ -822,7 +888,6 @@ __global__ void __launch_bounds__(SMP_THREADS, 2) sample_kernel(const SamplePara
         nan = __syncthreads_or(nan);
         if (tid == 0) sh.n_cand = sh.n_loc = 0;
         for (int i = tid; i < SMP_BINS; i += SMP_THREADS) sh.cnt[i] = sh.mhi[i] = sh.mlo[i] = 0;
-        if (tid < SMP_BINS2) sh.cnt2[tid] = 0;
         if (tid < SMP_SWEEP_CHUNKS) sh.extra[tid] = 0;
         asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
         if (tid < (int)cl) {

@@ -152,11 +152,11 @@ tbik_status dispatch_cache_attention(const CacheAttParams& p, const CattSplit& c
 
 template <typename T>
 tbik_status launch_sample(SampleParams& p, const DeviceInfo* info, int dev, cudaStream_t s) {
-    // Blocks per row: as few as hold the row in 48 KB each, more (up to 8) while the device has room for them and a
-    // block has at least 4096 tokens.
+    // Blocks per row: as few as hold the row in 80 KB each, more (up to 8) while the device holds all of them at once (two
+    // to an SM) and a block has at least 4096 tokens.
     int cl = 1;
-    while (cl < SMP_MAX_CLUSTER && ((long long)p.vocab * (int)sizeof(T) > 49152LL * cl ||
-                                    ((long long)p.batch * cl * 2 <= info->sms && p.vocab > 4096 * cl)))
+    while (cl < SMP_MAX_CLUSTER && ((long long)p.vocab * (int)sizeof(T) > 80000LL * cl ||
+                                    ((long long)p.batch * cl <= info->sms && p.vocab > 4096 * cl)))
         cl *= 2;
     p.seg = ((p.vocab + cl - 1) / cl + 15) / 16 * 16;
     const size_t smem = (size_t)p.seg * sizeof(T) + 32;
