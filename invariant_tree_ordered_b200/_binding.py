@@ -66,6 +66,8 @@ class RopeSwigluArgs(ctypes.Structure):
 def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     """Load ``libtbik.so`` (raises OSError if it is missing: build it first)."""
     global _lib
+    if _lib is not None and path is LIB_PATH:
+        return _lib
     with _lock:
         if _lib is not None and path == LIB_PATH:
             return _lib
@@ -139,9 +141,15 @@ def _check(status: int, what: str):
 
 # ------------------------------------------------------------ torch plumbing
 
+_torch_module = None
+
+
 def _torch():
-    import torch
-    return torch
+    global _torch_module
+    if _torch_module is None:
+        import torch
+        _torch_module = torch
+    return _torch_module
 
 
 def _ptr(t):
@@ -157,12 +165,14 @@ def _stream_handle(stream):
 def _need_out(t, dtype, shape, name="out"):
     """A caller-provided output: a contiguous CUDA tensor of this dtype and shape."""
     _need(t, dtype, name)
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape and tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
 
 
 def _need(t, dtype, name):
     torch = _torch()
+    if isinstance(t, torch.Tensor) and t.is_cuda and t.dtype is dtype and t.is_contiguous():
+        return
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
     if t.dtype != dtype:
@@ -528,14 +538,12 @@ def _on_device(first, others, stream, fn, args, what):
     """Calls the library on `first`'s device and stream (its current one by default), whatever the current device
     is; every tensor of the call has to be there."""
     torch = _torch()
-    index = first.device.index
+    index = first.get_device()
     for t in others:
-        if t is not None and t.device.index != index:
+        if t is not None and t.get_device() != index:
             raise ValueError("all tensors must be on one device")
-    if stream is None:
-        stream = torch.cuda.current_stream(index)
-    handle = stream.cuda_stream
-    if index == torch.cuda.current_device():
+    handle = torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
+    if index == torch._C._cuda_getDevice():
         status = fn(*args, handle)
     else:
         with torch.cuda.device(index):
@@ -559,12 +567,12 @@ def _pool(pages, scales, layered):
     torch = _torch()
     _need(pages, torch.float8_e4m3fn, "pages")
     _need(scales, torch.float32, "scales")
-    s = tuple(pages.shape)
+    s = pages.shape
     if not layered:
-        s = (1,) + s
+        s = (1, *s)
     if len(s) != 8 or s[1] != 2 or s[6] != 8 or s[7] != 16:
         raise ValueError("pages must be [%s2, num_pages, kv_heads, page/8, head_dim/16, 8, 16]" % ("layers, " if layered else ""))
-    if tuple(scales.shape) != tuple(pages.shape[: len(pages.shape) - 4]):
+    if scales.shape != pages.shape[:-4]:
         raise ValueError("scales must be [%s2, num_pages, kv_heads]" % ("layers, " if layered else ""))
     return s[0], s[2], s[3], s[4] * 8, s[5] * 16
 
@@ -718,6 +726,9 @@ def cache_attention_workspace(tokens, batch, max_q, max_keys, heads, kv_heads, h
     return n
 
 
+_attention_bytes = {}
+
+
 def cache_attention(q, pages, scales, table, start, *, cu=None, rows=None, max_q=None, max_keys=None, out=None,
                     workspace=None, stream=None):
     """Attention of new queries over one layer's pages [2, num_pages, ...] (tbik_cache_attention): q bf16 [tokens,
@@ -737,13 +748,19 @@ def cache_attention(q, pages, scales, table, start, *, cu=None, rows=None, max_q
     if max_keys is None:
         max_keys = max_pages * page
     cup, rp = _need_i32(cu, "cu", batch + 1), _need_i32(rows, "rows", batch)
+    key = (q.get_device(), tokens, batch, max_q, max_keys, heads, kv_heads, head_dim, page)
+    nbytes = _attention_bytes.get(key)
+    if nbytes is None:  # a function of the sizes and the device
+        with torch.cuda.device(key[0]):
+            nbytes = lib.tbik_cache_attention_workspace(*key[1:])
+        if len(_attention_bytes) < 4096:
+            _attention_bytes[key] = nbytes
     if out is None:
         # tokens outside every sequence are left as they are: zeros in a new tensor
         out = torch.empty_like(q) if cu is None else torch.zeros_like(q)
     else:
         _need_out(out, torch.bfloat16, q.shape)
-    ws, wsp, wsb = _bytes_on(lib.tbik_cache_attention_workspace(tokens, batch, max_q, max_keys, heads, kv_heads,
-                                                                head_dim, page), q.device, workspace)
+    ws, wsp, wsb = _bytes_on(nbytes, q.device, workspace)
     _on_device(pages, (q, scales, table, start, cu, rows, out, ws), stream, lib.tbik_cache_attention,
                (q.data_ptr(), pages.data_ptr(), scales.data_ptr(), table.data_ptr(), start.data_ptr(), cup, rp,
                 out.data_ptr(), tokens, batch, slots, max_pages, num_pages, heads, kv_heads, head_dim, page, max_q,
