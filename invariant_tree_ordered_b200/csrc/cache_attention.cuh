@@ -36,7 +36,7 @@
 namespace tbik {
 
 constexpr int CATT_LEAF = 128;
-constexpr int CATT_UNITS = 6;       // units per CTA that the split aims at
+constexpr int CATT_UNITS = 4;       // units per CTA that the split aims at
 constexpr int CATT_MAX_NODE = 64;   // leaves of a unit: six pending summaries
 constexpr int CATT_PENDING = 6;
 constexpr int CATT_JOIN_DEPTH = 4;  // levels above the units that one thread of the second kernel evaluates alone
@@ -315,7 +315,8 @@ struct CattPlan {
     int item, slot_base, tile_base, T;
 };
 
-// A unit: node v of tile `tau` of kv head h of an item.
+// A unit: node v of tile `tau` of kv head h of an item (in this order, the nodes of a tile one after the other, so that
+// its queries are taken once).
 template <int R>
 struct CattUnits {
     CattItem it;
@@ -333,6 +334,7 @@ struct CattUnits {
     __device__ __forceinline__ int imin(const CacheAttParams& p) const { return it.i0 + catt_div(p, tau * R); }
     __device__ __forceinline__ int imax(const CacheAttParams& p) const { return it.i0 + catt_div(p, min(it.rows, (tau + 1) * R) - 1); }
     __device__ __forceinline__ int slot() const { return slot_base + ((h * tiles + tau) << d) + v; }
+    __device__ __forceinline__ bool same_tile(const CattUnits& o) const { return item == o.item && h == o.h && tau == o.tau; }
     // The first unit that starts at or behind x0.
     __device__ __forceinline__ bool first(const CacheAttParams& p, const CattPlan& pl) {
         item = pl.item;
@@ -342,48 +344,43 @@ struct CattUnits {
         end = pl.x1;
         if (item < 0 || pl.x0 >= pl.x1) return false;
         enter(p);
-        const long long ht = (long long)p.kv_heads * tiles, y = pl.x0 - pl.at;
-        // down to the last node whose units start at or before y: nodes before v weigh their leaves and one for each
-        // that is not empty, lo + min(v, lo) in all
+        // a tile weighs its leaves and one for each node that is not empty; the nodes before v: lo + min(v, lo)
+        const int cost = it.L + min(it.L, 1 << d);
+        const long long y = pl.x0 - pl.at, tile = y < (1ll << 31) ? (long long)((uint32_t)y / (uint32_t)cost) : y / cost;
+        const int z = (int)(y - tile * cost);
+        h = (int)(tile / tiles);
+        tau = (int)(tile - (long long)h * tiles);
         v = lo = 0;
         size = it.L;
 #pragma unroll 1
-        for (int k = d - 1; k >= 0; --k) {
-            const int h = (size + 1) >> 1, r = lo + h;
-            if ((long long)(r + min(v + (1 << k), r)) * ht <= y) {
+        for (int k = d - 1; k >= 0; --k) {  // down to the last node that starts at or before z
+            const int left = (size + 1) >> 1, r = lo + left;
+            if (r + min(v + (1 << k), r) <= z) {
                 v += 1 << k;
                 lo = r;
-                size -= h;
+                size -= left;
             } else {
-                size = h;
+                size = left;
             }
         }
-        const long long base = (long long)(lo + min(v, lo)) * ht;
-        long long k = size ? (y - base + size) / (size + 1) : ht;
-        if (k >= ht) {
-            h = p.kv_heads - 1;
-            tau = tiles - 1;
-            at = pl.at + base + (size ? (ht - 1) * (size + 1) : 0);
-            return next(p);
-        }
-        h = (int)(k / tiles);
-        tau = (int)(k - (long long)h * tiles);
-        at = pl.at + base + k * (size + 1);
-        return at < end;
+        at = pl.at + tile * cost + lo + min(v, lo);
+        return at < pl.x0 || size == 0 ? next(p) : at < end;
     }
     __device__ __forceinline__ bool next(const CacheAttParams& p) {
         if (size) at += size + 1;
         if (at >= end) return false;
-        if (++tau < tiles) return true;
-        tau = 0;
-        if (++h < p.kv_heads) return true;
-        h = 0;
         lo += size;
 #pragma unroll 1
         while (++v < (1 << d)) {
             size = catt_node_size(it.L, d, v);
             if (size) return true;
         }
+        v = lo = 0;
+        size = catt_node_size(it.L, d, 0);
+        if (++tau < tiles) return true;
+        tau = 0;
+        if (++h < p.kv_heads) return true;
+        h = 0;
         if (d > 0) {
             slot_base += (p.kv_heads * tiles) << d;
             tile_base += p.kv_heads * tiles;
@@ -399,105 +396,133 @@ struct CattUnits {
     }
 };
 
-// Sum over the block; every thread gets it.  `buf`: 32 values.
-__device__ __forceinline__ long long catt_block_sum(long long v, long long* buf) {
-#pragma unroll
-    for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-    __syncthreads();
-    if ((threadIdx.x & 31) == 0) buf[threadIdx.x >> 5] = v;
-    __syncthreads();
-    v = 0;
-#pragma unroll 1
-    for (int w = 0; w < (int)blockDim.x / 32; ++w) v += buf[w];
-    return v;
-}
-// Sum of the values of lower threads; `total` over the block.
-__device__ __forceinline__ long long catt_block_before(long long v, long long* buf, long long& total) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    long long s = v;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const long long y = __shfl_up_sync(0xffffffffu, s, o);
-        if (lane >= o) s += y;
-    }
-    __syncthreads();
-    if (lane == 31) buf[warp] = s;
-    __syncthreads();
-    long long b = 0;
-    total = 0;
-#pragma unroll 1
-    for (int w = 0; w < (int)blockDim.x / 32; ++w) {
-        if (w < warp) b += buf[w];
-        total += buf[w];
-    }
-    return b + s - v;
+__device__ __forceinline__ long long catt_div_up(long long a, int b) {
+    return a < (1ll << 31) ? (long long)(((uint32_t)a + (uint32_t)b - 1u) / (uint32_t)b) : (a + b - 1) / b;
 }
 
-// Fills `pl`; true if some token of the call has no answer.
+// Per warp of the block: sums of a scan step.
+struct CattScan {
+    long long w, c;
+    int flags;
+};
+// Sums of w and c over lower threads, their totals over the block, and the or of the flags.  Two barriers.
+__device__ __forceinline__ void catt_scan(long long& w, long long& c, int& flags, CattScan* buf, long long& wt, long long& ct) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    long long sw = w, sc = c;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long y = __shfl_up_sync(0xffffffffu, sw, o), z = __shfl_up_sync(0xffffffffu, sc, o);
+        if (lane >= o) {
+            sw += y;
+            sc += z;
+        }
+    }
+    flags = __reduce_or_sync(0xffffffffu, flags);
+    __syncthreads();
+    if (lane == 31) buf[warp] = CattScan{sw, sc, flags};
+    __syncthreads();
+    long long bw = 0, bc = 0;
+    wt = ct = 0;
+    flags = 0;
+#pragma unroll 1
+    for (int k = 0; k < (int)blockDim.x / 32; ++k) {
+        const CattScan t = buf[k];
+        if (k < warp) {
+            bw += t.w;
+            bc += t.c;
+        }
+        wt += t.w;
+        ct += t.c;
+        flags |= t.flags;
+    }
+    w = bw + sw - w;
+    c = bc + sc - c;
+}
+
+// Fills `pl`; true if some token of the call has no answer.  One item per thread and step; with as many threads as
+// items (the usual case) every item is looked at once.
 template <int R>
-__device__ __forceinline__ bool catt_plan(const CacheAttParams& p, CattPlan* pl, long long* buf) {
+__device__ __forceinline__ bool catt_plan(const CacheAttParams& p, CattPlan* pl, CattScan* buf) {
     const int items = p.batch * p.blocks, tid = threadIdx.x, nt = blockDim.x;
     bool bad = false;
-    long long leaves = 0;
+    int L = 0, flags = 0;
+    long long ht = 0, leaves = 0, total = 0, t0, t1;
 #pragma unroll 1
     for (int i = tid; i < items; i += nt) {
         const CattItem t = catt_item(p, i, bad);
-        if (t.rows) leaves += (long long)t.L * p.kv_heads * ((t.rows + R - 1) / R);
+        L = t.L;
+        ht = t.rows ? (long long)p.kv_heads * ((t.rows + R - 1) / R) : 0;
+        leaves += ht * L;
     }
-    leaves = catt_block_sum(leaves, buf);
-    const long long aim = (long long)gridDim.x * CATT_UNITS;
-    const int T = (int)min((long long)CATT_MAX_NODE, max(1ll, (leaves + aim - 1) / aim));
+    long long unused = 0;
+    catt_scan(leaves, unused, flags, buf, t0, t1);
+    const long long aim = catt_div_up(t0, (int)gridDim.x * CATT_UNITS);
+    const int T = (int)min((long long)CATT_MAX_NODE, max(1ll, aim));
     // weight of a unit: its leaves and one for its start
-    long long total = 0;
+    auto weight = [&](int L, long long ht, int& d) {
+        d = catt_depth(L, T);
+        return (long long)(L + min(L, 1 << d)) * ht;
+    };
+    int d;
+    if (items > nt) {
+        long long w = 0;
 #pragma unroll 1
-    for (int i = tid; i < items; i += nt) {
-        const CattItem t = catt_item(p, i, bad);
-        if (t.rows) total += (long long)(t.L + min(t.L, 1 << catt_depth(t.L, T))) * p.kv_heads * ((t.rows + R - 1) / R);
+        for (int i = tid; i < items; i += nt) {
+            const CattItem t = catt_item(p, i, bad);
+            if (t.rows) w += weight(t.L, (long long)p.kv_heads * ((t.rows + R - 1) / R), d);
+        }
+        catt_scan(w, unused, flags, buf, total, t1);
     }
-    total = catt_block_sum(total, buf);
-    const long long x0 = total / gridDim.x * blockIdx.x + total % gridDim.x * blockIdx.x / gridDim.x;
-    const long long x1 = total / gridDim.x * (blockIdx.x + 1) + total % gridDim.x * (blockIdx.x + 1) / gridDim.x;
     if (tid == 0) {
-        pl->x0 = x0;
-        pl->x1 = x1;
         pl->item = -1;
         pl->T = T;
     }
-    __syncthreads();
-    bool deep = false;
-    long long at = 0, cut = 0;  // cut: (slots << 32) + tiles of the cut ones
+    long long at = 0, cut = 0, step = 0;  // cut: (slots << 32) + tiles of the cut ones
+    flags = 0;
 #pragma unroll 1
     for (int base = 0; base < items; base += nt) {
         const int i = base + tid;
-        long long w = 0, c = 0;
+        long long w = 0, c = 0, wt, ct;
         if (i < items) {
-            const CattItem t = catt_item(p, i, bad);
-            if (t.rows) {
-                const long long ht = (long long)p.kv_heads * ((t.rows + R - 1) / R);
-                const int d = catt_depth(t.L, T);
-                w = (long long)(t.L + min(t.L, 1 << d)) * ht;
-                if (d) c = ((ht << d) << 32) + ht;
-                deep |= d > CATT_JOIN_DEPTH;
+            if (items > nt) {
+                const CattItem t = catt_item(p, i, bad);
+                L = t.L;
+                ht = t.rows ? (long long)p.kv_heads * ((t.rows + R - 1) / R) : 0;
+            }
+            w = weight(L, ht, d);
+            if (d && ht) {
+                c = ((ht << d) << 32) + ht;
+                if (d > CATT_JOIN_DEPTH) flags |= 2;
             }
         }
-        long long wt, ct;
-        const long long wb = at + catt_block_before(w, buf, wt), cb = cut + catt_block_before(c, buf, ct);
-        if (w && wb <= x0 && x0 < wb + w) {
+        int f = flags | (bad ? 1 : 0);
+        const long long mine = w;
+        catt_scan(w, c, f, buf, wt, ct);
+        flags = f;
+        if (base == 0) {
+            if (items <= nt) total = wt;
+            step = catt_div_up(total, (int)gridDim.x);
+        }
+        const long long x0 = step * blockIdx.x;
+        if (mine && at + w <= x0 && x0 < at + w + mine) {
             pl->item = i;
-            pl->at = wb;
-            pl->slot_base = (int)(cb >> 32);
-            pl->tile_base = (int)(cb & 0xffffffff);
+            pl->at = at + w;
+            pl->slot_base = (int)((cut + c) >> 32);
+            pl->tile_base = (int)((cut + c) & 0xffffffff);
         }
         at += wt;
         cut += ct;
     }
-    // cu that lets sequences overlap can ask for more slots than there are
-    deep = __syncthreads_or(deep);
-    if (blockIdx.x == 0 && tid == 0 && p.max_slots) {
-        p.count[0] = (cut >> 32) > p.max_slots ? 0 : (int)(cut & 0xffffffff);
-        p.count[1] = deep;
+    if (tid == 0) {
+        pl->x0 = min(total, step * blockIdx.x);
+        pl->x1 = min(total, step * (blockIdx.x + 1));
+        // cu that lets sequences overlap can ask for more slots than there are
+        if (blockIdx.x == 0 && p.max_slots) {
+            p.count[0] = (cut >> 32) > p.max_slots ? 0 : (int)(cut & 0xffffffff);
+            p.count[1] = flags & 2;
+        }
     }
-    return __syncthreads_or(bad);
+    return flags & 1;
 }
 
 // Tokens without an answer: NaN, and an error unless the sequence was not granted (start < 0).
@@ -536,7 +561,7 @@ __global__ void __launch_bounds__(CattCfg<D, RW, NWG>::THREADS, CattCfg<D, RW, N
     constexpr int R = C::R, ST = C::STAGES;
     extern __shared__ __align__(1024) uint8_t smem[];
     __shared__ CattPlan plan;
-    __shared__ long long scan_buf[32];
+    __shared__ CattScan scan_buf[16];
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
     uint64_t *kf = bars, *ke = bars + ST, *vf = bars + 2 * ST, *ve = bars + 3 * ST;  // [ST] landed, MMAs retired
     uint64_t* wb = bars + 4 * ST;  // per group: s_full[2] s_empty[2] o_full[2] o_empty[2] p_full q_full
@@ -630,7 +655,8 @@ __global__ void __launch_bounds__(CattCfg<D, RW, NWG>::THREADS, CattCfg<D, RW, N
         // ---------------------------------------------------- MMA issue
         if (lane == 0) {
             constexpr uint32_t id_s = idesc_e4m3_f32(128, C::NQ, 0), id_o = idesc_e4m3_f32(128, C::NP, 1);
-            uint32_t g = 0, nu = 0;
+            uint32_t g = 0, nq = 0;
+            CattUnits<R> tile = u;
             // O^T of leaf x; D = 64 leaves lanes 64..127 with what lies behind (not read)
             auto values = [&](uint32_t x) -> bool {
                 const int st = x % ST;
@@ -656,7 +682,9 @@ __global__ void __launch_bounds__(CattCfg<D, RW, NWG>::THREADS, CattCfg<D, RW, N
                 return true;
             };
 #pragma unroll 1
-            for (bool more = any; more; more = u.next(p), ++nu) {
+            for (bool more = any; more; more = u.next(p)) {
+                const bool fresh = g == 0 || !u.same_tile(tile);
+                tile = u;
 #pragma unroll 1
                 for (int l = 0; l < u.size; ++l, ++g) {
                     const int st = g % ST;
@@ -665,7 +693,7 @@ __global__ void __launch_bounds__(CattCfg<D, RW, NWG>::THREADS, CattCfg<D, RW, N
                     for (int w = 0; w < NWG; ++w) {
                         uint64_t* b = wb + 10 * w;
                         const uint32_t sb = g % C::SBUF, use = g / C::SBUF;
-                        if (l == 0 && !catt_wait(&b[9], nu & 1, abort_flag, lim)) goto mma_out;
+                        if (l == 0 && fresh && !catt_wait(&b[9], nq & 1, abort_flag, lim)) goto mma_out;
                         if (use > 0 && !catt_wait(&b[2 + sb], (use - 1) & 1, abort_flag, lim)) goto mma_out;
                         tc_fence_after();
                         const uint32_t qa = smem_u32(smem + C::OFF_Q + w * C::QB), ka = smem_u32(smem + C::OFF_K + st * C::TILE);
@@ -675,6 +703,7 @@ __global__ void __launch_bounds__(CattCfg<D, RW, NWG>::THREADS, CattCfg<D, RW, N
                                       smem_desc_flat(qa + k * 256, 128, D * 8), id_s, k ? 1u : 0u);
                         tc_commit(&b[0 + sb]);
                     }
+                    if (l == 0 && fresh) ++nq;
                     tc_commit(&ke[st]);
                     if (g > 0 && !values(g - 1)) goto mma_out;
                 }
@@ -703,9 +732,9 @@ __global__ void __launch_bounds__(CattCfg<D, RW, NWG>::THREADS, CattCfg<D, RW, N
         bool ab = false;
 
         // Queries of a unit's rows as two e4m3 terms each, and their constants c.
-        auto load_q = [&](const CattUnits<R>& un, uint32_t nu) {
+        auto load_q = [&](const CattUnits<R>& un, uint32_t nq) {
             constexpr int TPR = D / 8, RPP = 128 / TPR;  // threads per row, rows per pass
-            float* cst = x + C::X_CST + (nu & 1) * RW;
+            float* cst = x + C::X_CST + (nq & 1) * RW;
             const int part = tid % TPR;
 #pragma unroll
             for (int r0 = 0; r0 < RW; r0 += RPP) {
@@ -764,7 +793,7 @@ __global__ void __launch_bounds__(CattCfg<D, RW, NWG>::THREADS, CattCfg<D, RW, N
         // Lane k: how many nodes leaf k closes (low half), and leaf k + 32 (high half).
         auto pop_codes = [&](int size) { return catt_pops(size, min(lane, size - 1)) | catt_pops(size, min(lane + 32, size - 1)) << 16; };
 
-        uint32_t g = 0, nu = 0, cleaned = 0;
+        uint32_t g = 0, nq = 0, cleaned = 0;  // leaves, tiles of queries, diagonal leaves
         CattUnits<R> prev = u;          // the unit of the previous leaf
         int prev_l = 0, prev_codes = 0;
         float prev_m = 0.0f, prev_o = 0.0f;  // lane = row: its maximum and the scale of its O
@@ -901,13 +930,14 @@ __global__ void __launch_bounds__(CattCfg<D, RW, NWG>::THREADS, CattCfg<D, RW, N
         };
 
 #pragma unroll 1
-        for (bool more = any; more; ++nu) {
+        for (bool more = any; more;) {
             CattUnits<R> nxt = u;
             const bool has_next = nxt.next(p);
             const int fr0 = u.tau * R + wg * RW, i0 = u.it.i0 & 127;
             const int nmax = has_next ? nxt.imax(p) : 0;
             const int row_i = (i0 + catt_div(p, fr0 + lane % RW)) & 127;  // lane = row: its position in the block
-            const float* cst = x + C::X_CST + (nu & 1) * RW;
+            const float* cst = x + C::X_CST + (nq & 1) * RW;
+            const bool fresh = has_next && !nxt.same_tile(u);  // other queries come next
 #pragma unroll 1
             for (int l = 0; l < u.size; ++l, ++g) {
                 const bool last = l + 1 == u.size;
@@ -965,7 +995,7 @@ __global__ void __launch_bounds__(CattCfg<D, RW, NWG>::THREADS, CattCfg<D, RW, N
                 // scales of the next leaf's key
                 float nks, nvs;
                 key_scales(last ? nxt.h : u.h, nid, nks, nvs);
-                if (last && has_next) load_q(nxt, nu + 1);
+                if (last && fresh) load_q(nxt, nq + 1);
                 // lane = row: its maximum, and the largest value scale among its visible pages of the leaf
                 float nm, no;
                 {
@@ -1102,6 +1132,7 @@ __global__ void __launch_bounds__(CattCfg<D, RW, NWG>::THREADS, CattCfg<D, RW, N
                 cvs = nvs;
             }
             u = nxt;
+            nq += fresh;
             more = has_next;
             imax = nmax;
             if (more) codes = pop_codes(u.size);
@@ -1128,14 +1159,15 @@ __global__ void __launch_bounds__(CattCfg<D, RW, NWG>::THREADS, CattCfg<D, RW, N
 
 // ------------------------------------------------------------------ the tree above the units
 //
-// A thread per dim.  Trees that are cut a few levels deep go to one group of D threads per row; for deeper ones (few rows
-// over long contexts) the block's eight groups take one subtree each.  Eight nodes' values are in flight at a time.
+// A group of D / 4 threads per row, four dims each.  Trees that are cut a few levels deep are one group's work; for deeper
+// ones (few rows over long contexts) the groups of a block take one subtree each.  Eight nodes are in flight at a time.
 // Empty nodes are passed over.
 
-constexpr int CATT_JOIN_GROUPS = 8;
+constexpr int CATT_JOIN_THREADS = 256;
 
 struct CattSum {
-    float m, s, o;
+    float m, s;
+    float4 o;
     bool any;
 };
 __device__ __forceinline__ CattSum catt_join(const CattSum& a, const CattSum& b) {
@@ -1145,33 +1177,37 @@ __device__ __forceinline__ CattSum catt_join(const CattSum& a, const CattSum& b)
     float ea, eb;
     catt_factors(a.m, b.m, r.m, ea, eb);
     r.s = __fmaf_rn(b.s, eb, __fmul_rn(a.s, ea));
-    r.o = __fmaf_rn(b.o, eb, __fmul_rn(a.o, ea));
+    r.o.x = __fmaf_rn(b.o.x, eb, __fmul_rn(a.o.x, ea));
+    r.o.y = __fmaf_rn(b.o.y, eb, __fmul_rn(a.o.y, ea));
+    r.o.z = __fmaf_rn(b.o.z, eb, __fmul_rn(a.o.z, ea));
+    r.o.w = __fmaf_rn(b.o.w, eb, __fmul_rn(a.o.w, ea));
     r.any = true;
     return r;
+}
+__device__ __forceinline__ CattSum catt_node_sum(const CacheAttParams& p, size_t at, int D, int part) {
+    CattSum x;
+    const float2 ms = p.ms[at];
+    x.m = ms.x;
+    x.s = ms.y;
+    x.o = *reinterpret_cast<const float4*>(p.o + at * D + part * 4);
+    x.any = true;
+    return x;
 }
 
 // The tree over nodes v0 .. v0 + n - 1 (n a power of two) of a tile's 2^d; PEND: log2(n / 8) at most.
 template <int D, int R, int PEND>
-__device__ __forceinline__ CattSum catt_join_nodes(const CacheAttParams& p, int slot, int L, int d, int v0, int n, int row, int dim) {
+__device__ __forceinline__ CattSum catt_join_nodes(const CacheAttParams& p, int slot, int L, int d, int v0, int n, int row, int part) {
     CattSum st[PEND + 1], r;
     r.any = false;
     int depth = 0;
     const int step = min(n, 8);
+#pragma unroll 1
     for (int v = 0; v < n; v += step) {
         CattSum x[8];
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
             x[k].any = false;
-            if (k < step) {
-                if (catt_node_size(L, d, v0 + v + k)) {
-                    const size_t at = (size_t)(slot + v0 + v + k) * R + row;
-                    const float2 ms = p.ms[at];
-                    x[k].m = ms.x;
-                    x[k].s = ms.y;
-                    x[k].o = p.o[at * D + dim];
-                    x[k].any = true;
-                }
-            }
+            if (k < step && catt_node_size(L, d, v0 + v + k)) x[k] = catt_node_sum(p, (size_t)(slot + v0 + v + k) * R + row, D, part);
         }
 #pragma unroll
         for (int h = 1; h < 8; h <<= 1)
@@ -1186,39 +1222,47 @@ __device__ __forceinline__ CattSum catt_join_nodes(const CacheAttParams& p, int 
 }
 
 template <int D, int R>
-__global__ void __launch_bounds__(D* CATT_JOIN_GROUPS) cache_attention_join_kernel(const __grid_constant__ CacheAttParams p) {
-    __shared__ CattSum part[CATT_JOIN_GROUPS][D];
-    const int dim = threadIdx.x % D, grp = threadIdx.x / D;
+__global__ void __launch_bounds__(CATT_JOIN_THREADS) cache_attention_join_kernel(const __grid_constant__ CacheAttParams p) {
+    constexpr int LANES = D / 4, GROUPS = CATT_JOIN_THREADS / LANES;
+    static_assert((1 << CATT_JOIN_DEPTH) >= GROUPS, "deeper trees have a subtree for every group");
+    __shared__ CattSum sums[GROUPS][LANES];
+    const int part = threadIdx.x % LANES, grp = threadIdx.x / LANES;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int count = p.count[0], deep = p.count[1];
     auto put = [&](const int4& t1, int row, const CattSum& x) {
         const int fr = t1.y + row, t = catt_div(p, fr), hd = t1.z * p.group + fr - t * p.group;
-        p.out[((size_t)(t1.x + t) * p.heads + hd) * D + dim] = f2bf(__fmul_rn(x.o, __frcp_rn(x.s)));
+        const float is = __frcp_rn(x.s);
+        uint2 y;
+        y.x = pack_bf2(__fmul_rn(x.o.x, is), __fmul_rn(x.o.y, is));
+        y.y = pack_bf2(__fmul_rn(x.o.z, is), __fmul_rn(x.o.w, is));
+        *reinterpret_cast<uint2*>(p.out + ((size_t)(t1.x + t) * p.heads + hd) * D + part * 4) = y;
     };
-    for (long long w = (long long)blockIdx.x * CATT_JOIN_GROUPS + grp; w < (long long)count * R; w += (long long)gridDim.x * CATT_JOIN_GROUPS) {
+#pragma unroll 1
+    for (long long w = (long long)blockIdx.x * GROUPS + grp; w < (long long)count * R; w += (long long)gridDim.x * GROUPS) {
         const int4 t0 = p.tiles[2 * (w / R)], t1 = p.tiles[2 * (w / R) + 1];  // slot, d, L, rows; token, first row, kv head
         const int row = (int)(w % R);
         if (row >= t0.w || t0.y > CATT_JOIN_DEPTH) continue;
-        put(t1, row, catt_join_nodes<D, R, 1>(p, t0.x, t0.z, t0.y, 0, 1 << t0.y, row, dim));
+        put(t1, row, catt_join_nodes<D, R, 1>(p, t0.x, t0.z, t0.y, 0, 1 << t0.y, row, part));
     }
     if (!deep) return;
+#pragma unroll 1
     for (long long w = blockIdx.x; w < (long long)count * R; w += gridDim.x) {
         const int4 t0 = p.tiles[2 * (w / R)], t1 = p.tiles[2 * (w / R) + 1];
         const int row = (int)(w % R);
         if (row >= t0.w || t0.y <= CATT_JOIN_DEPTH) continue;  // the same for the whole block
-        const int per = 1 << (t0.y - 3);
-        const CattSum r = catt_join_nodes<D, R, 14>(p, t0.x, t0.z, t0.y, grp * per, per, row, dim);
+        const int per = (1 << t0.y) / GROUPS;
+        const CattSum r = catt_join_nodes<D, R, 14>(p, t0.x, t0.z, t0.y, grp * per, per, row, part);
         __syncthreads();
-        part[grp][dim] = r;
+        sums[grp][part] = r;
         __syncthreads();
         if (grp == 0) {
-            CattSum x[8];
+            CattSum x[GROUPS];
 #pragma unroll
-            for (int k = 0; k < 8; ++k) x[k] = part[k][dim];
+            for (int k = 0; k < GROUPS; ++k) x[k] = sums[k][part];
 #pragma unroll
-            for (int h = 1; h < 8; h <<= 1)
+            for (int h = 1; h < GROUPS; h <<= 1)
 #pragma unroll
-                for (int k = 0; k + h < 8; k += 2 * h) x[k] = catt_join(x[k], x[k + h]);
+                for (int k = 0; k + h < GROUPS; k += 2 * h) x[k] = catt_join(x[k], x[k + h]);
             put(t1, row, x[0]);
         }
     }

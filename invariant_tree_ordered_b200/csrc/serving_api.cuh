@@ -127,9 +127,9 @@ tbik_status launch_cache_attention(const CacheAttParams& p, const CattSplit& c, 
     if (st != TBIK_OK || !c.slots) return st;
     // the second kernel's blocks may be set up while the first one ends; they wait for its results themselves
     cudaLaunchConfig_t cfg = {};
-    const long long rows = (long long)(c.slots / 2) * c.rows, full = (long long)info->sms * 2;
+    const long long rows = (long long)(c.slots / 2) * c.rows, full = (long long)info->sms * 8;
     cfg.gridDim = dim3((unsigned)(rows < full ? rows : full));
-    cfg.blockDim = dim3(D * CATT_JOIN_GROUPS);
+    cfg.blockDim = dim3(CATT_JOIN_THREADS);
     cfg.stream = s;
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
