@@ -59,6 +59,20 @@ __host__ __device__ __forceinline__ uint32_t cache_quant(uint32_t h, int E) {
     return sign | b;
 }
 
+// The same for the two halves of a word whose magnitudes are finite, as two bytes: round4 on both halves at once (no
+// carry leaves a half), cut by an addition of 2^14 that rounds toward zero (fp32's spacing there is e4m3's below 2^-6,
+// and finer ones above stay), and a conversion that is then exact.  `down` is 2^-E, E < 120 (there, fp32 holds every
+// rounded value).
+__device__ __forceinline__ uint32_t cache_quant2(uint32_t w, float down) {
+    const uint32_t mag = w & 0x7fff7fffu;
+    const uint32_t r = (mag + 0x00070007u + ((mag >> 4) & 0x00010001u)) & 0x7ff07ff0u;
+    const float lo = __fsub_rn(__fadd_rz(__fmul_rn(__uint_as_float(r << 16), down), 16384.0f), 16384.0f);
+    const float hi = __fsub_rn(__fadd_rz(__fmul_rn(__uint_as_float(r & 0xffff0000u), down), 16384.0f), 16384.0f);
+    uint16_t b;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(b) : "f"(hi), "f"(lo));
+    return (uint32_t)b | ((w >> 8) & 0x80u) | ((w >> 16) & 0x8000u);
+}
+
 // An e4m3 byte cut to the grid of a scale 2^d times larger.
 __host__ __device__ __forceinline__ uint32_t cache_down(uint32_t q, int d) {
     const uint32_t sign = q & 0x80u, b = q & 0x7Fu;
@@ -85,7 +99,7 @@ struct CacheAppendParams {
     const int32_t* start;
     const int32_t* cu;    // null: token b belongs to sequence b
     const int32_t* rows;  // null: sequence b has table row b
-    int tokens, batch, slots, max_pages, num_pages, kv_heads, page;
+    int tokens, batch, slots, max_pages, num_pages, kv_heads, page, page_shift;
 };
 
 // One block per (page that a sequence's new tokens touch, kv head, keys or values): the page's new tokens are read
@@ -101,18 +115,17 @@ __global__ void __launch_bounds__(THREADS) cache_append_kernel(const CacheAppend
     int b, t0, n, j;  // sequence, its first token, its tokens, page number among the touched ones
     if (p.cu) {
         const int x = blockIdx.x;
-        int lo = 0, hi = p.batch - 1;
-        while (lo < hi) {  // the last b with its first virtual page <= x
-            const int mid = (lo + hi + 1) >> 1;
-            if (p.cu[mid] / p.page + 2 * mid <= x)
-                lo = mid;
-            else
-                hi = mid - 1;
+        b = -1;  // the last b with its first virtual page <= x: they are counted, a load per thread at a time
+        for (int base = 0; base < p.batch; base += THREADS) {
+            const int i = base + tid;
+            const int c = __syncthreads_count(i < p.batch && (p.cu[i] >> p.page_shift) + 2 * i <= x);
+            b += c;
+            if (c < THREADS) break;
         }
-        b = lo;
+        if (b < 0) return;  // cu[0] > 0 and before the first page
         t0 = p.cu[b];
         n = p.cu[b + 1] - t0;
-        j = x - (t0 / p.page + 2 * b);
+        j = x - ((t0 >> p.page_shift) + 2 * b);
         if (t0 < 0 || n < 0 || t0 > p.tokens - n) {
             if (tid == 0) set_error(TBIK_ERR_POSITION);
             return;
@@ -124,12 +137,26 @@ __global__ void __launch_bounds__(THREADS) cache_append_kernel(const CacheAppend
         j = 0;
     }
     const int s = p.start[b];
-    const int first = s / p.page;  // the page of the first new token
+    const int first = s >> p.page_shift;  // the page of the first new token
     if (n <= 0 || j < 0 || s < 0) return;
     const long long end = (long long)s + n;
     const long long pg = (long long)first + j;
     const long long pg0 = pg * p.page;
     if (pg0 >= end) return;  // fewer pages than the bound allows
+    const int o0 = pg0 >= s ? 0 : (int)(s - pg0);                          // first new token's place in the page
+    const int o1 = (int)(end - pg0 < p.page ? end - pg0 : p.page);         // behind the last
+    const int src0 = t0 + (int)(pg0 + o0 - s);                             // its packed token
+    const int chunks = (o1 - o0) * (D / 8);
+    const uint16_t* x = (kv ? p.v : p.k) + ((size_t)src0 * p.kv_heads + head) * D;
+    const size_t tstride = (size_t)p.kv_heads * D;
+    uint4 w[CH];
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+        const int i = c * THREADS + tid;
+        w[c] = make_uint4(0, 0, 0, 0);
+        if (i < chunks) w[c] = __ldg(reinterpret_cast<const uint4*>(x + (size_t)(i / (D / 8)) * tstride) + i % (D / 8));
+    }
+    // the tokens are on their way while the page is looked up
     const int row = p.rows ? p.rows[b] : b;
     bool bad = row < 0 || row >= p.slots || pg >= p.max_pages;
     if (!bad && p.rows) {  // the same row twice would be written by two blocks at once
@@ -146,21 +173,8 @@ __global__ void __launch_bounds__(THREADS) cache_append_kernel(const CacheAppend
         if (tid == 0) set_error(TBIK_ERR_PAGE);
         return;
     }
-    const int o0 = pg0 >= s ? 0 : (int)(s - pg0);                          // first new token's place in the page
-    const int o1 = (int)(end - pg0 < p.page ? end - pg0 : p.page);         // behind the last
-    const int src0 = t0 + (int)(pg0 + o0 - s);                             // its packed token
-    const int chunks = (o1 - o0) * (D / 8);
-    const uint16_t* x = (kv ? p.v : p.k) + ((size_t)src0 * p.kv_heads + head) * D;
-    const size_t tstride = (size_t)p.kv_heads * D;
-    uint4 w[CH];
     uint32_t top = 0;
     bool odd = false;
-#pragma unroll
-    for (int c = 0; c < CH; ++c) {
-        const int i = c * THREADS + tid;
-        w[c] = make_uint4(0, 0, 0, 0);
-        if (i < chunks) w[c] = __ldg(reinterpret_cast<const uint4*>(x + (size_t)(i / (D / 8)) * tstride) + i % (D / 8));
-    }
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
         const uint32_t a[4] = {w[c].x, w[c].y, w[c].z, w[c].w};
@@ -210,6 +224,7 @@ __global__ void __launch_bounds__(THREADS) cache_append_kernel(const CacheAppend
         }
     }
     if (tid == 0) p.scales[ph] = cache_pow2(E);
+    const float down = cache_pow2(-E);
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
         const int i = c * THREADS + tid;
@@ -217,10 +232,15 @@ __global__ void __launch_bounds__(THREADS) cache_append_kernel(const CacheAppend
             const int t = o0 + i / (D / 8), g = i % (D / 8);
             const uint32_t a[4] = {w[c].x, w[c].y, w[c].z, w[c].w};
             uint2 y;
-            y.x = cache_quant(a[0] & 0xffffu, E) | cache_quant(a[0] >> 16, E) << 8 |
-                  cache_quant(a[1] & 0xffffu, E) << 16 | cache_quant(a[1] >> 16, E) << 24;
-            y.y = cache_quant(a[2] & 0xffffu, E) | cache_quant(a[2] >> 16, E) << 8 |
-                  cache_quant(a[3] & 0xffffu, E) << 16 | cache_quant(a[3] >> 16, E) << 24;
+            if (!odd && E < 120) {  // at 120 the largest rounded value is 2^128
+                y.x = cache_quant2(a[0], down) | cache_quant2(a[1], down) << 16;
+                y.y = cache_quant2(a[2], down) | cache_quant2(a[3], down) << 16;
+            } else {
+                y.x = cache_quant(a[0] & 0xffffu, E) | cache_quant(a[0] >> 16, E) << 8 |
+                      cache_quant(a[1] & 0xffffu, E) << 16 | cache_quant(a[1] >> 16, E) << 24;
+                y.y = cache_quant(a[2] & 0xffffu, E) | cache_quant(a[2] >> 16, E) << 8 |
+                      cache_quant(a[3] & 0xffffu, E) << 16 | cache_quant(a[3] >> 16, E) << 24;
+            }
             *reinterpret_cast<uint2*>(dst + (t >> 3) * (D * 8) + (g >> 1) * 128 + (t & 7) * 16 + (g & 1) * 8) = y;
         }
     }

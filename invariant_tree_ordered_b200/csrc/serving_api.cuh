@@ -320,6 +320,7 @@ tbik_status tbik_cache_append(const uint16_t* k, const uint16_t* v, uint8_t* pag
     p.k = k, p.v = v, p.pages = pages, p.scales = scales, p.table = table, p.refs = refs, p.start = start;
     p.cu = cu, p.rows = rows, p.tokens = tokens, p.batch = batch, p.slots = slots, p.max_pages = max_pages;
     p.num_pages = num_pages, p.kv_heads = kv_heads, p.page = page;
+    p.page_shift = page == 16 ? 4 : page == 32 ? 5 : page == 64 ? 6 : 7;
     if (head_dim == 128)
         launch_append<128>(p, reinterpret_cast<cudaStream_t>(stream));
     else
