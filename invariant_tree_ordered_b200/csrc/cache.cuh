@@ -66,11 +66,11 @@ __host__ __device__ __forceinline__ uint32_t cache_quant(uint32_t h, int E) {
 __device__ __forceinline__ uint32_t cache_quant2(uint32_t w, float down) {
     const uint32_t mag = w & 0x7fff7fffu;
     const uint32_t r = (mag + 0x00070007u + ((mag >> 4) & 0x00010001u)) & 0x7ff07ff0u;
-    const float lo = __fsub_rn(__fadd_rz(__fmul_rn(__uint_as_float(r << 16), down), 16384.0f), 16384.0f);
-    const float hi = __fsub_rn(__fadd_rz(__fmul_rn(__uint_as_float(r & 0xffff0000u), down), 16384.0f), 16384.0f);
+    const float lo = __fsub_rn(__fmaf_rz(__uint_as_float(r << 16), down, 16384.0f), 16384.0f);
+    const float hi = __fsub_rn(__fmaf_rz(__uint_as_float(r & 0xffff0000u), down, 16384.0f), 16384.0f);
     uint16_t b;
     asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(b) : "f"(hi), "f"(lo));
-    return (uint32_t)b | ((w >> 8) & 0x80u) | ((w >> 16) & 0x8000u);
+    return (uint32_t)b | (__byte_perm(w, 0, 0x4431) & 0x8080u);  // the signs are in bytes 1 and 3
 }
 
 // An e4m3 byte cut to the grid of a scale 2^d times larger.
@@ -173,17 +173,24 @@ __global__ void __launch_bounds__(THREADS) cache_append_kernel(const CacheAppend
         if (tid == 0) set_error(TBIK_ERR_PAGE);
         return;
     }
-    uint32_t top = 0;
-    bool odd = false;
+    uint32_t top2 = 0;  // largest magnitudes of the even and the odd dims
 #pragma unroll
-    for (int c = 0; c < CH; ++c) {
-        const uint32_t a[4] = {w[c].x, w[c].y, w[c].z, w[c].w};
+    for (int c = 0; c < CH; ++c)
+        top2 = __vmaxu2(__vmaxu2(top2, __vmaxu2(w[c].x & 0x7fff7fffu, w[c].y & 0x7fff7fffu)),
+                        __vmaxu2(w[c].z & 0x7fff7fffu, w[c].w & 0x7fff7fffu));
+    uint32_t top = max(top2 & 0xffffu, top2 >> 16);
+    const bool odd = top >= 0x7F80u;
+    if (odd) {  // what is not finite does not count
+        top = 0;
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            const uint32_t l = a[q] & 0x7FFFu, h = (a[q] >> 16) & 0x7FFFu;
-            odd |= l >= 0x7F80u || h >= 0x7F80u;
-            if (l < 0x7F80u) top = max(top, l);
-            if (h < 0x7F80u) top = max(top, h);
+        for (int c = 0; c < CH; ++c) {
+            const uint32_t a[4] = {w[c].x, w[c].y, w[c].z, w[c].w};
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const uint32_t l = a[q] & 0x7FFFu, h = (a[q] >> 16) & 0x7FFFu;
+                if (l < 0x7F80u) top = max(top, l);
+                if (h < 0x7F80u) top = max(top, h);
+            }
         }
     }
     __shared__ uint32_t red[THREADS / 32];

@@ -59,7 +59,7 @@ void launch_append(const CacheAppendParams& p, cudaStream_t s) {
         case 2: cache_append_kernel<D, 128, 2><<<grid, 128, 0, s>>>(p); break;
         case 4: cache_append_kernel<D, 128, 4><<<grid, 128, 0, s>>>(p); break;
         case 8: cache_append_kernel<D, 128, 8><<<grid, 128, 0, s>>>(p); break;
-        default: cache_append_kernel<D, 128, 16><<<grid, 128, 0, s>>>(p); break;
+        default: cache_append_kernel<D, 256, 8><<<grid, 256, 0, s>>>(p); break;
     }
 }
 
