@@ -794,8 +794,6 @@ __global__ void __launch_bounds__(CattCfg<D, RW, NWG>::THREADS, CattCfg<D, RW, N
         auto pop_codes = [&](int size) { return catt_pops(size, min(lane, size - 1)) | catt_pops(size, min(lane + 32, size - 1)) << 16; };
 
         uint32_t g = 0, nq = 0, cleaned = 0;  // leaves, tiles of queries, diagonal leaves
-        CattUnits<R> prev = u;          // the unit of the previous leaf
-        int prev_l = 0, prev_codes = 0;
         float prev_m = 0.0f, prev_o = 0.0f;  // lane = row: its maximum and the scale of its O
         int depth = 0;
         float cks = 0.0f, cvs = 0.0f;
@@ -808,17 +806,17 @@ __global__ void __launch_bounds__(CattCfg<D, RW, NWG>::THREADS, CattCfg<D, RW, N
             codes = pop_codes(u.size);
         }
 
-        // The summary of leaf g1 of unit `prev` enters the tree.
-        auto tree_step = [&](uint32_t g1) {
+        // The summary of leaf l of the unit (the CTA's leaf g1) enters the tree.
+        auto tree_step = [&](uint32_t g1, int l) {
             const uint32_t ob = g1 % C::OBUF;
             float* sums = x + C::X_SUM + (g1 & 1) * 4 * RW;
             const int row = lane % RW;
             float m = prev_m;
             float s = __fadd_rn(__fadd_rn(sums[row], sums[RW + row]), __fadd_rn(sums[2 * RW + row], sums[3 * RW + row]));
-            const int code = __shfl_sync(0xffffffffu, prev_codes, prev_l & 31);
-            int pops = prev_l < 32 ? code & 0xffff : code >> 16;
-            const bool last = prev_l + 1 == prev.size;
-            if (prev_l == 0) depth = CATT_PENDING - (32 - __clz(max(prev.size - 1, 0)));  // small trees stay in TMEM
+            const int code = __shfl_sync(0xffffffffu, codes, l & 31);
+            int pops = l < 32 ? code & 0xffff : code >> 16;
+            const bool last = l + 1 == u.size;
+            if (l == 0) depth = CATT_PENDING - (32 - __clz(max(u.size - 1, 0)));  // small trees stay in TMEM
             // O is in units of prev_o, a power of two: the first step multiplies it in
             float scale_o = prev_o;
             float o[RW];
@@ -891,13 +889,13 @@ __global__ void __launch_bounds__(CattCfg<D, RW, NWG>::THREADS, CattCfg<D, RW, N
                 __syncwarp();
                 return;
             }
-            const int fr0 = prev.tau * R + wg * RW, live = min(RW, prev.it.rows - fr0);
-            if (prev.d == 0) {
+            const int fr0 = u.tau * R + wg * RW, live = min(RW, u.it.rows - fr0);
+            if (u.d == 0) {
                 if (lane < RW) ofac[lane] = __frcp_rn(s);
                 __syncwarp();
                 if (has_dim) {
                     int t = catt_div(p, fr0), hd = fr0 - t * p.group;
-                    uint16_t* op = p.out + ((size_t)(prev.it.tok0 + t) * p.heads + prev.h * p.group) * D + tid;
+                    uint16_t* op = p.out + ((size_t)(u.it.tok0 + t) * p.heads + u.h * p.group) * D + tid;
 #pragma unroll
                     for (int r = 0; r < RW; ++r) {
                         if (r < live) op[hd * D] = f2bf(__fmul_rn(o[r], ofac[r]));
@@ -908,7 +906,7 @@ __global__ void __launch_bounds__(CattCfg<D, RW, NWG>::THREADS, CattCfg<D, RW, N
                     }
                 }
             } else {
-                const int slot = prev.slot();
+                const int slot = u.slot();
                 if ((unsigned)slot >= (unsigned)p.max_slots) {
                     set_error(TBIK_ERR_WORKSPACE);
                 } else {
@@ -919,10 +917,10 @@ __global__ void __launch_bounds__(CattCfg<D, RW, NWG>::THREADS, CattCfg<D, RW, N
                         for (int r = 0; r < RW; ++r)
                             if (r < live) op[r * D] = o[r];
                     }
-                    if (prev.v == 0 && wg == 0 && tid == 0) {
-                        int4* t = p.tiles + 2 * (size_t)(prev.tile_base + prev.h * prev.tiles + prev.tau);
-                        t[0] = make_int4(slot, prev.d, prev.it.L, min(R, prev.it.rows - prev.tau * R));
-                        t[1] = make_int4(prev.it.tok0, prev.tau * R, prev.h, 0);
+                    if (u.v == 0 && wg == 0 && tid == 0) {
+                        int4* t = p.tiles + 2 * (size_t)(u.tile_base + u.h * u.tiles + u.tau);
+                        t[0] = make_int4(slot, u.d, u.it.L, min(R, u.it.rows - u.tau * R));
+                        t[1] = make_int4(u.it.tok0, u.tau * R, u.h, 0);
                     }
                 }
             }
@@ -939,192 +937,195 @@ __global__ void __launch_bounds__(CattCfg<D, RW, NWG>::THREADS, CattCfg<D, RW, N
             const float* cst = x + C::X_CST + (nq & 1) * RW;
             const bool fresh = has_next && !nxt.same_tile(u);  // other queries come next
 #pragma unroll 1
-            for (int l = 0; l < u.size; ++l, ++g) {
-                const bool last = l + 1 == u.size;
-                const uint32_t sb = g % C::SBUF;
-                float a[RW];
-                float* mx = x + C::X_MAX + (g & 1) * 4 * RW;
-                float* pv = x + C::X_PV + (g & 1) * 8;
-                const bool diag = u.lo + l == u.it.L - 1;
-                // the next leaf's key
-                int nid = -1;
-                if (!last) nid = key_page(u, imax, l + 1);
-                else if (has_next) nid = key_page(nxt, nmax, 0);
-                if (!ab) ab = !catt_wait(&b[0 + sb], (g / C::SBUF) & 1, abort_flag, lim);
-                ab = __any_sync(0xffffffffu, ab);
-                const bool seen = (u.lo + l) * CATT_LEAF + tid <= imax, no_page = seen && (cid < 0 || cid >= p.num_pages);
-                if (!ab) {
-                    tc_fence_after();
-                    uint32_t raw[C::NQ];
-                    catt_ld<C::NQ>(tm + C::S_COL + sb * C::NQ, raw);
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&b[2 + sb]);
-                    const f2x k2 = pk2(cks, cks), i32 = pk2(0.03125f, 0.03125f);
-#pragma unroll
-                    for (int r = 0; r < RW; r += 2)
-                        upk2(mul2(fma2(pk2(__uint_as_float(raw[RW + r]), __uint_as_float(raw[RW + r + 1])), i32,
-                                       pk2(__uint_as_float(raw[r]), __uint_as_float(raw[r + 1]))), k2), a[r], a[r + 1]);
-                    if (__any_sync(0xffffffffu, no_page)) {
-                        if (no_page) {
-#pragma unroll
-                            for (int r = 0; r < RW; ++r) a[r] = __uint_as_float(0x7fc00000u);
-                            set_error(TBIK_ERR_PAGE);
-                        }
-                    }
-                    if (diag) {
-                        // row r is at block position i0 + (fr0 + r) / group and does not see this key if that is less
-                        // than tid, that is, if fr0 + r < (tid - i0) * group
-                        const int hidden = (tid - i0) * p.group - fr0;
-#pragma unroll
-                        for (int r = 0; r < RW; ++r)
-                            if (r < hidden) a[r] = -INFINITY;
-                    }
-#pragma unroll
-                    for (int r = 0; r < RW; r += 4) {
-                        float4 m4;
-                        m4.x = warp_max_f32(a[r]);
-                        m4.y = warp_max_f32(a[r + 1]);
-                        m4.z = warp_max_f32(a[r + 2]);
-                        m4.w = warp_max_f32(a[r + 3]);
-                        if (lane == 0) *reinterpret_cast<float4*>(mx + qd * RW + r) = m4;
-                    }
-                    if ((tid & (p.page - 1)) == 0) pv[tid >> p.page_shift] = cvs;
-                }
-                if (named_barrier_or(bar, 128, ab)) goto epi_out;
-                // scales of the next leaf's key
-                float nks, nvs;
-                key_scales(last ? nxt.h : u.h, nid, nks, nvs);
-                if (last && fresh) load_q(nxt, nq + 1);
-                // lane = row: its maximum, and the largest value scale among its visible pages of the leaf
-                float nm, no;
-                {
-                    const int row = lane % RW, i = diag ? row_i : 127;
-                    const float4 v0 = *reinterpret_cast<const float4*>(pv), v1 = *reinterpret_cast<const float4*>(pv + 4);
-                    const float v[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
-                    float vm = v[0];
-#pragma unroll
-                    for (int k = 1; k < 8; ++k)
-                        if (k << p.page_shift <= i) vm = fmaxf(vm, v[k]);
-                    nm = __fmul_rn(fmaxf(fmax3(mx[row], mx[RW + row], mx[2 * RW + row]), mx[3 * RW + row]), cst[row]);
-                    no = __fmul_rn(vm, 0.00390625f);
-                    // 256 / vm: scales are powers of two
-                    const float iv = __fmul_rn(256.0f, __uint_as_float((254u << 23) - __float_as_uint(vm)));
-                    if (lane < RW) {
-                        rmax[lane] = -nm;
-                        rval[lane] = iv;
-                    }
-                    __syncwarp();
-                }
-#pragma unroll
-                for (int r = 0; r < RW; r += 4) {
-                    const float4 c4 = *reinterpret_cast<const float4*>(cst + r), m4 = *reinterpret_cast<const float4*>(rmax + r);
-                    float y[4];
-                    upk2(fma2(pk2(a[r], a[r + 1]), pk2(c4.x, c4.y), pk2(m4.x, m4.y)), y[0], y[1]);
-                    upk2(fma2(pk2(a[r + 2], a[r + 3]), pk2(c4.z, c4.w), pk2(m4.z, m4.w)), y[2], y[3]);
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) a[r + k] = ex2_hw(y[k]);
-                }
-                float w[RW];  // 256 f p
-                if (!diag) {
-                    const float f = __fmul_rn(cvs, rval[0]);
-                    const f2x f2 = pk2(f, f);
-#pragma unroll
-                    for (int r = 0; r < RW; r += 2) upk2(mul2(pk2(a[r], a[r + 1]), f2), w[r], w[r + 1]);
+            for (int l = 0; l <= u.size; ++l) {
+                int nid = -1;  // the next leaf's key, its scales, and lane = row: this leaf's maximum and scale of O
+                float nks = 0.0f, nvs = 0.0f, nm = 0.0f, no = 0.0f;
+                if (l == u.size) {  // nothing but the last leaf's O is left
+                    if (named_barrier_or(bar, 128, ab)) goto epi_out;
+                    ab = !catt_wait(&b[4 + (g - 1) % C::OBUF], ((g - 1) / C::OBUF) & 1, abort_flag, lim);
+                    ab = __any_sync(0xffffffffu, ab);
                 } else {
-                    // f <= 1 for a key that the row sees; for others p is 0
-#pragma unroll
-                    for (int r = 0; r < RW; ++r) w[r] = __fmul_rn(a[r], fminf(__fmul_rn(cvs, rval[r]), 256.0f));
-                }
-                // P of the previous leaf is read until its O is there
-                if (g > 0 && !ab) {
-                    const uint32_t g1 = g - 1;
-                    ab = !catt_wait(&b[4 + g1 % C::OBUF], (g1 / C::OBUF) & 1, abort_flag, lim);
+                    const bool last = l + 1 == u.size;
+                    const uint32_t sb = g % C::SBUF;
+                    float a[RW];
+                    float* mx = x + C::X_MAX + (g & 1) * 4 * RW;
+                    float* pv = x + C::X_PV + (g & 1) * 8;
+                    const bool diag = u.lo + l == u.it.L - 1;
+                    if (!last) nid = key_page(u, imax, l + 1);
+                    else if (has_next) nid = key_page(nxt, nmax, 0);
+                    if (!ab) ab = !catt_wait(&b[0 + sb], (g / C::SBUF) & 1, abort_flag, lim);
                     ab = __any_sync(0xffffffffu, ab);
-                }
-                if (!ab) {
-                    uint32_t hi[RW / 4], lo[RW / 4];
+                    const bool seen = (u.lo + l) * CATT_LEAF + tid <= imax, no_page = seen && (cid < 0 || cid >= p.num_pages);
+                    if (!ab) {
+                        tc_fence_after();
+                        uint32_t raw[C::NQ];
+                        catt_ld<C::NQ>(tm + C::S_COL + sb * C::NQ, raw);
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&b[2 + sb]);
+                        const f2x k2 = pk2(cks, cks), i32 = pk2(0.03125f, 0.03125f);
+#pragma unroll
+                        for (int r = 0; r < RW; r += 2)
+                            upk2(mul2(fma2(pk2(__uint_as_float(raw[RW + r]), __uint_as_float(raw[RW + r + 1])), i32,
+                                           pk2(__uint_as_float(raw[r]), __uint_as_float(raw[r + 1]))), k2), a[r], a[r + 1]);
+                        if (__any_sync(0xffffffffu, no_page)) {
+                            if (no_page) {
+#pragma unroll
+                                for (int r = 0; r < RW; ++r) a[r] = __uint_as_float(0x7fc00000u);
+                                set_error(TBIK_ERR_PAGE);
+                            }
+                        }
+                        if (diag) {
+                            // row r is at block position i0 + (fr0 + r) / group and does not see this key if that is less
+                            // than tid, that is, if fr0 + r < (tid - i0) * group
+                            const int hidden = (tid - i0) * p.group - fr0;
+#pragma unroll
+                            for (int r = 0; r < RW; ++r)
+                                if (r < hidden) a[r] = -INFINITY;
+                        }
+#pragma unroll
+                        for (int r = 0; r < RW; r += 4) {
+                            float4 m4;
+                            m4.x = warp_max_f32(a[r]);
+                            m4.y = warp_max_f32(a[r + 1]);
+                            m4.z = warp_max_f32(a[r + 2]);
+                            m4.w = warp_max_f32(a[r + 3]);
+                            if (lane == 0) *reinterpret_cast<float4*>(mx + qd * RW + r) = m4;
+                        }
+                        if ((tid & (p.page - 1)) == 0) pv[tid >> p.page_shift] = cvs;
+                    }
+                    if (named_barrier_or(bar, 128, ab)) goto epi_out;
+                    // scales of the next leaf's key
+                    key_scales(last ? nxt.h : u.h, nid, nks, nvs);
+                    if (last && fresh) load_q(nxt, nq + 1);
+                    // lane = row: its maximum, and the largest value scale among its visible pages of the leaf
+                    {
+                        const int row = lane % RW, i = diag ? row_i : 127;
+                        const float4 v0 = *reinterpret_cast<const float4*>(pv), v1 = *reinterpret_cast<const float4*>(pv + 4);
+                        const float v[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
+                        float vm = v[0];
+#pragma unroll
+                        for (int k = 1; k < 8; ++k)
+                            if (k << p.page_shift <= i) vm = fmaxf(vm, v[k]);
+                        nm = __fmul_rn(fmaxf(fmax3(mx[row], mx[RW + row], mx[2 * RW + row]), mx[3 * RW + row]), cst[row]);
+                        no = __fmul_rn(vm, 0.00390625f);
+                        // 256 / vm: scales are powers of two
+                        const float iv = __fmul_rn(256.0f, __uint_as_float((254u << 23) - __float_as_uint(vm)));
+                        if (lane < RW) {
+                            rmax[lane] = -nm;
+                            rval[lane] = iv;
+                        }
+                        __syncwarp();
+                    }
 #pragma unroll
                     for (int r = 0; r < RW; r += 4) {
-                        const uint32_t h0 = pack_e4m3(w[r], w[r + 1]), h1 = pack_e4m3(w[r + 2], w[r + 3]);
-                        const float2 z0 = unpack_e4m3(h0), z1 = unpack_e4m3(h1);
-                        hi[r / 4] = h0 | h1 << 16;
-                        lo[r / 4] = pack_e4m3(__fsub_rn(w[r], z0.x), __fsub_rn(w[r + 1], z0.y)) |
-                                    pack_e4m3(__fsub_rn(w[r + 2], z1.x), __fsub_rn(w[r + 3], z1.y)) << 16;
+                        const float4 c4 = *reinterpret_cast<const float4*>(cst + r), m4 = *reinterpret_cast<const float4*>(rmax + r);
+                        float y[4];
+                        upk2(fma2(pk2(a[r], a[r + 1]), pk2(c4.x, c4.y), pk2(m4.x, m4.y)), y[0], y[1]);
+                        upk2(fma2(pk2(a[r + 2], a[r + 3]), pk2(c4.z, c4.w), pk2(m4.z, m4.w)), y[2], y[3]);
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) a[r + k] = ex2_hw(y[k]);
                     }
-                    uint8_t* dst = ps + (tid >> 3) * (8 * C::NP) + (tid & 7) * 16;
-                    if constexpr (RW == 8) {
-                        *reinterpret_cast<uint2*>(dst) = make_uint2(hi[0], hi[1]);
-                        *reinterpret_cast<uint2*>(dst + 128 * C::NP) = make_uint2(lo[0], lo[1]);
+                    float w[RW];  // 256 f p
+                    if (!diag) {
+                        const float f = __fmul_rn(cvs, rval[0]);
+                        const f2x f2 = pk2(f, f);
+#pragma unroll
+                        for (int r = 0; r < RW; r += 2) upk2(mul2(pk2(a[r], a[r + 1]), f2), w[r], w[r + 1]);
                     } else {
+                        // f <= 1 for a key that the row sees; for others p is 0
 #pragma unroll
-                        for (int k = 0; k < RW / 16; ++k) {
-                            *reinterpret_cast<uint4*>(dst + k * 128) = make_uint4(hi[4 * k], hi[4 * k + 1], hi[4 * k + 2], hi[4 * k + 3]);
-                            *reinterpret_cast<uint4*>(dst + 128 * C::NP + k * 128) = make_uint4(lo[4 * k], lo[4 * k + 1], lo[4 * k + 2], lo[4 * k + 3]);
-                        }
+                        for (int r = 0; r < RW; ++r) w[r] = __fmul_rn(a[r], fminf(__fmul_rn(cvs, rval[r]), 256.0f));
                     }
-                }
-                if (diag) {
-                    // values that no row sees must be finite (0 x NaN): zero behind the tile's last key, and NaN bytes
-                    // between its first row's key and that
-                    const int st = g % ST;
-                    if (!ab) ab = !catt_wait(&vf[st], (g / ST) & 1, abort_flag, lim);
-                    ab = __any_sync(0xffffffffu, ab);
+                    // P of the previous leaf is read until its O is there
+                    if (l > 0 && !ab) {
+                        const uint32_t g1 = g - 1;
+                        ab = !catt_wait(&b[4 + g1 % C::OBUF], (g1 / C::OBUF) & 1, abort_flag, lim);
+                        ab = __any_sync(0xffffffffu, ab);
+                    }
                     if (!ab) {
-                        if (tid > (u.imin(p) & 127)) {
-                            uint8_t* vt = smem + C::OFF_V + st * C::TILE + (tid >> 3) * (D * 8) + (tid & 7) * 16;
-                            for (int k = wg; k < D / 16; k += NWG) {
-                                uint4* at = reinterpret_cast<uint4*>(vt + k * 128);
-                                if (!seen || no_page) {
-                                    *at = make_uint4(0, 0, 0, 0);
-                                } else {
-                                    const uint4 y = *at;
-                                    const uint32_t z[4] = {y.x, y.y, y.z, y.w};
-                                    uint32_t o[4];
+                        uint32_t hi[RW / 4], lo[RW / 4];
 #pragma unroll
-                                    for (int e = 0; e < 4; ++e) o[e] = z[e] & ~__vcmpeq4(z[e] & 0x7f7f7f7fu, 0x7f7f7f7fu);
-                                    *at = make_uint4(o[0], o[1], o[2], o[3]);
-                                }
+                        for (int r = 0; r < RW; r += 4) {
+                            const uint32_t h0 = pack_e4m3(w[r], w[r + 1]), h1 = pack_e4m3(w[r + 2], w[r + 3]);
+                            const float2 z0 = unpack_e4m3(h0), z1 = unpack_e4m3(h1);
+                            hi[r / 4] = h0 | h1 << 16;
+                            lo[r / 4] = pack_e4m3(__fsub_rn(w[r], z0.x), __fsub_rn(w[r + 1], z0.y)) |
+                                        pack_e4m3(__fsub_rn(w[r + 2], z1.x), __fsub_rn(w[r + 3], z1.y)) << 16;
+                        }
+                        uint8_t* dst = ps + (tid >> 3) * (8 * C::NP) + (tid & 7) * 16;
+                        if constexpr (RW == 8) {
+                            *reinterpret_cast<uint2*>(dst) = make_uint2(hi[0], hi[1]);
+                            *reinterpret_cast<uint2*>(dst + 128 * C::NP) = make_uint2(lo[0], lo[1]);
+                        } else {
+#pragma unroll
+                            for (int k = 0; k < RW / 16; ++k) {
+                                *reinterpret_cast<uint4*>(dst + k * 128) = make_uint4(hi[4 * k], hi[4 * k + 1], hi[4 * k + 2], hi[4 * k + 3]);
+                                *reinterpret_cast<uint4*>(dst + 128 * C::NP + k * 128) = make_uint4(lo[4 * k], lo[4 * k + 1], lo[4 * k + 2], lo[4 * k + 3]);
                             }
                         }
                     }
-                    if (NWG > 1 && !ab) {  // each group has cleaned its share of the dims
-                        fence_proxy_async_smem();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(clean);
-                        ab = !catt_wait(clean, cleaned++ & 1, abort_flag, lim);
+                    if (diag) {
+                        // values that no row sees must be finite (0 x NaN): zero behind the tile's last key, and NaN bytes
+                        // between its first row's key and that
+                        const int st = g % ST;
+                        if (!ab) ab = !catt_wait(&vf[st], (g / ST) & 1, abort_flag, lim);
                         ab = __any_sync(0xffffffffu, ab);
-                    }
-                }
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0 && !ab && !(p.debug & TBIK_DEBUG_WITHHOLD_ACC_ARRIVE)) mbar_arrive(&b[8]);
-                // sums over the warp's 32 keys: halves 16, 8, 4, 2, 1 apart; the rows are dealt out on the way
-                {
-                    int n = RW;
+                        if (!ab) {
+                            if (tid > (u.imin(p) & 127)) {
+                                uint8_t* vt = smem + C::OFF_V + st * C::TILE + (tid >> 3) * (D * 8) + (tid & 7) * 16;
+                                for (int k = wg; k < D / 16; k += NWG) {
+                                    uint4* at = reinterpret_cast<uint4*>(vt + k * 128);
+                                    if (!seen || no_page) {
+                                        *at = make_uint4(0, 0, 0, 0);
+                                    } else {
+                                        const uint4 y = *at;
+                                        const uint32_t z[4] = {y.x, y.y, y.z, y.w};
+                                        uint32_t o[4];
 #pragma unroll
-                    for (int o = 16; o; o >>= 1) {
-                        if (n > 1) {
-                            n >>= 1;
-#pragma unroll
-                            for (int k = 0; k < RW / 2; ++k)
-                                if (k < n) {
-                                    const float keep = (lane & o) ? a[k + n] : a[k], send = (lane & o) ? a[k] : a[k + n];
-                                    a[k] = __fadd_rn(keep, __shfl_xor_sync(0xffffffffu, send, o));
+                                        for (int e = 0; e < 4; ++e) o[e] = z[e] & ~__vcmpeq4(z[e] & 0x7f7f7f7fu, 0x7f7f7f7fu);
+                                        *at = make_uint4(o[0], o[1], o[2], o[3]);
+                                    }
                                 }
-                        } else {
-                            a[0] = __fadd_rn(a[0], __shfl_xor_sync(0xffffffffu, a[0], o));
+                            }
+                        }
+                        if (NWG > 1 && !ab) {  // each group has cleaned its share of the dims
+                            fence_proxy_async_smem();
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive(clean);
+                            ab = !catt_wait(clean, cleaned++ & 1, abort_flag, lim);
+                            ab = __any_sync(0xffffffffu, ab);
                         }
                     }
-                    if (lane % (32 / RW) == 0) x[C::X_SUM + (g & 1) * 4 * RW + qd * RW + lane / (32 / RW)] = a[0];
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0 && !ab && !(p.debug & TBIK_DEBUG_WITHHOLD_ACC_ARRIVE)) mbar_arrive(&b[8]);
+                    // sums over the warp's 32 keys: halves 16, 8, 4, 2, 1 apart; the rows are dealt out on the way
+                    {
+                        int n = RW;
+#pragma unroll
+                        for (int o = 16; o; o >>= 1) {
+                            if (n > 1) {
+                                n >>= 1;
+#pragma unroll
+                                for (int k = 0; k < RW / 2; ++k)
+                                    if (k < n) {
+                                        const float keep = (lane & o) ? a[k + n] : a[k], send = (lane & o) ? a[k] : a[k + n];
+                                        a[k] = __fadd_rn(keep, __shfl_xor_sync(0xffffffffu, send, o));
+                                    }
+                            } else {
+                                a[0] = __fadd_rn(a[0], __shfl_xor_sync(0xffffffffu, a[0], o));
+                            }
+                        }
+                        if (lane % (32 / RW) == 0) x[C::X_SUM + (g & 1) * 4 * RW + qd * RW + lane / (32 / RW)] = a[0];
+                    }
                 }
-                if (g > 0 && !ab) {
+                if (l > 0 && !ab) {
                     tc_fence_after();
-                    tree_step(g - 1);
+                    tree_step(g - 1, l - 1);
                 }
-                prev = u;
-                prev_l = l;
-                prev_codes = codes;
+                if (l == u.size) break;
+                ++g;
                 prev_m = nm;
                 prev_o = no;
                 cid = nid;
@@ -1136,15 +1137,6 @@ __global__ void __launch_bounds__(CattCfg<D, RW, NWG>::THREADS, CattCfg<D, RW, N
             more = has_next;
             imax = nmax;
             if (more) codes = pop_codes(u.size);
-        }
-        if (named_barrier_or(bar, 128, ab)) goto epi_out;
-        if (g > 0) {
-            const uint32_t g1 = g - 1;
-            ab = !catt_wait(&b[4 + g1 % C::OBUF], (g1 / C::OBUF) & 1, abort_flag, lim);
-            if (!__any_sync(0xffffffffu, ab)) {
-                tc_fence_after();
-                tree_step(g1);
-            }
         }
     epi_out:;
     }
