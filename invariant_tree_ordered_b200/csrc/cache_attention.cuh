@@ -15,7 +15,9 @@
 //   a_j = (S_h + S_l / 32) kscale_j;  m = max over the leaf's visible keys;  p_j = 2^((a_j - m) c), c = 2^-x log2(e) / sqrt(D)
 //   f_j = vscale_j / (largest vscale among the row's visible pages of the leaf), a power of two
 //   s = sum of p_j in fp32: within 32 keys by halves (16 apart first), then (w0 + w1) + (w2 + w3)
-//   O^T = V^T [256 f p] M = 128 dims, N = rows, K = 128 keys, h and l one after the other
+//   O^T = V^T [h | l]   M = 128 dims, N = 2 rows, K = 128 keys, O = O_h + O_l
+// The two terms stand side by side in N, not one after the other in K: with few columns an MMA's time is that of reading
+// its 128 rows (measured: scores as K h + K l, l in e5m2, took four long contexts from 108 to 154 us).
 // Combining two summaries: M = max, e = 2^(m - M) (1 for the side that holds M), s = fma(s', e', s e), o likewise.
 //
 // One CTA works on tiles of R = RW * NWG rows (query, head) that share a kv head and a 128-position block, hence the
@@ -36,9 +38,7 @@
 namespace tbik {
 
 constexpr int CATT_LEAF = 128;
-constexpr int CATT_UNITS = 4;       // units per CTA that the split aims at
-constexpr int CATT_MAX_NODE = 64;   // leaves of a unit: six pending summaries
-constexpr int CATT_PENDING = 6;
+constexpr int CATT_UNITS = 3;       // units per CTA that the split aims at
 constexpr int CATT_JOIN_DEPTH = 4;  // levels above the units that one thread of the second kernel evaluates alone
 
 struct CacheAttParams {
@@ -69,29 +69,32 @@ struct CacheAttParams {
 template <int D_, int RW_, int NWG_>
 struct CattCfg {
     static constexpr int D = D_, RW = RW_, NWG = NWG_, R = RW * NWG;
-    static constexpr int NQ = 2 * RW;                // columns of S
-    static constexpr int NP = RW < 16 ? 16 : RW;     // columns of O (an MMA of 128 rows has at least 16)
+    static constexpr int NC = 2 * RW;                // columns of S and of O
     static constexpr int SBUF = RW == 32 ? 1 : 2, OBUF = RW == 32 ? 1 : 2;
-    static constexpr int TPEND = RW == 32 ? 5 : 6;   // pending summaries in TMEM; the largest one may be in shared memory
-    static constexpr int S_COL = 0, O_COL = SBUF * NQ, ST_COL = O_COL + OBUF * NP;
+    static constexpr int PENDING = RW == 32 && NWG == 1 ? 5 : 6;  // summaries that can wait: log2 of the leaves of a unit
+    static constexpr int MAX_NODE = 1 << PENDING;
+    static constexpr int TPEND = RW == 32 ? 4 : 6;   // of them in TMEM; the largest ones may be in shared memory
+    static constexpr int S_COL = 0, O_COL = SBUF * NC, ST_COL = O_COL + OBUF * NC;
     static constexpr int WG_COLS = ST_COL + TPEND * RW;
     static constexpr int COLS = NWG * WG_COLS <= 128 ? 128 : NWG * WG_COLS <= 256 ? 256 : 512;
+    static_assert(NWG * WG_COLS <= 512, "TMEM columns");
     static constexpr int CTAS = RW == 8 ? 3 : NWG == 1 ? 2 : 1;
     static constexpr int THREADS = 64 + 128 * NWG;
     static constexpr int TILE = 128 * D;             // bytes of a leaf's keys or values
-    static constexpr int STAGES = NWG == 2 ? 4 : RW == 16 && D == 128 ? 3 : D == 64 ? 4 : 2;
+    static constexpr int STAGES = NWG == 2 ? (D == 64 ? 4 : 3) : RW == 16 && D == 128 ? 3 : D == 64 ? 4 : 2;
     static constexpr int OFF_K = 0, OFF_V = STAGES * TILE, OFF_Q = 2 * STAGES * TILE;
-    static constexpr int QB = NQ * D, PB = 2 * 128 * NP;
+    static constexpr int QB = NC * D, PB = 128 * NC;
     static constexpr int OFF_P = OFF_Q + NWG * QB;
-    static constexpr int OFF_ST = OFF_P + NWG * PB;                          // the pending summary that TMEM has no room for
-    static constexpr int OFF_BAR = OFF_ST + (TPEND < CATT_PENDING ? NWG * RW * 128 * 4 : 0);
+    static constexpr int OFF_ST = OFF_P + NWG * PB;                          // the pending summaries that TMEM has no room for
+    static constexpr int OFF_BAR = OFF_ST + (TPEND < PENDING ? (PENDING - TPEND) * NWG * RW * 128 * 4 : 0);
     static constexpr int OFF_X = OFF_BAR + 512;
     // per group of 4 warps, in floats: maxima [2][4][RW], sums [2][4][RW], constants [2][RW], value scales [2][8],
-    // and per warp: factors and rows [4][RW], pending (m, s) [6][2][RW]
+    // and per warp: factors and rows [4][RW], pending (m, s) [PENDING][2][RW]
     static constexpr int X_MAX = 0, X_SUM = 8 * RW, X_CST = 16 * RW, X_PV = 18 * RW, X_WARP = X_PV + 16;
-    static constexpr int X_PER_WARP = 4 * RW + CATT_PENDING * 2 * RW;
+    static constexpr int X_PER_WARP = 4 * RW + PENDING * 2 * RW;
     static constexpr int X_FLOATS = X_WARP + 4 * X_PER_WARP;
     static constexpr int SMEM = OFF_X + NWG * X_FLOATS * 4;
+    static_assert(SMEM <= 230000, "shared memory");
 };
 
 __device__ __forceinline__ uint64_t smem_desc_flat(uint32_t saddr, uint32_t lbo, uint32_t sbo) {
@@ -441,7 +444,7 @@ __device__ __forceinline__ void catt_scan(long long& w, long long& c, int& flags
 
 // Fills `pl`; true if some token of the call has no answer.  One item per thread and step; with as many threads as
 // items (the usual case) every item is looked at once.
-template <int R>
+template <int R, int MAX_NODE>
 __device__ __forceinline__ bool catt_plan(const CacheAttParams& p, CattPlan* pl, CattScan* buf) {
     const int items = p.batch * p.blocks, tid = threadIdx.x, nt = blockDim.x;
     bool bad = false;
@@ -457,7 +460,7 @@ __device__ __forceinline__ bool catt_plan(const CacheAttParams& p, CattPlan* pl,
     long long unused = 0;
     catt_scan(leaves, unused, flags, buf, t0, t1);
     const long long aim = catt_div_up(t0, (int)gridDim.x * CATT_UNITS);
-    const int T = (int)min((long long)CATT_MAX_NODE, max(1ll, aim));
+    const int T = (int)min((long long)MAX_NODE, max(1ll, aim));
     // weight of a unit: its leaves and one for its start
     auto weight = [&](int L, long long ht, int& d) {
         d = catt_depth(L, T);
@@ -591,11 +594,7 @@ __global__ void __launch_bounds__(CattCfg<D, RW, NWG>::THREADS, CattCfg<D, RW, N
         tmem_alloc(tmem_slot, C::COLS);
         tmem_relinquish();
     }
-    // the columns of P that no row has stay zero
-    if (RW < 16)
-#pragma unroll 1
-        for (int i = threadIdx.x; i < NWG * C::PB / 16; i += C::THREADS) reinterpret_cast<uint4*>(smem + C::OFF_P)[i] = make_uint4(0, 0, 0, 0);
-    const bool marks = catt_plan<R>(p, &plan, scan_buf);
+    const bool marks = catt_plan<R, C::MAX_NODE>(p, &plan, scan_buf);
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     tc_fence_before();
     __syncthreads();
@@ -654,7 +653,7 @@ __global__ void __launch_bounds__(CattCfg<D, RW, NWG>::THREADS, CattCfg<D, RW, N
     } else if (warp == 1) {
         // ---------------------------------------------------- MMA issue
         if (lane == 0) {
-            constexpr uint32_t id_s = idesc_e4m3_f32(128, C::NQ, 0), id_o = idesc_e4m3_f32(128, C::NP, 1);
+            constexpr uint32_t id_s = idesc_e4m3_f32(128, C::NC, 0), id_o = idesc_e4m3_f32(128, C::NC, 1);
             uint32_t g = 0, nq = 0;
             CattUnits<R> tile = u;
             // O^T of leaf x; D = 64 leaves lanes 64..127 with what lies behind (not read)
@@ -670,12 +669,10 @@ __global__ void __launch_bounds__(CattCfg<D, RW, NWG>::THREADS, CattCfg<D, RW, N
                     tc_fence_after();
                     const uint32_t pa = smem_u32(smem + C::OFF_P + w * C::PB);
 #pragma unroll
-                    for (int part = 0; part < 2; ++part)
-#pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            tc_mma_f8(tmem + w * C::WG_COLS + C::O_COL + ob * C::NP,
-                                      smem_desc_flat(smem_u32(smem + C::OFF_V + st * C::TILE) + k * 32 * D, D * 8, 128),
-                                      smem_desc_flat(pa + part * 128 * C::NP + k * 32 * C::NP, 8 * C::NP, 128), id_o, (part | k) ? 1u : 0u);
+                    for (int k = 0; k < 4; ++k)
+                        tc_mma_f8(tmem + w * C::WG_COLS + C::O_COL + ob * C::NC,
+                                  smem_desc_flat(smem_u32(smem + C::OFF_V + st * C::TILE) + k * 32 * D, D * 8, 128),
+                                  smem_desc_flat(pa + k * 32 * C::NC, 8 * C::NC, 128), id_o, k ? 1u : 0u);
                     tc_commit(&b[4 + ob]);
                 }
                 tc_commit(&ve[st]);
@@ -699,7 +696,7 @@ __global__ void __launch_bounds__(CattCfg<D, RW, NWG>::THREADS, CattCfg<D, RW, N
                         const uint32_t qa = smem_u32(smem + C::OFF_Q + w * C::QB), ka = smem_u32(smem + C::OFF_K + st * C::TILE);
 #pragma unroll
                         for (int k = 0; k < D / 32; ++k)
-                            tc_mma_f8(tmem + w * C::WG_COLS + C::S_COL + sb * C::NQ, smem_desc_flat(ka + k * 256, 128, D * 8),
+                            tc_mma_f8(tmem + w * C::WG_COLS + C::S_COL + sb * C::NC, smem_desc_flat(ka + k * 256, 128, D * 8),
                                       smem_desc_flat(qa + k * 256, 128, D * 8), id_s, k ? 1u : 0u);
                         tc_commit(&b[0 + sb]);
                     }
@@ -722,11 +719,11 @@ __global__ void __launch_bounds__(CattCfg<D, RW, NWG>::THREADS, CattCfg<D, RW, N
         float* xw = x + C::X_WARP + qd * C::X_PER_WARP;   // this warp's own
         float *fac = xw, *ofac = xw + RW;                 // [RW] factors of a step
         float *rmax = xw + 2 * RW, *rval = xw + 3 * RW;   // [RW] a row's -m c, and 256 / its largest value scale
-        float2* pend = reinterpret_cast<float2*>(xw + 4 * RW);  // [6][RW] (m, s)
+        float2* pend = reinterpret_cast<float2*>(xw + 4 * RW);  // [PENDING][RW] (m, s)
         const uint32_t tm = tmem + wg * C::WG_COLS + ((uint32_t)(qd * 32) << 16);
         uint8_t* qs = smem + C::OFF_Q + wg * C::QB;
         uint8_t* ps = smem + C::OFF_P + wg * C::PB;
-        float* overflow = reinterpret_cast<float*>(smem + C::OFF_ST) + (size_t)wg * RW * 128 + tid;  // [RW][128]
+        float* overflow = reinterpret_cast<float*>(smem + C::OFF_ST) + (size_t)wg * RW * 128 + tid;  // [PENDING - TPEND][NWG][RW][128]
         const bool has_dim = tid < D;
         const int bar = 1 + wg;
         bool ab = false;
@@ -816,15 +813,17 @@ __global__ void __launch_bounds__(CattCfg<D, RW, NWG>::THREADS, CattCfg<D, RW, N
             const int code = __shfl_sync(0xffffffffu, codes, l & 31);
             int pops = l < 32 ? code & 0xffff : code >> 16;
             const bool last = l + 1 == u.size;
-            if (l == 0) depth = CATT_PENDING - (32 - __clz(max(u.size - 1, 0)));  // small trees stay in TMEM
+            if (l == 0) depth = C::PENDING - (32 - __clz(max(u.size - 1, 0)));  // small trees stay in TMEM
             // O is in units of prev_o, a power of two: the first step multiplies it in
             float scale_o = prev_o;
             float o[RW];
             if (has_dim) {
-                uint32_t raw[RW];
-                catt_ld<RW>(tm + C::O_COL + ob * C::NP, raw);
+                uint32_t raw[C::NC];
+                catt_ld<C::NC>(tm + C::O_COL + ob * C::NC, raw);
 #pragma unroll
-                for (int r = 0; r < RW; ++r) o[r] = __uint_as_float(raw[r]);
+                for (int r = 0; r < RW; r += 2)
+                    upk2(add2(pk2(__uint_as_float(raw[r]), __uint_as_float(raw[r + 1])),
+                              pk2(__uint_as_float(raw[RW + r]), __uint_as_float(raw[RW + r + 1]))), o[r], o[r + 1]);
             }
             tc_fence_before();
             __syncwarp();
@@ -856,11 +855,11 @@ __global__ void __launch_bounds__(CattCfg<D, RW, NWG>::THREADS, CattCfg<D, RW, N
                 __syncwarp();
                 if (has_dim) {
                     uint32_t raw[RW];
-                    if (C::TPEND < CATT_PENDING && depth < CATT_PENDING - C::TPEND) {
+                    if (C::TPEND < C::PENDING && depth < C::PENDING - C::TPEND) {
 #pragma unroll
-                        for (int r = 0; r < RW; ++r) raw[r] = __float_as_uint(overflow[r * 128]);
+                        for (int r = 0; r < RW; ++r) raw[r] = __float_as_uint(overflow[(depth * NWG * RW + r) * 128]);
                     } else {
-                        catt_ld<RW>(tm + C::ST_COL + (depth - (CATT_PENDING - C::TPEND)) * RW, raw);
+                        catt_ld<RW>(tm + C::ST_COL + (depth - (C::PENDING - C::TPEND)) * RW, raw);
                     }
 #pragma unroll
                     for (int r = 0; r < RW; r += 4) {
@@ -878,11 +877,11 @@ __global__ void __launch_bounds__(CattCfg<D, RW, NWG>::THREADS, CattCfg<D, RW, N
             if (!last) {
                 if (lane < RW) pend[depth * RW + lane] = make_float2(m, s);
                 if (has_dim) {
-                    if (C::TPEND < CATT_PENDING && depth < CATT_PENDING - C::TPEND) {
+                    if (C::TPEND < C::PENDING && depth < C::PENDING - C::TPEND) {
 #pragma unroll
-                        for (int r = 0; r < RW; ++r) overflow[r * 128] = o[r];
+                        for (int r = 0; r < RW; ++r) overflow[(depth * NWG * RW + r) * 128] = o[r];
                     } else {
-                        catt_st<RW>(tm + C::ST_COL + (depth - (CATT_PENDING - C::TPEND)) * RW, o);
+                        catt_st<RW>(tm + C::ST_COL + (depth - (C::PENDING - C::TPEND)) * RW, o);
                     }
                 }
                 ++depth;
@@ -958,8 +957,8 @@ __global__ void __launch_bounds__(CattCfg<D, RW, NWG>::THREADS, CattCfg<D, RW, N
                     const bool seen = (u.lo + l) * CATT_LEAF + tid <= imax, no_page = seen && (cid < 0 || cid >= p.num_pages);
                     if (!ab) {
                         tc_fence_after();
-                        uint32_t raw[C::NQ];
-                        catt_ld<C::NQ>(tm + C::S_COL + sb * C::NQ, raw);
+                        uint32_t raw[C::NC];
+                        catt_ld<C::NC>(tm + C::S_COL + sb * C::NC, raw);
                         tc_fence_before();
                         __syncwarp();
                         if (lane == 0) mbar_arrive(&b[2 + sb]);
@@ -1053,15 +1052,14 @@ __global__ void __launch_bounds__(CattCfg<D, RW, NWG>::THREADS, CattCfg<D, RW, N
                             lo[r / 4] = pack_e4m3(__fsub_rn(w[r], z0.x), __fsub_rn(w[r + 1], z0.y)) |
                                         pack_e4m3(__fsub_rn(w[r + 2], z1.x), __fsub_rn(w[r + 3], z1.y)) << 16;
                         }
-                        uint8_t* dst = ps + (tid >> 3) * (8 * C::NP) + (tid & 7) * 16;
+                        uint8_t* dst = ps + (tid >> 3) * (8 * C::NC) + (tid & 7) * 16;  // 16 bytes per key and 16 columns
                         if constexpr (RW == 8) {
-                            *reinterpret_cast<uint2*>(dst) = make_uint2(hi[0], hi[1]);
-                            *reinterpret_cast<uint2*>(dst + 128 * C::NP) = make_uint2(lo[0], lo[1]);
+                            *reinterpret_cast<uint4*>(dst) = make_uint4(hi[0], hi[1], lo[0], lo[1]);
                         } else {
 #pragma unroll
                             for (int k = 0; k < RW / 16; ++k) {
                                 *reinterpret_cast<uint4*>(dst + k * 128) = make_uint4(hi[4 * k], hi[4 * k + 1], hi[4 * k + 2], hi[4 * k + 3]);
-                                *reinterpret_cast<uint4*>(dst + 128 * C::NP + k * 128) = make_uint4(lo[4 * k], lo[4 * k + 1], lo[4 * k + 2], lo[4 * k + 3]);
+                                *reinterpret_cast<uint4*>(dst + (RW / 16 + k) * 128) = make_uint4(lo[4 * k], lo[4 * k + 1], lo[4 * k + 2], lo[4 * k + 3]);
                             }
                         }
                     }

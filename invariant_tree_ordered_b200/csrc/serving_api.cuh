@@ -96,7 +96,8 @@ tbik_status plan_cache_attention(int tokens, int batch, int max_q, int max_keys,
     c.grid = (int)(work < full ? work : full);
     if (leaves > 1) {
         // a cut tile of L leaves has fewer than 2 L / T nodes, T >= all leaves / (grid * CATT_UNITS) or the cap
-        const long long by_grid = 2ll * c.grid * CATT_UNITS, by_cap = 2 * work / CATT_MAX_NODE;
+        // (32 or 64)
+        const long long by_grid = 2ll * c.grid * CATT_UNITS, by_cap = 2 * work / 32;
         long long slots = by_grid > by_cap ? by_grid : by_cap;
         if (slots > 2 * work) slots = 2 * work;
         slots += 2;
