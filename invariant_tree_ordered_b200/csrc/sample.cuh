@@ -74,6 +74,7 @@ struct SampleShared {
     } from[SMP_MAX_CLUSTER];
     unsigned long long part[3][SMP_WARPS];
     uint32_t n_loc;
+    float wbound;
     unsigned long long scan[SMP_WARPS + 1];
     unsigned long long total;           // this block's kept mass (read by the others)
     unsigned long long mass;            // mass up to and with the last kept token
@@ -158,15 +159,33 @@ struct SmpPiece<uint16_t> {
 
 // What is kept, and with which weight.
 struct SampleFilter {
-    float m, c, min_w;  // row maximum, log2(e) / temperature, min_p
+    float m, min_w;     // row maximum, min_p
+    float c, c_lo, low; // log2(e) / temperature in two parts; differences below `low` have weight 0
     bool greedy;        // only tokens at the maximum
     bool ones;          // weights 1 for tokens of key lkey (counting equal ones)
     uint32_t lkey, lidx;
 
+    // 2^(x c) with the product's rounding and c's carried along: an error of c alone would move all of a row's tail
+    // against its head by some 10^-6, a few tokens' worth at the top-p border.
+    __device__ __forceinline__ float power(float x) const {
+        x = fmaxf(x, low);
+        const float a = __fmul_rn(x, c), lo = __fmaf_rn(x, -c_lo, __fmaf_rn(x, -c, a)), e = ex2_hw(a);
+        return __fmaf_rn(e, __fmul_rn(lo, -0.693147181f), e);
+    }
+    // The same for two logits.
+    __device__ __forceinline__ void power2(float z0, float z1, float& w0, float& w1) const {
+        float x0, x1, a0, a1;
+        upk2(add2(pk2(z0, z1), pk2(-m, -m)), x0, x1);
+        const f2x x = pk2(fmaxf(x0, low), fmaxf(x1, low)), a = mul2(x, pk2(c, c));
+        const f2x lo = fma2(x, pk2(-c_lo, -c_lo), fma2(x, pk2(-c, -c), a));
+        upk2(a, a0, a1);
+        const f2x e = pk2(ex2_hw(a0), ex2_hw(a1));
+        upk2(fma2(e, mul2(lo, pk2(-0.693147181f, -0.693147181f)), e), w0, w1);
+    }
     __device__ __forceinline__ float weight(float z) const {
         if (z == m) return 1.0f;
-        if (z == -INFINITY) return 0.0f;
-        return ex2_hw(__fmul_rn(__fsub_rn(z, m), c));
+        if (z == -INFINITY || m == INFINITY) return 0.0f;
+        return power(__fsub_rn(z, m));
     }
     __device__ __forceinline__ unsigned long long units(float z) const { return __float2ull_rn(__fmul_rn(weight(z), 0x1p32f)); }
     __device__ __forceinline__ unsigned long long kept(float z, uint32_t idx) const {
@@ -502,27 +521,41 @@ __device__ bool sample_fast(const SampleParams& p, SampleShared& sh, uint8_t* ra
             return true;
         }
         // ---- top-p alone: a bracket of bins around the limit, from counts and the bins' middle weights
-        float mf[BPT], s1 = 0.0f, s2 = 0.0f, all1, all2;
+        auto mass = [&](int x) { return __fmul_rn((float)cnt[x], ex2_hw(-1.44269504f / 32.0f * ((float)(tid * BPT + x) + 0.5f))); };
+        float s1 = 0.0f, s2 = 0.0f, all1, all2;
 #pragma unroll
         for (int x = 0; x < BPT; ++x) {
-            const float w = ex2_hw(-1.44269504f / 32.0f * ((float)(tid * BPT + x) + 0.5f));
-            mf[x] = __fmul_rn((float)cnt[x], w);
-            s1 += mf[x];
-            s2 += mf[x] * w;
+            const float w = mass(x);
+            s1 += w;
+            if (cnt[x]) s2 += w * w / (float)cnt[x];
         }
         float b = sample_before(s1, reinterpret_cast<float*>(sh.wmin), all1);
         sample_before(s2, reinterpret_cast<float*>(sh.wmax), all2);
-        // a token's weight is off by up to 1.6 % of it, evenly spread (0.9 % rms): four deviations of the sum, and a
-        // little for weights that change across a bin; twice, for the mass up to the limit and for the row's
-        const float margin = 2.0f * (0.036f * sqrtf(all2) + 0.0005f * all1), want = fmaxf(tp, 0.0f) * all1;
+        // The limit is where P >= p S.  A token's weight is off by up to 1.6 % of it, evenly spread (0.9 % rms; the margin
+        // takes four deviations); above the limit that shifts P and p S together, (1 - p) of it is left, and below it
+        // the weights are at most the border's, w: a variance of w times the mass (1 - p) S.  A little more for weights
+        // that change across a bin.
+        const float share = fminf(fmaxf(tp, 0.0f), 1.0f), want = share * all1;
         if (tid == 0) {
             sh.border = 0;
             sh.border_cnt = SMP_BINS - 1;
+            sh.wbound = 1.0f;
         }
         __syncthreads();
+        const float b0 = b;
 #pragma unroll
         for (int x = 0; x < BPT; ++x) {
-            const float e = b + mf[x];
+            const float e = b + mass(x);
+            if (b < want && e >= want) sh.wbound = 1.1f * mass(x) / (float)cnt[x];
+            b = e;
+        }
+        __syncthreads();
+        const float w = sh.wbound;
+        const float margin = 0.036f * ((1.0f - share) * sqrtf(all2) + share * sqrtf(w * (1.0f - share) * all1)) + 0.0004f * all1;
+        b = b0;
+#pragma unroll
+        for (int x = 0; x < BPT; ++x) {
+            const float e = b + mass(x);
             if (b < want - margin && e >= want - margin) sh.border = tid * BPT + x;
             if (b < want + margin && e >= want + margin) sh.border_cnt = tid * BPT + x;
             b = e;
@@ -550,9 +583,12 @@ __device__ bool sample_fast(const SampleParams& p, SampleShared& sh, uint8_t* ra
             if (v < pieces) {
                 float z[PER];
                 SmpPiece<T>::get(img[v], z);
+                float ws[PER];
+#pragma unroll
+                for (int e = 0; e < PER; e += 2) f.power2(z[e], z[e + 1], ws[e], ws[e + 1]);
 #pragma unroll
                 for (int e = 0; e < PER; ++e) {
-                    const float x = __fsub_rn(z[e], m), w = ex2_hw(__fmul_rn(x, f.c)), y = __fmul_rn(x, -scale);
+                    const float w = ws[e], y = __fmul_rn(__fsub_rn(m, z[e]), scale);
                     const uint32_t q = __float_as_uint(__fmaf_rn(w, 0x1p32f, 0x1p23f)) - 0x4b000000u;
                     const bool up = y < above, mid = !up && y < inside && q, big = !mid && w >= 0x1p-9f;
                     if (mid) between |= 1u << (r * PER + e);
@@ -916,7 +952,12 @@ __global__ void __launch_bounds__(SMP_THREADS, 2) sample_kernel(const SamplePara
     f.m = m;
     f.greedy = !(temp > 0.0f) || k == 1;
     f.ones = false;
-    f.c = f.greedy ? 1.0f : __fdiv_rn(1.44269504088896341f, temp);
+    {
+        const double c = f.greedy ? 1.0 : 1.4426950408889634 / (double)temp;
+        f.c = (float)fmin(c, 3e38);
+        f.c_lo = c < 1e30 ? (float)(c - (double)f.c) : 0.0f;
+        f.low = -__fdiv_rn(200.0f, f.c);
+    }
     f.min_w = p.min_p ? p.min_p[row] : 0.0f;
     f.lkey = 0;
     f.lidx = 0xffffffffu;

@@ -194,3 +194,34 @@ def test_streams_graphs_and_refusals():
     with pytest.raises(tbik.TbikError):
         tbik.sample(torch.zeros(8 * 5 + 1, device=DEV)[1:].view(5, 8), u)
     assert tbik.sample(z[:0], u[:0]).shape == (0,)
+
+
+@pytest.mark.parametrize("B,V,half", [(80, 50257, False), (150, 33001, False), (76, 151936, True)])
+def test_more_rows_than_the_device_holds(B, V, half):
+    """Rows that stay in global memory: every filter, masked tokens, low and high temperatures, flat rows among others,
+    and the same tokens as in a small batch."""
+    z = rows(B, B, V, half=half)
+    z[1::7, : V // 2] = float("-inf")
+    z[2::7] *= 0.001
+    z[3] = -1.25
+    z[4::9] += 40
+    z[5::9] -= 300
+    t = np.resize([1.0, 0.7, 0.2, 1.3, 0.0, 5.0, 0.05], B)
+    k = np.resize([0, 50, 1000, 0, V // 2, 2, 0, 0], B)
+    p = np.resize([0.95, 1.0, 0.9, 0.999, 0.3], B)
+    mp = np.resize([0.0, 0.05, 0.0], B)
+    got = check(z, uni(1, B), temp=t, k=k, p=p, mp=mp)
+    check(z, uni(2, B))
+    check(z, uni(3, B), p=p)
+    f = lambda x, dt: torch.tensor(np.asarray(x), dtype=dt, device=DEV)  # noqa: E731
+    for a in range(0, B, 40):
+        r = slice(a, a + 5)
+        few = tbik.sample(z[r].contiguous(), f(uni(1, B)[r], torch.float32), temperature=f(t[r], torch.float32),
+                          top_k=f(k[r], torch.int32), top_p=f(p[r], torch.float32), min_p=f(mp[r], torch.float32))
+        assert few.tolist() == got[r].tolist()
+    z[6, V - 1] = float("nan")
+    z[8] = float("-inf")
+    z[9, 7] = float("inf")
+    out = tbik.sample(z, f(uni(4, B), torch.float32), top_p=f(p, torch.float32))
+    assert tbik.get_error() == tbik.TBIK_ERR_VALUE
+    assert out[6].item() == -1 and out[8].item() == -1 and out[9].item() == 7
