@@ -38,6 +38,7 @@
 namespace tbik {
 
 constexpr int CATT_LEAF = 128;
+constexpr int CATT_START = 2;       // weight of a unit's start, in leaves
 constexpr int CATT_UNITS = 3;       // units per CTA that the split aims at
 constexpr int CATT_JOIN_DEPTH = 4;  // levels above the units that one thread of the second kernel evaluates alone
 
@@ -347,8 +348,8 @@ struct CattUnits {
         end = pl.x1;
         if (item < 0 || pl.x0 >= pl.x1) return false;
         enter(p);
-        // a tile weighs its leaves and one for each node that is not empty; the nodes before v: lo + min(v, lo)
-        const int cost = it.L + min(it.L, 1 << d);
+        // a tile weighs its leaves and a start for each node that is not empty; of these there are min(v, lo) before v
+        const int cost = it.L + CATT_START * min(it.L, 1 << d);
         const long long y = pl.x0 - pl.at, tile = y < (1ll << 31) ? (long long)((uint32_t)y / (uint32_t)cost) : y / cost;
         const int z = (int)(y - tile * cost);
         h = (int)(tile / tiles);
@@ -358,7 +359,7 @@ struct CattUnits {
 #pragma unroll 1
         for (int k = d - 1; k >= 0; --k) {  // down to the last node that starts at or before z
             const int left = (size + 1) >> 1, r = lo + left;
-            if (r + min(v + (1 << k), r) <= z) {
+            if (r + CATT_START * min(v + (1 << k), r) <= z) {
                 v += 1 << k;
                 lo = r;
                 size -= left;
@@ -366,11 +367,11 @@ struct CattUnits {
                 size = left;
             }
         }
-        at = pl.at + tile * cost + lo + min(v, lo);
+        at = pl.at + tile * cost + lo + CATT_START * min(v, lo);
         return at < pl.x0 || size == 0 ? next(p) : at < end;
     }
     __device__ __forceinline__ bool next(const CacheAttParams& p) {
-        if (size) at += size + 1;
+        if (size) at += size + CATT_START;
         if (at >= end) return false;
         lo += size;
 #pragma unroll 1
@@ -461,10 +462,10 @@ __device__ __forceinline__ bool catt_plan(const CacheAttParams& p, CattPlan* pl,
     catt_scan(leaves, unused, flags, buf, t0, t1);
     const long long aim = catt_div_up(t0, (int)gridDim.x * CATT_UNITS);
     const int T = (int)min((long long)MAX_NODE, max(1ll, aim));
-    // weight of a unit: its leaves and one for its start
+    // weight of a unit: its leaves and its start
     auto weight = [&](int L, long long ht, int& d) {
         d = catt_depth(L, T);
-        return (long long)(L + min(L, 1 << d)) * ht;
+        return (long long)(L + CATT_START * min(L, 1 << d)) * ht;
     };
     int d;
     if (items > nt) {
