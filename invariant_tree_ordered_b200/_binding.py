@@ -552,6 +552,16 @@ def _on_device(first, others, stream, fn, args, what):
         raise TbikError(status, what)
 
 
+def _new(shape, dtype, device, stream):
+    """A tensor for a call on `stream`: it belongs to that stream's memory, so that what the call drops at its end (a
+    workspace) is not handed to another stream while the kernels run."""
+    torch = _torch()
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
 def _need_i32(t, name, n=None):
     torch = _torch()
     if t is None:
@@ -600,7 +610,7 @@ def cache_extend(table, lens, refs, n_new, *, page: int, rows=None, start=None, 
     batch = n_new.numel()
     rp = _need_i32(rows, "rows", batch)
     if start is None:
-        start = torch.empty(batch, dtype=torch.int32, device=table.device)
+        start = _new(batch, torch.int32, table.device, stream)
     _need_out(start, torch.int32, (batch,), "start")
     _on_device(table, (lens, refs, n_new, rows, start), stream, lib.tbik_cache_extend,
                (table.data_ptr(), lens.data_ptr(), refs.data_ptr(), rp, n_new.data_ptr(), start.data_ptr(), batch,
@@ -608,7 +618,7 @@ def cache_extend(table, lens, refs, n_new, *, page: int, rows=None, start=None, 
     return start
 
 
-def _bytes_on(nbytes, device, workspace):
+def _bytes_on(nbytes, device, workspace, stream):
     """(tensor, pointer, bytes) of the caller's workspace, or of a new one."""
     torch = _torch()
     if nbytes == (1 << 64) - 1:
@@ -616,7 +626,7 @@ def _bytes_on(nbytes, device, workspace):
     if workspace is None:
         if nbytes == 0:
             return None, None, 0
-        workspace = torch.empty(nbytes, dtype=torch.uint8, device=device)
+        workspace = _new(nbytes, torch.uint8, device, stream)
     return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
@@ -632,7 +642,7 @@ def cache_fork(pages, scales, table, lens, refs, parents, children, *, workspace
     _need(parents, torch.int32, "parents")
     count = parents.numel()
     cp = _need_i32(children, "children", count)
-    ws, wsp, wsb = _bytes_on(lib.tbik_cache_fork_workspace(count), pages.device, workspace)
+    ws, wsp, wsb = _bytes_on(lib.tbik_cache_fork_workspace(count), pages.device, workspace, stream)
     _on_device(pages, (scales, table, lens, refs, parents, children, ws), stream, lib.tbik_cache_fork,
                (pages.data_ptr(), scales.data_ptr(), table.data_ptr(), lens.data_ptr(), refs.data_ptr(),
                 parents.data_ptr(), cp, count, layers, slots, max_pages, num_pages, kv_heads, head_dim, page, wsp, wsb),
@@ -659,9 +669,9 @@ def cache_compact(pages, scales, table, lens, refs, *, live=None, workspace=None
     if n_refs != num_pages:
         raise ValueError("refs must hold one count per page")
     if live is None:
-        live = torch.empty(1, dtype=torch.int32, device=pages.device)
+        live = _new(1, torch.int32, pages.device, stream)
     _need_out(live, torch.int32, (1,), "live")
-    ws, wsp, wsb = _bytes_on(lib.tbik_cache_compact_workspace(num_pages), pages.device, workspace)
+    ws, wsp, wsb = _bytes_on(lib.tbik_cache_compact_workspace(num_pages), pages.device, workspace, stream)
     _on_device(pages, (scales, table, lens, refs, live, ws), stream, lib.tbik_cache_compact,
                (pages.data_ptr(), scales.data_ptr(), table.data_ptr(), lens.data_ptr(), refs.data_ptr(),
                 live.data_ptr(), layers, slots, max_pages, num_pages, kv_heads, head_dim, page, wsp, wsb),
@@ -677,7 +687,7 @@ def cache_copy(pages, scales, src, dst, *, workspace=None, stream=None):
     _need(src, torch.int32, "src")
     count = src.numel()
     dp = _need_i32(dst, "dst", count)
-    ws, wsp, wsb = _bytes_on(lib.tbik_cache_fork_workspace(count), pages.device, workspace)
+    ws, wsp, wsb = _bytes_on(lib.tbik_cache_fork_workspace(count), pages.device, workspace, stream)
     _on_device(pages, (scales, src, dst, ws), stream, lib.tbik_cache_copy,
                (pages.data_ptr(), scales.data_ptr(), src.data_ptr(), dp, count, layers, num_pages, kv_heads, head_dim,
                 page, wsp, wsb), "tbik_cache_copy")
@@ -757,10 +767,16 @@ def cache_attention(q, pages, scales, table, start, *, cu=None, rows=None, max_q
             _attention_bytes[key] = nbytes
     if out is None:
         # tokens outside every sequence are left as they are: zeros in a new tensor
-        out = torch.empty_like(q) if cu is None else torch.zeros_like(q)
+        out = _new(q.shape, q.dtype, q.device, stream)
+        if cu is not None:
+            if stream is None:
+                out.zero_()
+            else:
+                with torch.cuda.stream(stream):
+                    out.zero_()
     else:
         _need_out(out, torch.bfloat16, q.shape)
-    ws, wsp, wsb = _bytes_on(nbytes, q.device, workspace)
+    ws, wsp, wsb = _bytes_on(nbytes, q.device, workspace, stream)
     _on_device(pages, (q, scales, table, start, cu, rows, out, ws), stream, lib.tbik_cache_attention,
                (q.data_ptr(), pages.data_ptr(), scales.data_ptr(), table.data_ptr(), start.data_ptr(), cup, rp,
                 out.data_ptr(), tokens, batch, slots, max_pages, num_pages, heads, kv_heads, head_dim, page, max_q,
@@ -792,7 +808,7 @@ def sample(logits, u, *, temperature=None, top_k=None, top_p=None, min_p=None, o
             raise ValueError(f"{name} must hold one value per row")
         ptrs.append(t.data_ptr())
     if out is None:
-        out = torch.empty(batch, dtype=torch.int32, device=logits.device)
+        out = _new(batch, torch.int32, logits.device, stream)
     _need_out(out, torch.int32, (batch,))
     _on_device(logits, (u, temperature, top_k, top_p, min_p, out), stream, lib.tbik_sample,
                (logits.data_ptr(), *ptrs, out.data_ptr(), batch, vocab, int(logits.dtype == torch.bfloat16)), "tbik_sample")

@@ -1220,6 +1220,13 @@ __global__ void __launch_bounds__(CATT_JOIN_THREADS) cache_attention_join_kernel
     const int part = threadIdx.x % LANES, grp = threadIdx.x / LANES;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int count = p.count[0], deep = p.count[1];
+    // A call that gave up (an expired wait) has left descriptors unwritten: whatever they hold, nothing outside the
+    // workspace and the output is touched.
+    auto sound = [&](const int4& t0, const int4& t1) {
+        return t0.x >= 0 && t0.y > 0 && t0.y < 20 && t0.z > 0 && t0.w > 0 && t0.w <= R && (long long)t0.x + (1 << t0.y) <= p.max_slots &&
+               t1.x >= 0 && t1.y >= 0 && t1.y <= CATT_LEAF * p.group - t0.w && t1.z >= 0 && t1.z < p.kv_heads &&
+               t1.x <= p.tokens - 1 - catt_div(p, t1.y + t0.w - 1);
+    };
     auto put = [&](const int4& t1, int row, const CattSum& x) {
         const int fr = t1.y + row, t = catt_div(p, fr), hd = t1.z * p.group + fr - t * p.group;
         const float is = __frcp_rn(x.s);
@@ -1232,7 +1239,7 @@ __global__ void __launch_bounds__(CATT_JOIN_THREADS) cache_attention_join_kernel
     for (long long w = (long long)blockIdx.x * GROUPS + grp; w < (long long)count * R; w += (long long)gridDim.x * GROUPS) {
         const int4 t0 = p.tiles[2 * (w / R)], t1 = p.tiles[2 * (w / R) + 1];  // slot, d, L, rows; token, first row, kv head
         const int row = (int)(w % R);
-        if (row >= t0.w || t0.y > CATT_JOIN_DEPTH) continue;
+        if (!sound(t0, t1) || row >= t0.w || t0.y > CATT_JOIN_DEPTH) continue;
         put(t1, row, catt_join_nodes<D, R, 1>(p, t0.x, t0.z, t0.y, 0, 1 << t0.y, row, part));
     }
     if (!deep) return;
@@ -1240,7 +1247,7 @@ __global__ void __launch_bounds__(CATT_JOIN_THREADS) cache_attention_join_kernel
     for (long long w = blockIdx.x; w < (long long)count * R; w += gridDim.x) {
         const int4 t0 = p.tiles[2 * (w / R)], t1 = p.tiles[2 * (w / R) + 1];
         const int row = (int)(w % R);
-        if (row >= t0.w || t0.y <= CATT_JOIN_DEPTH) continue;  // the same for the whole block
+        if (!sound(t0, t1) || row >= t0.w || t0.y <= CATT_JOIN_DEPTH) continue;  // the same for the whole block
         const int per = (1 << t0.y) / GROUPS;
         const CattSum r = catt_join_nodes<D, R, 14>(p, t0.x, t0.z, t0.y, grp * per, per, row, part);
         __syncthreads();

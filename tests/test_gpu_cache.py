@@ -503,3 +503,156 @@ def test_a_large_pool():
     check_written(c, 1, k, v)
     assert torch.equal(c.attend(q, i32([page + 2]), [1], [1], packed=False, max_keys=page + 3).double().cpu(), torch.from_numpy(got))
     assert tbik.get_error() == tbik.TBIK_OK
+
+
+# ------------------------------------------------- calls at their edges
+
+def test_nan_bytes_that_a_row_does_not_see():
+    """Bytes behind a row's position (written by nobody, or NaN under a later query of the same tile) leave it alone."""
+    H, D, page = 2, 64, 16
+    c, rows = filled([300], H, D, page, seed=4)
+    q = torch.randn(6, 8, D, device=DEV).to(torch.bfloat16)
+    good = c.attend(q, i32([294]), [6], rows)
+    at = 298  # the last two queries see it, the first four do not
+    pg, o = int(c.book.table[rows[0], at // page]), at % page
+    raw(c.pages)[0][:, pg, :, o // 8, :, o % 8] = NAN_BYTE
+    raw(c.pages)[0][:, pg, :, (o + 2) // 8:, :, (o + 2) % 8:] = NAN_BYTE
+    got = c.attend(q, i32([294]), [6], rows)
+    assert torch.equal(got[:4], good[:4])
+    assert tbik.get_error() == tbik.TBIK_OK
+
+
+def test_attention_bounds_that_are_too_tight_and_offsets_that_cannot_be():
+    H, D, page = 2, 128, 32
+    c, rows = filled([300, 200], H, D, page, seed=7)
+    q = torch.randn(9, 4, D, device=DEV).to(torch.bfloat16)
+    good = c.attend(q, i32([295, 196]), [5, 4], rows)
+    got = c.attend(q, i32([295, 196]), [5, 4], rows, max_q=4)      # one query more than announced
+    assert tbik.get_error() == tbik.TBIK_ERR_PAGE
+    assert torch.isnan(got[4]).all() and torch.equal(got[:4], good[:4]) and torch.equal(got[5:], good[5:])
+    got = c.attend(q, i32([295, 196]), [5, 4], rows, max_keys=298)  # the last two queries see more keys
+    assert tbik.get_error() == tbik.TBIK_ERR_PAGE
+    assert torch.isnan(got[3:5]).all() and torch.equal(got[:3], good[:3]) and torch.equal(got[5:], good[5:])
+    for cu in ([0, 5, 10], [0, 5, 4], [-1, 5, 9]):  # beyond the tokens, descending, before the first
+        out = torch.full_like(q, 3.0)
+        tbik.cache_attention(q, c.pages[0], c.scales[0], c.table, i32([295, 196]), cu=i32(cu), rows=i32(rows), out=out, max_q=5, max_keys=300)
+        assert tbik.get_error() == tbik.TBIK_ERR_POSITION
+        which = slice(0, 5) if cu[0] == 0 else slice(5, 9)  # the sequence whose range is sound
+        rest = slice(5, 9) if cu[0] == 0 else slice(0, 5)
+        assert torch.equal(out[which], good[which]) and (out[rest] == 3.0).all()
+
+
+def test_the_same_slot_for_many_sequences_and_two_streams_at_once():
+    """Reading needs no slot of its own: 300 queries over one sequence, in two calls that run side by side."""
+    H, heads, D, page = 1, 4, 128, 64
+    c, rows = filled([5000], H, D, page, seed=3)
+    q = torch.randn(300, heads, D, device=DEV).to(torch.bfloat16)
+    start = i32(np.arange(300) * 16 + 5)
+    args = (c.pages[0], c.scales[0], c.table, start)
+    ref = tbik.cache_attention(q, *args, rows=i32(rows * 300), max_keys=5000)
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    outs = [tbik.cache_attention(q, *args, rows=i32(rows * 300), max_keys=5000, stream=s) for s in streams for _ in range(4)]
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, ref) for o in outs)
+    assert tbik.get_error() == tbik.TBIK_OK
+
+
+@pytest.mark.parametrize("heads,H,ctx,n", [(8, 2, [3000, 700], [1, 1]), (16, 2, [1500, 130], [40, 3])])
+def test_withheld_arrive_times_out_and_context_survives(heads, H, ctx, n):
+    """The softmax warps are told to withhold their "weights written" arrive: the MMA issuer's bounded wait expires,
+    every role leaves, and the next call gives the same bits as before."""
+    c, rows = filled(ctx, H, 128, 64, seed=2)
+    q = torch.randn(sum(n), heads, 128, device=DEV).to(torch.bfloat16)
+    start = i32([a - b for a, b in zip(ctx, n)])
+    good = c.attend(q, start, n, rows)
+    assert tbik.get_error() == tbik.TBIK_OK
+    try:
+        tbik.debug_set(tbik.DEBUG_WITHHOLD_ACC_ARRIVE, 50_000_000)  # 50 ms per wait
+        c.attend(q, start, n, rows)
+        status = tbik.get_error()
+    finally:
+        tbik.debug_set(0, 0)
+    assert status == tbik.TBIK_ERR_TIMEOUT
+    assert torch.equal(c.attend(q, start, n, rows), good)
+    assert tbik.get_error() == tbik.TBIK_OK
+
+
+# ------------------------------------------------- together, as a rollout uses them
+
+def test_a_rollout_and_its_replay():
+    """Prompts written, forked into samples, generated token by token (room, write, attention, logits, choice), some
+    freed and the pool compacted on the way.  Every sequence by itself gives the same pages, bits and tokens."""
+    L, H, G, D, page, V, E = 2, 2, 4, 64, 16, 1000, 512
+    heads = H * G
+    g = torch.Generator(device=DEV).manual_seed(0)
+    rnd = lambda *s: (torch.randn(*s, device=DEV, generator=g) / s[0] ** 0.5).to(torch.bfloat16)  # noqa: E731
+    emb = (torch.randn(V, E, device=DEV, generator=g)).to(torch.bfloat16)
+    wq, wk, wv, wo = [[rnd(E, k * D) for _ in range(L)] for k in (heads, H, H)] + [[rnd(heads * D, E) for _ in range(L)]]
+    head = rnd(E, V)
+
+    def forward(c, tok, start, n, rows):
+        """Hidden states of packed tokens; every GEMM in tree order, so a row's bits do not depend on the others."""
+        h = emb[tok]
+        for l in range(L):
+            mm = lambda x, w: tbik.gemm(x, w, T=1, leaf=64, out_bf16=True)  # noqa: E731
+            c.append(mm(h, wk[l]).view(-1, H, D), mm(h, wv[l]).view(-1, H, D), start, n, rows, layer=l)
+            a = c.attend(mm(h, wq[l]).view(-1, heads, D), start, n, rows, layer=l)
+            h = tbik.gemm(a.reshape(-1, heads * D).contiguous(), wo[l], T=1, leaf=64, residual=h.contiguous())
+        return h
+
+    def choose(h, u):
+        B = h.shape[0]
+        z = tbik.gemm(h.contiguous(), head, T=1, leaf=64)
+        full = lambda x, dt: torch.full((B,), x, dtype=dt, device=DEV)  # noqa: E731
+        return tbik.sample(z, u, temperature=full(0.8, torch.float32), top_k=full(200, torch.int32),
+                           top_p=full(0.95, torch.float32), min_p=full(0.001, torch.float32))
+
+    prompts = [torch.randint(0, V, (m,), device=DEV, generator=g) for m in (37, 16, 150)]
+    slots, steps, per = 16, 20, 3
+    c = Cache(slots, 20, 200, H, D, page, layers=L)
+    n = [len(p) for p in prompts]
+    h = forward(c, torch.cat(prompts), c.extend([0, 1, 2], n), n, [0, 1, 2])
+    ends = (torch.tensor(n, device=DEV).cumsum(0) - 1)
+    parents, children = [i for i in range(3) for _ in range(per)], list(range(3, 3 + 3 * per))
+    tbik.cache_fork(c.pages, c.scales, c.table, c.lens, c.refs, i32(parents), i32(children))
+    c.book.fork(parents, children)
+    tbik.cache_free(c.table, c.lens, c.refs, i32([0, 1, 2]), page=page)
+    c.book.free([0, 1, 2])
+    c.check()
+    us = torch.rand(steps + 1, len(children), device=DEV, generator=g)
+    tok = choose(h[ends][torch.tensor(parents, device=DEV)], us[0])
+    seqs = [[p.tolist() for p in prompts][i] + [t] for i, t in zip(parents, tok.tolist())]
+    live, hidden = list(children), {}
+    for s in range(steps):
+        if s == 7:  # two sequences end
+            for r in (live[1], live[5]):
+                tbik.cache_free(c.table, c.lens, c.refs, i32([r]), page=page)
+                c.book.free([r])
+            live = [r for i, r in enumerate(live) if i not in (1, 5)]
+            assert tbik.cache_compact(c.pages, c.scales, c.table, c.lens, c.refs).item() == c.book.compact()[0]
+            c.check()
+        start = c.extend(live, [1] * len(live))
+        h = forward(c, torch.tensor([seqs[r - 3][-1] for r in live], device=DEV), start, [1] * len(live), live)
+        tok = choose(h, us[s + 1][torch.tensor([r - 3 for r in live], device=DEV)].contiguous())
+        for r, t, x in zip(live, tok.tolist(), h):
+            seqs[r - 3].append(t)
+            hidden[r, len(seqs[r - 3]) - 2] = x
+    assert tbik.get_error() == tbik.TBIK_OK
+    # the replay: every sequence by itself, never forked, in other slots and pages; its tokens in the same steps, since a
+    # page's scale grows while it fills and a query sees the page as it is at its time
+    for i, r in enumerate(live):
+        one = Cache(3, 20, 40, H, D, page, layers=L)
+        prompt = prompts[parents[r - 3]]
+        m = len(prompt)
+        h = forward(one, prompt, one.extend([2], [m]), [m], [2])
+        u = us[:, r - 3]
+        assert choose(h[-1:], u[:1].contiguous()).item() == seqs[r - 3][m]
+        for pos in range(m, len(seqs[r - 3]) - 1):
+            h = forward(one, torch.tensor([seqs[r - 3][pos]], device=DEV), one.extend([2], [1]), [1], [2])
+            assert torch.equal(h[0], hidden[r, pos])
+            assert choose(h, u[pos - m + 1:pos - m + 2].contiguous()).item() == seqs[r - 3][pos + 1]
+        n_tok = len(seqs[r - 3]) - 1
+        for l in range(L):
+            assert np.array_equal(c.stored(r, n_tok, l), one.stored(2, n_tok, l))
+    assert tbik.get_error() == tbik.TBIK_OK
