@@ -499,7 +499,8 @@ TBIK_API tbik_status tbik_cache_copy(uint8_t* pages, float* scales, const int32_
  *   scale: the smallest with max |round4| <= 448 * 2^E over the tokens the page
  *   holds so far, E >= -100.
  * When a token raises E, the page's older bytes are cut again under the larger
- * scale.  A page's contents therefore depend on its tokens only, not on how
+ * scale (a query that ran before saw them under the smaller one: a replay that
+ * wants its bits writes and attends in the same steps).  A page's contents therefore depend on its tokens only, not on how
  * they were split into calls.  Bytes of positions that no token has reached
  * stay as they are.  Infinities are stored as +-448 * 2^E and NaN as 0, neither
  * counts for E, and TBIK_ERR_VALUE is recorded.  A page that is not in the
@@ -522,12 +523,17 @@ TBIK_API tbik_status tbik_cache_append(const uint16_t* k, const uint16_t* v, uin
  * combined by TREE over the ceil((i+1)/128) leaves like in tbik_attention_tc.
  * A row's bits depend on its query and on the cache's contents at positions
  * 0..i, not on the batch, the other queries, page numbers or the device's load.
- * Checked against the binary64 definition by tolerance.
+ * The weights are rounded to 2^-9 relative, or 2^-18 of the leaf's largest times
+ * the ratio of its value scales, the output once; checked against the binary64
+ * definition by tolerance.
  *   max_q     no sequence has more than max_q new tokens
  *   max_keys  no query sees more than max_keys keys (start[b] + n_b <= max_keys)
  * Rows of sequences with start[b] < 0, beyond max_q or max_keys, or with a page
- * number outside the pool are NaN, the latter three with TBIK_ERR_PAGE.  Tokens
- * outside every sequence's range are left as they are.  out may alias q.
+ * number outside the pool are NaN, the latter three with TBIK_ERR_PAGE; a range
+ * cu[b] .. cu[b+1] outside the tokens is passed over with TBIK_ERR_POSITION.
+ * Tokens outside every sequence's range are left as they are.  Bytes at positions
+ * that a row does not see leave it alone, whatever they hold.  Sequences may name
+ * the same slot.  out may alias q.
  * ws: tbik_cache_attention_workspace() bytes, not shared by concurrent calls.
  */
 TBIK_API size_t tbik_cache_attention_workspace(int tokens, int batch, int max_q, int max_keys, int heads, int kv_heads,

@@ -104,7 +104,11 @@ struct CacheAppendParams {
 
 // One block per (page that a sequence's new tokens touch, kv head, keys or values): the page's new tokens are read
 // once into registers (16-byte loads, CH of them in flight per thread), their largest magnitude fixes the scale, and
-// the bytes go out 8 at a time (two tokens of a warp fill a 32-byte sector).
+// the bytes go out 8 at a time (two tokens of a warp fill a 32-byte sector).  The tokens are asked for before the page is
+// looked up, so that the chain of loads is sequence, start, tokens.  Bound by integer instructions (about six per value
+// for rounding, cutting, sign and packing) ahead of HBM: 32 prompts of 100 to 4096 tokens, 8 heads of 128 dims, 58 us,
+// 3.9 TB/s.  128 threads with eight loads each measured 58 us there, 256 with four 65 us.  A decode step (one token each:
+// one warp per token, head and operand) takes 2.8 us for 64 sequences.
 //
 // Which page a block has: sequence b's pages start at virtual index cu[b] / page + 2 b.  n tokens touch at most
 // n / page + 2 pages, so the ranges do not overlap, and the grid is known without reading `start`.
@@ -576,7 +580,8 @@ constexpr int CACHE_MOVE_THREADS = 256;
 constexpr int CACHE_MOVE_BYTES = CACHE_MOVE_THREADS * 16 * 4;  // bytes of one step of a block
 
 // The data of the moves in every layer's keys and values: blocks take 16 KB pieces in turn, four 16-byte loads in
-// flight per thread.
+// flight per thread.  Bound by HBM: 5.6 TB/s read and written for the moves of a pool of 2048 pages, 60 % live (4 layers,
+// 8 heads of 128 dims, pages of 32: 47 us).
 __device__ __forceinline__ void move_pages(const CacheMoveParams& p) {
     const int count = p.ws[0];
     const int2* moves = reinterpret_cast<const int2*>(p.ws) + 1;

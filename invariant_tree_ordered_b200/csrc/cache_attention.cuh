@@ -20,15 +20,23 @@
 // its 128 rows (measured: scores as K h + K l, l in e5m2, took four long contexts from 108 to 154 us).
 // Combining two summaries: M = max, e = 2^(m - M) (1 for the side that holds M), s = fma(s', e', s e), o likewise.
 //
-// One CTA works on tiles of R = RW * NWG rows (query, head) that share a kv head and a 128-position block, hence the
-// number of leaves.  Warp 0 copies pages to shared memory (cp.async.bulk, one copy per page and operand), warp 1 issues
-// the MMAs, and each group of 4 warps has RW rows: a thread is a key for the scores and a dim for the values, so its
-// summaries' value parts live in its TMEM lane (pending ones too).
+// A CTA works on tiles of R rows (query, head) that share a kv head and a 128-position block, hence the number of leaves.
+// Warp 0 copies pages to shared memory (cp.async.bulk, one copy per page and operand), warp 1 issues the MMAs, and four
+// warps do the rest: a thread is a key for the scores and a dim for the values, so its summaries' value parts live in its
+// TMEM lane (pending ones too).
 //
 // Split: the work is cut into units (tile, tree node of at most T leaves) and each CTA takes a contiguous run of them
 // by weight; T is chosen on the device such that a CTA has about CATT_UNITS units.  A tile whose tree is cut leaves its
 // nodes' summaries in the workspace, and a second kernel evaluates the tree above them.  Nodes are subtrees of the row's
 // own tree, so the bits do not depend on the cut.
+//
+// What bounds it.  Few rows over long contexts: the cache's bytes (4 sequences of 120-131 thousand positions, 32 query and
+// 4 kv heads of 128 dims: 111 us with both kernels, 4.7 TB/s; under a profiler the first kernel's DRAM reads are the
+// cache's bytes and nothing more).  Mixed batches: the chain of a leaf (scores, maximum over four warps, weights, values,
+// tree: 3.7 thousand cycles alone, 6.5 with three CTAs on an SM) and the 10 us of planning, first loads and the second
+// kernel (64 sequences of 1 to 8192 positions: 53 us, 18 us of bytes).  Many rows: the same chain's instructions, about
+// 30 per row, key and lane (chunks of 300-512 queries over 5-8 thousand positions: 0.87 ms, 198 TFLOP/s); issue slots are
+// 40 % used, the tensor pipe 3 to 10 %.
 #pragma once
 
 #include <cuda_fp16.h>
@@ -38,8 +46,11 @@
 namespace tbik {
 
 constexpr int CATT_LEAF = 128;
-constexpr int CATT_START = 2;       // weight of a unit's start, in leaves
-constexpr int CATT_UNITS = 3;       // units per CTA that the split aims at
+// Units per CTA that the split aims at, and the weight of a unit's start in leaves.  Units of 1, 2, 3, 4 per CTA took
+// 137, 117, 110, 108 us for four long contexts and 53, 56, 57, 58 us for a mixed batch; starts of 1, 2, 3, 5 leaves 54,
+// 52, 56, 54 us for that batch and the same for the others.
+constexpr int CATT_UNITS = 3;
+constexpr int CATT_START = 2;
 constexpr int CATT_JOIN_DEPTH = 4;  // levels above the units that one thread of the second kernel evaluates alone
 
 struct CacheAttParams {
@@ -67,34 +78,33 @@ struct CacheAttParams {
     unsigned debug;
 };
 
-template <int D_, int RW_, int NWG_>
+template <int D_, int R_>
 struct CattCfg {
-    static constexpr int D = D_, RW = RW_, NWG = NWG_, R = RW * NWG;
-    static constexpr int NC = 2 * RW;                // columns of S and of O
-    static constexpr int SBUF = RW == 32 ? 1 : 2, OBUF = RW == 32 ? 1 : 2;
-    static constexpr int PENDING = RW == 32 && NWG == 1 ? 5 : 6;  // summaries that can wait: log2 of the leaves of a unit
+    static constexpr int D = D_, R = R_;
+    static constexpr int NC = 2 * R;                // columns of S and of O
+    static constexpr int SBUF = R == 32 ? 1 : 2, OBUF = SBUF;
+    static constexpr int PENDING = R == 32 ? 5 : 6;  // summaries that can wait: log2 of the leaves of a unit
     static constexpr int MAX_NODE = 1 << PENDING;
-    static constexpr int TPEND = RW == 32 ? 4 : 6;   // of them in TMEM; the largest ones may be in shared memory
+    static constexpr int TPEND = R == 32 ? 4 : 6;   // of them in TMEM; the largest ones may be in shared memory
     static constexpr int S_COL = 0, O_COL = SBUF * NC, ST_COL = O_COL + OBUF * NC;
-    static constexpr int WG_COLS = ST_COL + TPEND * RW;
-    static constexpr int COLS = NWG * WG_COLS <= 128 ? 128 : NWG * WG_COLS <= 256 ? 256 : 512;
-    static_assert(NWG * WG_COLS <= 512, "TMEM columns");
-    static constexpr int CTAS = RW == 8 ? 3 : NWG == 1 ? 2 : 1;
-    static constexpr int THREADS = 64 + 128 * NWG;
+    static constexpr int COLS = R == 8 ? 128 : 256;
+    static constexpr int CTAS = R == 8 ? 3 : 2;      // that an SM holds
+    static_assert(ST_COL + TPEND * R <= COLS && COLS * CTAS <= 512, "TMEM columns");
+    static constexpr int THREADS = 192;
     static constexpr int TILE = 128 * D;             // bytes of a leaf's keys or values
-    static constexpr int STAGES = NWG == 2 ? (D == 64 ? 4 : 3) : RW == 16 && D == 128 ? 3 : D == 64 ? 4 : 2;
+    static constexpr int STAGES = D == 64 ? 4 : R == 16 ? 3 : 2;
     static constexpr int OFF_K = 0, OFF_V = STAGES * TILE, OFF_Q = 2 * STAGES * TILE;
     static constexpr int QB = NC * D, PB = 128 * NC;
-    static constexpr int OFF_P = OFF_Q + NWG * QB;
-    static constexpr int OFF_ST = OFF_P + NWG * PB;                          // the pending summaries that TMEM has no room for
-    static constexpr int OFF_BAR = OFF_ST + (TPEND < PENDING ? (PENDING - TPEND) * NWG * RW * 128 * 4 : 0);
+    static constexpr int OFF_P = OFF_Q + QB;
+    static constexpr int OFF_ST = OFF_P + PB;  // the pending summaries that TMEM has no room for
+    static constexpr int OFF_BAR = OFF_ST + (PENDING - TPEND) * R * 128 * 4;
     static constexpr int OFF_X = OFF_BAR + 512;
-    // per group of 4 warps, in floats: maxima [2][4][RW], sums [2][4][RW], constants [2][RW], value scales [2][8],
-    // and per warp: factors and rows [4][RW], pending (m, s) [PENDING][2][RW]
-    static constexpr int X_MAX = 0, X_SUM = 8 * RW, X_CST = 16 * RW, X_PV = 18 * RW, X_WARP = X_PV + 16;
-    static constexpr int X_PER_WARP = 4 * RW + PENDING * 2 * RW;
+    // in floats: maxima [2][4][R], sums [2][4][R], constants [2][R], value scales [2][8],
+    // and per warp: factors and rows [4][R], pending (m, s) [PENDING][2][R]
+    static constexpr int X_MAX = 0, X_SUM = 8 * R, X_CST = 16 * R, X_PV = 18 * R, X_WARP = X_PV + 16;
+    static constexpr int X_PER_WARP = 4 * R + PENDING * 2 * R;
     static constexpr int X_FLOATS = X_WARP + 4 * X_PER_WARP;
-    static constexpr int SMEM = OFF_X + NWG * X_FLOATS * 4;
+    static constexpr int SMEM = OFF_X + X_FLOATS * 4;
     static_assert(SMEM <= 230000, "shared memory");
 };
 
@@ -559,35 +569,28 @@ __device__ __forceinline__ void catt_factors(float am, float bm, float& M, float
     eb = bm == M ? 1.0f : ex2_hw(bm - M);
 }
 
-template <int D, int RW, int NWG>
-__global__ void __launch_bounds__(CattCfg<D, RW, NWG>::THREADS, CattCfg<D, RW, NWG>::CTAS) cache_attention_kernel(const __grid_constant__ CacheAttParams p) {
-    using C = CattCfg<D, RW, NWG>;
-    constexpr int R = C::R, ST = C::STAGES;
+template <int D, int R>
+__global__ void __launch_bounds__(CattCfg<D, R>::THREADS, CattCfg<D, R>::CTAS) cache_attention_kernel(const __grid_constant__ CacheAttParams p) {
+    using C = CattCfg<D, R>;
+    constexpr int ST = C::STAGES;
     extern __shared__ __align__(1024) uint8_t smem[];
     __shared__ CattPlan plan;
     __shared__ CattScan scan_buf[16];
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
     uint64_t *kf = bars, *ke = bars + ST, *vf = bars + 2 * ST, *ve = bars + 3 * ST;  // [ST] landed, MMAs retired
-    uint64_t* wb = bars + 4 * ST;  // per group: s_full[2] s_empty[2] o_full[2] o_empty[2] p_full q_full
-    uint64_t* done = wb + 10 * NWG;
-    uint64_t* clean = done + 1;  // values behind the last key zeroed by every group
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(clean + 1);
+    uint64_t* b = bars + 4 * ST;   // s_full[2] s_empty[2] o_full[2] o_empty[2] p_full q_full
+    uint64_t* done = b + 10;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-    static_assert((4 * ST + 10 * NWG + 3) * 8 <= 512, "barriers");
+    static_assert((4 * ST + 12) * 8 <= 512, "barriers");
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint64_t lim = p.wait_cycles;
     if (threadIdx.x == 0) {
 #pragma unroll 1
         for (int i = 0; i < 4 * ST; ++i) mbar_init(&bars[i], 1);
 #pragma unroll 1
-        for (int w = 0; w < NWG; ++w)
-#pragma unroll 1
-            for (int i = 0; i < 10; ++i) {
-                const bool by_warps = i == 2 || i == 3 || i >= 6;
-                mbar_init(&wb[10 * w + i], by_warps ? 4 : 1);
-            }
+        for (int i = 0; i < 10; ++i) mbar_init(&b[i], i == 2 || i == 3 || i >= 6 ? 4 : 1);  // what four warps report
         mbar_init(done, 1);
-        mbar_init(clean, 4 * NWG);
         *abort_flag = 0;
         fence_barrier_init();
     }
@@ -661,21 +664,17 @@ __global__ void __launch_bounds__(CattCfg<D, RW, NWG>::THREADS, CattCfg<D, RW, N
             auto values = [&](uint32_t x) -> bool {
                 const int st = x % ST;
                 if (!catt_wait(&vf[st], (x / ST) & 1, abort_flag, lim)) return false;
-#pragma unroll 1
-                for (int w = 0; w < NWG; ++w) {
-                    uint64_t* b = wb + 10 * w;
-                    const uint32_t ob = x % C::OBUF, use = x / C::OBUF;
-                    if (!catt_wait(&b[8], x & 1, abort_flag, lim)) return false;
-                    if (use > 0 && !catt_wait(&b[6 + ob], (use - 1) & 1, abort_flag, lim)) return false;
-                    tc_fence_after();
-                    const uint32_t pa = smem_u32(smem + C::OFF_P + w * C::PB);
+                const uint32_t ob = x % C::OBUF, use = x / C::OBUF;
+                if (!catt_wait(&b[8], x & 1, abort_flag, lim)) return false;
+                if (use > 0 && !catt_wait(&b[6 + ob], (use - 1) & 1, abort_flag, lim)) return false;
+                tc_fence_after();
+                const uint32_t pa = smem_u32(smem + C::OFF_P);
 #pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        tc_mma_f8(tmem + w * C::WG_COLS + C::O_COL + ob * C::NC,
-                                  smem_desc_flat(smem_u32(smem + C::OFF_V + st * C::TILE) + k * 32 * D, D * 8, 128),
-                                  smem_desc_flat(pa + k * 32 * C::NC, 8 * C::NC, 128), id_o, k ? 1u : 0u);
-                    tc_commit(&b[4 + ob]);
-                }
+                for (int k = 0; k < 4; ++k)
+                    tc_mma_f8(tmem + C::O_COL + ob * C::NC,
+                              smem_desc_flat(smem_u32(smem + C::OFF_V + st * C::TILE) + k * 32 * D, D * 8, 128),
+                              smem_desc_flat(pa + k * 32 * C::NC, 8 * C::NC, 128), id_o, k ? 1u : 0u);
+                tc_commit(&b[4 + ob]);
                 tc_commit(&ve[st]);
                 return true;
             };
@@ -687,20 +686,16 @@ __global__ void __launch_bounds__(CattCfg<D, RW, NWG>::THREADS, CattCfg<D, RW, N
                 for (int l = 0; l < u.size; ++l, ++g) {
                     const int st = g % ST;
                     if (!catt_wait(&kf[st], (g / ST) & 1, abort_flag, lim)) goto mma_out;
-#pragma unroll 1
-                    for (int w = 0; w < NWG; ++w) {
-                        uint64_t* b = wb + 10 * w;
-                        const uint32_t sb = g % C::SBUF, use = g / C::SBUF;
-                        if (l == 0 && fresh && !catt_wait(&b[9], nq & 1, abort_flag, lim)) goto mma_out;
-                        if (use > 0 && !catt_wait(&b[2 + sb], (use - 1) & 1, abort_flag, lim)) goto mma_out;
-                        tc_fence_after();
-                        const uint32_t qa = smem_u32(smem + C::OFF_Q + w * C::QB), ka = smem_u32(smem + C::OFF_K + st * C::TILE);
+                    const uint32_t sb = g % C::SBUF, use = g / C::SBUF;
+                    if (l == 0 && fresh && !catt_wait(&b[9], nq & 1, abort_flag, lim)) goto mma_out;
+                    if (use > 0 && !catt_wait(&b[2 + sb], (use - 1) & 1, abort_flag, lim)) goto mma_out;
+                    tc_fence_after();
+                    const uint32_t qa = smem_u32(smem + C::OFF_Q), ka = smem_u32(smem + C::OFF_K + st * C::TILE);
 #pragma unroll
-                        for (int k = 0; k < D / 32; ++k)
-                            tc_mma_f8(tmem + w * C::WG_COLS + C::S_COL + sb * C::NC, smem_desc_flat(ka + k * 256, 128, D * 8),
-                                      smem_desc_flat(qa + k * 256, 128, D * 8), id_s, k ? 1u : 0u);
-                        tc_commit(&b[0 + sb]);
-                    }
+                    for (int k = 0; k < D / 32; ++k)
+                        tc_mma_f8(tmem + C::S_COL + sb * C::NC, smem_desc_flat(ka + k * 256, 128, D * 8),
+                                  smem_desc_flat(qa + k * 256, 128, D * 8), id_s, k ? 1u : 0u);
+                    tc_commit(&b[0 + sb]);
                     if (l == 0 && fresh) ++nq;
                     tc_commit(&ke[st]);
                     if (g > 0 && !values(g - 1)) goto mma_out;
@@ -714,31 +709,30 @@ __global__ void __launch_bounds__(CattCfg<D, RW, NWG>::THREADS, CattCfg<D, RW, N
         __syncwarp();
     } else {
         // ---------------------------------------------------- scores, weights, summaries
-        const int wg = (warp - 2) >> 2, qd = warp & 3, tid = qd * 32 + lane;  // tid: TMEM lane = key = dim
-        uint64_t* b = wb + 10 * wg;
-        float* x = reinterpret_cast<float*>(smem + C::OFF_X) + wg * C::X_FLOATS;
+        const int qd = warp & 3, tid = qd * 32 + lane;  // tid: TMEM lane = key = dim
+        float* x = reinterpret_cast<float*>(smem + C::OFF_X);
         float* xw = x + C::X_WARP + qd * C::X_PER_WARP;   // this warp's own
-        float *fac = xw, *ofac = xw + RW;                 // [RW] factors of a step
-        float *rmax = xw + 2 * RW, *rval = xw + 3 * RW;   // [RW] a row's -m c, and 256 / its largest value scale
-        float2* pend = reinterpret_cast<float2*>(xw + 4 * RW);  // [PENDING][RW] (m, s)
-        const uint32_t tm = tmem + wg * C::WG_COLS + ((uint32_t)(qd * 32) << 16);
-        uint8_t* qs = smem + C::OFF_Q + wg * C::QB;
-        uint8_t* ps = smem + C::OFF_P + wg * C::PB;
-        float* overflow = reinterpret_cast<float*>(smem + C::OFF_ST) + (size_t)wg * RW * 128 + tid;  // [PENDING - TPEND][NWG][RW][128]
+        float *fac = xw, *ofac = xw + R;                 // [R] factors of a step
+        float *rmax = xw + 2 * R, *rval = xw + 3 * R;   // [R] a row's -m c, and 256 / its largest value scale
+        float2* pend = reinterpret_cast<float2*>(xw + 4 * R);  // [PENDING][R] (m, s)
+        const uint32_t tm = tmem + ((uint32_t)(qd * 32) << 16);
+        uint8_t* qs = smem + C::OFF_Q;
+        uint8_t* ps = smem + C::OFF_P;
+        float* overflow = reinterpret_cast<float*>(smem + C::OFF_ST) + tid;  // [PENDING - TPEND][R][128]
         const bool has_dim = tid < D;
-        const int bar = 1 + wg;
+        const int bar = 1;
         bool ab = false;
 
         // Queries of a unit's rows as two e4m3 terms each, and their constants c.
         auto load_q = [&](const CattUnits<R>& un, uint32_t nq) {
             constexpr int TPR = D / 8, RPP = 128 / TPR;  // threads per row, rows per pass
-            float* cst = x + C::X_CST + (nq & 1) * RW;
+            float* cst = x + C::X_CST + (nq & 1) * R;
             const int part = tid % TPR;
 #pragma unroll
-            for (int r0 = 0; r0 < RW; r0 += RPP) {
+            for (int r0 = 0; r0 < R; r0 += RPP) {
                 const int r = r0 + tid / TPR;
-                const int fr = un.tau * R + wg * RW + r;
-                const bool live = r < RW && fr < un.it.rows;
+                const int fr = un.tau * R + r;
+                const bool live = r < R && fr < un.it.rows;
                 uint4 w = make_uint4(0, 0, 0, 0);
                 if (live) {
                     const int t = catt_div(p, fr), hd = un.h * p.group + fr - t * p.group;
@@ -764,10 +758,10 @@ __global__ void __launch_bounds__(CattCfg<D, RW, NWG>::THREADS, CattCfg<D, RW, N
                     lo[k] = pack_e4m3(__fmul_rn(__fsub_rn(y0, z.x), 32.0f), __fmul_rn(__fsub_rn(y1, z.y), 32.0f));
                     if (top >= 0x7f80u) hi[k] = 0x7f7fu;  // not finite: the row's result is NaN
                 }
-                if (r < RW) {
+                if (r < R) {
                     const int at = (r & 7) * 16 + (part >> 1) * 128 + (part & 1) * 8;
                     *reinterpret_cast<uint2*>(qs + (r >> 3) * (D * 8) + at) = make_uint2(hi[0] | hi[1] << 16, hi[2] | hi[3] << 16);
-                    *reinterpret_cast<uint2*>(qs + ((RW + r) >> 3) * (D * 8) + at) = make_uint2(lo[0] | lo[1] << 16, lo[2] | lo[3] << 16);
+                    *reinterpret_cast<uint2*>(qs + ((R + r) >> 3) * (D * 8) + at) = make_uint2(lo[0] | lo[1] << 16, lo[2] | lo[3] << 16);
                     if (part == 0) cst[r] = top >= 0x7f80u ? 1.0f : __fmul_rn(cache_pow2(e - 7), p.scale);
                 }
             }
@@ -791,7 +785,7 @@ __global__ void __launch_bounds__(CattCfg<D, RW, NWG>::THREADS, CattCfg<D, RW, N
         // Lane k: how many nodes leaf k closes (low half), and leaf k + 32 (high half).
         auto pop_codes = [&](int size) { return catt_pops(size, min(lane, size - 1)) | catt_pops(size, min(lane + 32, size - 1)) << 16; };
 
-        uint32_t g = 0, nq = 0, cleaned = 0;  // leaves, tiles of queries, diagonal leaves
+        uint32_t g = 0, nq = 0;  // leaves, tiles of queries
         float prev_m = 0.0f, prev_o = 0.0f;  // lane = row: its maximum and the scale of its O
         int depth = 0;
         float cks = 0.0f, cvs = 0.0f;
@@ -807,34 +801,34 @@ __global__ void __launch_bounds__(CattCfg<D, RW, NWG>::THREADS, CattCfg<D, RW, N
         // The summary of leaf l of the unit (the CTA's leaf g1) enters the tree.
         auto tree_step = [&](uint32_t g1, int l) {
             const uint32_t ob = g1 % C::OBUF;
-            float* sums = x + C::X_SUM + (g1 & 1) * 4 * RW;
-            const int row = lane % RW;
+            float* sums = x + C::X_SUM + (g1 & 1) * 4 * R;
+            const int row = lane % R;
             float m = prev_m;
-            float s = __fadd_rn(__fadd_rn(sums[row], sums[RW + row]), __fadd_rn(sums[2 * RW + row], sums[3 * RW + row]));
+            float s = __fadd_rn(__fadd_rn(sums[row], sums[R + row]), __fadd_rn(sums[2 * R + row], sums[3 * R + row]));
             const int code = __shfl_sync(0xffffffffu, codes, l & 31);
             int pops = l < 32 ? code & 0xffff : code >> 16;
             const bool last = l + 1 == u.size;
             if (l == 0) depth = C::PENDING - (32 - __clz(max(u.size - 1, 0)));  // small trees stay in TMEM
             // O is in units of prev_o, a power of two: the first step multiplies it in
             float scale_o = prev_o;
-            float o[RW];
+            float o[R];
             if (has_dim) {
                 uint32_t raw[C::NC];
                 catt_ld<C::NC>(tm + C::O_COL + ob * C::NC, raw);
 #pragma unroll
-                for (int r = 0; r < RW; r += 2)
+                for (int r = 0; r < R; r += 2)
                     upk2(add2(pk2(__uint_as_float(raw[r]), __uint_as_float(raw[r + 1])),
-                              pk2(__uint_as_float(raw[RW + r]), __uint_as_float(raw[RW + r + 1]))), o[r], o[r + 1]);
+                              pk2(__uint_as_float(raw[R + r]), __uint_as_float(raw[R + r + 1]))), o[r], o[r + 1]);
             }
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&b[6 + ob]);
             if (pops == 0) {
-                if (lane < RW) ofac[lane] = scale_o;
+                if (lane < R) ofac[lane] = scale_o;
                 __syncwarp();
                 if (has_dim)
 #pragma unroll
-                    for (int r = 0; r < RW; r += 4) {
+                    for (int r = 0; r < R; r += 4) {
                         const float4 f = *reinterpret_cast<const float4*>(ofac + r);
                         upk2(mul2(pk2(o[r], o[r + 1]), pk2(f.x, f.y)), o[r], o[r + 1]);
                         upk2(mul2(pk2(o[r + 2], o[r + 3]), pk2(f.z, f.w)), o[r + 2], o[r + 3]);
@@ -843,27 +837,27 @@ __global__ void __launch_bounds__(CattCfg<D, RW, NWG>::THREADS, CattCfg<D, RW, N
 #pragma unroll 1
             for (; pops > 0; --pops) {
                 --depth;
-                const float2 a = pend[depth * RW + row];
+                const float2 a = pend[depth * R + row];
                 float M, ea, eb;
                 catt_factors(a.x, m, M, ea, eb);
                 s = __fmaf_rn(s, eb, __fmul_rn(a.y, ea));
                 m = M;
-                if (lane < RW) {
+                if (lane < R) {
                     fac[lane] = ea;
                     ofac[lane] = __fmul_rn(eb, scale_o);
                 }
                 scale_o = 1.0f;
                 __syncwarp();
                 if (has_dim) {
-                    uint32_t raw[RW];
+                    uint32_t raw[R];
                     if (C::TPEND < C::PENDING && depth < C::PENDING - C::TPEND) {
 #pragma unroll
-                        for (int r = 0; r < RW; ++r) raw[r] = __float_as_uint(overflow[(depth * NWG * RW + r) * 128]);
+                        for (int r = 0; r < R; ++r) raw[r] = __float_as_uint(overflow[(depth * R + r) * 128]);
                     } else {
-                        catt_ld<RW>(tm + C::ST_COL + (depth - (C::PENDING - C::TPEND)) * RW, raw);
+                        catt_ld<R>(tm + C::ST_COL + (depth - (C::PENDING - C::TPEND)) * R, raw);
                     }
 #pragma unroll
-                    for (int r = 0; r < RW; r += 4) {
+                    for (int r = 0; r < R; r += 4) {
                         const float4 fa = *reinterpret_cast<const float4*>(fac + r), fb = *reinterpret_cast<const float4*>(ofac + r);
                         upk2(fma2(pk2(o[r], o[r + 1]), pk2(fb.x, fb.y),
                                   mul2(pk2(__uint_as_float(raw[r]), __uint_as_float(raw[r + 1])), pk2(fa.x, fa.y))),
@@ -876,28 +870,28 @@ __global__ void __launch_bounds__(CattCfg<D, RW, NWG>::THREADS, CattCfg<D, RW, N
                 __syncwarp();
             }
             if (!last) {
-                if (lane < RW) pend[depth * RW + lane] = make_float2(m, s);
+                if (lane < R) pend[depth * R + lane] = make_float2(m, s);
                 if (has_dim) {
                     if (C::TPEND < C::PENDING && depth < C::PENDING - C::TPEND) {
 #pragma unroll
-                        for (int r = 0; r < RW; ++r) overflow[(depth * NWG * RW + r) * 128] = o[r];
+                        for (int r = 0; r < R; ++r) overflow[(depth * R + r) * 128] = o[r];
                     } else {
-                        catt_st<RW>(tm + C::ST_COL + (depth - (C::PENDING - C::TPEND)) * RW, o);
+                        catt_st<R>(tm + C::ST_COL + (depth - (C::PENDING - C::TPEND)) * R, o);
                     }
                 }
                 ++depth;
                 __syncwarp();
                 return;
             }
-            const int fr0 = u.tau * R + wg * RW, live = min(RW, u.it.rows - fr0);
+            const int fr0 = u.tau * R, live = min(R, u.it.rows - fr0);
             if (u.d == 0) {
-                if (lane < RW) ofac[lane] = __frcp_rn(s);
+                if (lane < R) ofac[lane] = __frcp_rn(s);
                 __syncwarp();
                 if (has_dim) {
                     int t = catt_div(p, fr0), hd = fr0 - t * p.group;
                     uint16_t* op = p.out + ((size_t)(u.it.tok0 + t) * p.heads + u.h * p.group) * D + tid;
 #pragma unroll
-                    for (int r = 0; r < RW; ++r) {
+                    for (int r = 0; r < R; ++r) {
                         if (r < live) op[hd * D] = f2bf(__fmul_rn(o[r], ofac[r]));
                         if (++hd == p.group) {
                             hd = 0;
@@ -910,14 +904,14 @@ __global__ void __launch_bounds__(CattCfg<D, RW, NWG>::THREADS, CattCfg<D, RW, N
                 if ((unsigned)slot >= (unsigned)p.max_slots) {
                     set_error(TBIK_ERR_WORKSPACE);
                 } else {
-                    if (qd == 0 && lane < RW) p.ms[(size_t)slot * R + wg * RW + lane] = make_float2(m, s);
+                    if (qd == 0 && lane < R) p.ms[(size_t)slot * R + lane] = make_float2(m, s);
                     if (has_dim) {
-                        float* op = p.o + ((size_t)slot * R + wg * RW) * D + tid;
+                        float* op = p.o + ((size_t)slot * R) * D + tid;
 #pragma unroll
-                        for (int r = 0; r < RW; ++r)
+                        for (int r = 0; r < R; ++r)
                             if (r < live) op[r * D] = o[r];
                     }
-                    if (u.v == 0 && wg == 0 && tid == 0) {
+                    if (u.v == 0 && tid == 0) {
                         int4* t = p.tiles + 2 * (size_t)(u.tile_base + u.h * u.tiles + u.tau);
                         t[0] = make_int4(slot, u.d, u.it.L, min(R, u.it.rows - u.tau * R));
                         t[1] = make_int4(u.it.tok0, u.tau * R, u.h, 0);
@@ -931,10 +925,10 @@ __global__ void __launch_bounds__(CattCfg<D, RW, NWG>::THREADS, CattCfg<D, RW, N
         for (bool more = any; more;) {
             CattUnits<R> nxt = u;
             const bool has_next = nxt.next(p);
-            const int fr0 = u.tau * R + wg * RW, i0 = u.it.i0 & 127;
+            const int fr0 = u.tau * R, i0 = u.it.i0 & 127;
             const int nmax = has_next ? nxt.imax(p) : 0;
-            const int row_i = (i0 + catt_div(p, fr0 + lane % RW)) & 127;  // lane = row: its position in the block
-            const float* cst = x + C::X_CST + (nq & 1) * RW;
+            const int row_i = (i0 + catt_div(p, fr0 + lane % R)) & 127;  // lane = row: its position in the block
+            const float* cst = x + C::X_CST + (nq & 1) * R;
             const bool fresh = has_next && !nxt.same_tile(u);  // other queries come next
 #pragma unroll 1
             for (int l = 0; l <= u.size; ++l) {
@@ -947,8 +941,8 @@ __global__ void __launch_bounds__(CattCfg<D, RW, NWG>::THREADS, CattCfg<D, RW, N
                 } else {
                     const bool last = l + 1 == u.size;
                     const uint32_t sb = g % C::SBUF;
-                    float a[RW];
-                    float* mx = x + C::X_MAX + (g & 1) * 4 * RW;
+                    float a[R];
+                    float* mx = x + C::X_MAX + (g & 1) * 4 * R;
                     float* pv = x + C::X_PV + (g & 1) * 8;
                     const bool diag = u.lo + l == u.it.L - 1;
                     if (!last) nid = key_page(u, imax, l + 1);
@@ -965,13 +959,13 @@ __global__ void __launch_bounds__(CattCfg<D, RW, NWG>::THREADS, CattCfg<D, RW, N
                         if (lane == 0) mbar_arrive(&b[2 + sb]);
                         const f2x k2 = pk2(cks, cks), i32 = pk2(0.03125f, 0.03125f);
 #pragma unroll
-                        for (int r = 0; r < RW; r += 2)
-                            upk2(mul2(fma2(pk2(__uint_as_float(raw[RW + r]), __uint_as_float(raw[RW + r + 1])), i32,
+                        for (int r = 0; r < R; r += 2)
+                            upk2(mul2(fma2(pk2(__uint_as_float(raw[R + r]), __uint_as_float(raw[R + r + 1])), i32,
                                            pk2(__uint_as_float(raw[r]), __uint_as_float(raw[r + 1]))), k2), a[r], a[r + 1]);
                         if (__any_sync(0xffffffffu, no_page)) {
                             if (no_page) {
 #pragma unroll
-                                for (int r = 0; r < RW; ++r) a[r] = __uint_as_float(0x7fc00000u);
+                                for (int r = 0; r < R; ++r) a[r] = __uint_as_float(0x7fc00000u);
                                 set_error(TBIK_ERR_PAGE);
                             }
                         }
@@ -980,17 +974,17 @@ __global__ void __launch_bounds__(CattCfg<D, RW, NWG>::THREADS, CattCfg<D, RW, N
                             // than tid, that is, if fr0 + r < (tid - i0) * group
                             const int hidden = (tid - i0) * p.group - fr0;
 #pragma unroll
-                            for (int r = 0; r < RW; ++r)
+                            for (int r = 0; r < R; ++r)
                                 if (r < hidden) a[r] = -INFINITY;
                         }
 #pragma unroll
-                        for (int r = 0; r < RW; r += 4) {
+                        for (int r = 0; r < R; r += 4) {
                             float4 m4;
                             m4.x = warp_max_f32(a[r]);
                             m4.y = warp_max_f32(a[r + 1]);
                             m4.z = warp_max_f32(a[r + 2]);
                             m4.w = warp_max_f32(a[r + 3]);
-                            if (lane == 0) *reinterpret_cast<float4*>(mx + qd * RW + r) = m4;
+                            if (lane == 0) *reinterpret_cast<float4*>(mx + qd * R + r) = m4;
                         }
                         if ((tid & (p.page - 1)) == 0) pv[tid >> p.page_shift] = cvs;
                     }
@@ -1000,25 +994,25 @@ __global__ void __launch_bounds__(CattCfg<D, RW, NWG>::THREADS, CattCfg<D, RW, N
                     if (last && fresh) load_q(nxt, nq + 1);
                     // lane = row: its maximum, and the largest value scale among its visible pages of the leaf
                     {
-                        const int row = lane % RW, i = diag ? row_i : 127;
+                        const int row = lane % R, i = diag ? row_i : 127;
                         const float4 v0 = *reinterpret_cast<const float4*>(pv), v1 = *reinterpret_cast<const float4*>(pv + 4);
                         const float v[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
                         float vm = v[0];
 #pragma unroll
                         for (int k = 1; k < 8; ++k)
                             if (k << p.page_shift <= i) vm = fmaxf(vm, v[k]);
-                        nm = __fmul_rn(fmaxf(fmax3(mx[row], mx[RW + row], mx[2 * RW + row]), mx[3 * RW + row]), cst[row]);
+                        nm = __fmul_rn(fmaxf(fmax3(mx[row], mx[R + row], mx[2 * R + row]), mx[3 * R + row]), cst[row]);
                         no = __fmul_rn(vm, 0.00390625f);
                         // 256 / vm: scales are powers of two
                         const float iv = __fmul_rn(256.0f, __uint_as_float((254u << 23) - __float_as_uint(vm)));
-                        if (lane < RW) {
+                        if (lane < R) {
                             rmax[lane] = -nm;
                             rval[lane] = iv;
                         }
                         __syncwarp();
                     }
 #pragma unroll
-                    for (int r = 0; r < RW; r += 4) {
+                    for (int r = 0; r < R; r += 4) {
                         const float4 c4 = *reinterpret_cast<const float4*>(cst + r), m4 = *reinterpret_cast<const float4*>(rmax + r);
                         float y[4];
                         upk2(fma2(pk2(a[r], a[r + 1]), pk2(c4.x, c4.y), pk2(m4.x, m4.y)), y[0], y[1]);
@@ -1026,16 +1020,16 @@ __global__ void __launch_bounds__(CattCfg<D, RW, NWG>::THREADS, CattCfg<D, RW, N
 #pragma unroll
                         for (int k = 0; k < 4; ++k) a[r + k] = ex2_hw(y[k]);
                     }
-                    float w[RW];  // 256 f p
+                    float w[R];  // 256 f p
                     if (!diag) {
                         const float f = __fmul_rn(cvs, rval[0]);
                         const f2x f2 = pk2(f, f);
 #pragma unroll
-                        for (int r = 0; r < RW; r += 2) upk2(mul2(pk2(a[r], a[r + 1]), f2), w[r], w[r + 1]);
+                        for (int r = 0; r < R; r += 2) upk2(mul2(pk2(a[r], a[r + 1]), f2), w[r], w[r + 1]);
                     } else {
                         // f <= 1 for a key that the row sees; for others p is 0
 #pragma unroll
-                        for (int r = 0; r < RW; ++r) w[r] = __fmul_rn(a[r], fminf(__fmul_rn(cvs, rval[r]), 256.0f));
+                        for (int r = 0; r < R; ++r) w[r] = __fmul_rn(a[r], fminf(__fmul_rn(cvs, rval[r]), 256.0f));
                     }
                     // P of the previous leaf is read until its O is there
                     if (l > 0 && !ab) {
@@ -1044,9 +1038,9 @@ __global__ void __launch_bounds__(CattCfg<D, RW, NWG>::THREADS, CattCfg<D, RW, N
                         ab = __any_sync(0xffffffffu, ab);
                     }
                     if (!ab) {
-                        uint32_t hi[RW / 4], lo[RW / 4];
+                        uint32_t hi[R / 4], lo[R / 4];
 #pragma unroll
-                        for (int r = 0; r < RW; r += 4) {
+                        for (int r = 0; r < R; r += 4) {
                             const uint32_t h0 = pack_e4m3(w[r], w[r + 1]), h1 = pack_e4m3(w[r + 2], w[r + 3]);
                             const float2 z0 = unpack_e4m3(h0), z1 = unpack_e4m3(h1);
                             hi[r / 4] = h0 | h1 << 16;
@@ -1054,13 +1048,13 @@ __global__ void __launch_bounds__(CattCfg<D, RW, NWG>::THREADS, CattCfg<D, RW, N
                                         pack_e4m3(__fsub_rn(w[r + 2], z1.x), __fsub_rn(w[r + 3], z1.y)) << 16;
                         }
                         uint8_t* dst = ps + (tid >> 3) * (8 * C::NC) + (tid & 7) * 16;  // 16 bytes per key and 16 columns
-                        if constexpr (RW == 8) {
+                        if constexpr (R == 8) {
                             *reinterpret_cast<uint4*>(dst) = make_uint4(hi[0], hi[1], lo[0], lo[1]);
                         } else {
 #pragma unroll
-                            for (int k = 0; k < RW / 16; ++k) {
+                            for (int k = 0; k < R / 16; ++k) {
                                 *reinterpret_cast<uint4*>(dst + k * 128) = make_uint4(hi[4 * k], hi[4 * k + 1], hi[4 * k + 2], hi[4 * k + 3]);
-                                *reinterpret_cast<uint4*>(dst + (RW / 16 + k) * 128) = make_uint4(lo[4 * k], lo[4 * k + 1], lo[4 * k + 2], lo[4 * k + 3]);
+                                *reinterpret_cast<uint4*>(dst + (R / 16 + k) * 128) = make_uint4(lo[4 * k], lo[4 * k + 1], lo[4 * k + 2], lo[4 * k + 3]);
                             }
                         }
                     }
@@ -1073,7 +1067,7 @@ __global__ void __launch_bounds__(CattCfg<D, RW, NWG>::THREADS, CattCfg<D, RW, N
                         if (!ab) {
                             if (tid > (u.imin(p) & 127)) {
                                 uint8_t* vt = smem + C::OFF_V + st * C::TILE + (tid >> 3) * (D * 8) + (tid & 7) * 16;
-                                for (int k = wg; k < D / 16; k += NWG) {
+                                for (int k = 0; k < D / 16; ++k) {
                                     uint4* at = reinterpret_cast<uint4*>(vt + k * 128);
                                     if (!seen || no_page) {
                                         *at = make_uint4(0, 0, 0, 0);
@@ -1088,26 +1082,19 @@ __global__ void __launch_bounds__(CattCfg<D, RW, NWG>::THREADS, CattCfg<D, RW, N
                                 }
                             }
                         }
-                        if (NWG > 1 && !ab) {  // each group has cleaned its share of the dims
-                            fence_proxy_async_smem();
-                            __syncwarp();
-                            if (lane == 0) mbar_arrive(clean);
-                            ab = !catt_wait(clean, cleaned++ & 1, abort_flag, lim);
-                            ab = __any_sync(0xffffffffu, ab);
-                        }
                     }
                     fence_proxy_async_smem();
                     __syncwarp();
                     if (lane == 0 && !ab && !(p.debug & TBIK_DEBUG_WITHHOLD_ACC_ARRIVE)) mbar_arrive(&b[8]);
                     // sums over the warp's 32 keys: halves 16, 8, 4, 2, 1 apart; the rows are dealt out on the way
                     {
-                        int n = RW;
+                        int n = R;
 #pragma unroll
                         for (int o = 16; o; o >>= 1) {
                             if (n > 1) {
                                 n >>= 1;
 #pragma unroll
-                                for (int k = 0; k < RW / 2; ++k)
+                                for (int k = 0; k < R / 2; ++k)
                                     if (k < n) {
                                         const float keep = (lane & o) ? a[k + n] : a[k], send = (lane & o) ? a[k] : a[k + n];
                                         a[k] = __fadd_rn(keep, __shfl_xor_sync(0xffffffffu, send, o));
@@ -1116,7 +1103,7 @@ __global__ void __launch_bounds__(CattCfg<D, RW, NWG>::THREADS, CattCfg<D, RW, N
                                 a[0] = __fadd_rn(a[0], __shfl_xor_sync(0xffffffffu, a[0], o));
                             }
                         }
-                        if (lane % (32 / RW) == 0) x[C::X_SUM + (g & 1) * 4 * RW + qd * RW + lane / (32 / RW)] = a[0];
+                        if (lane % (32 / R) == 0) x[C::X_SUM + (g & 1) * 4 * R + qd * R + lane / (32 / R)] = a[0];
                     }
                 }
                 if (l > 0 && !ab) {

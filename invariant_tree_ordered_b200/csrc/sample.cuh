@@ -21,6 +21,11 @@
 // A row that does not fit (the limit outside the bracket, too many tokens in a list, infinite logits, temperatures near
 // 0) takes the general steps: histograms of masses, the border bin split again on the bits of the logits until it
 // fits or all its logits are equal.
+//
+// Measured: 256 rows of 151936 fp32 logits, every row with its own settings, 165 us (an HBM read takes 24 us; at two blocks
+// an SM the row's steps are a chain of some 25 to 60 thousand cycles, of which the sweeps are half and the five meetings
+// of the cluster a quarter); one row 24 us; 97 rows of 32000 in bf16 34 us.  A row read again from memory by one block for
+// each sweep, without meetings, measured 172 us for the first and is not kept.
 #pragma once
 
 #include "device_common.cuh"

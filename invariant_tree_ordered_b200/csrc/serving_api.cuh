@@ -73,7 +73,7 @@ tbik_status check_attention(int tokens, int batch, int max_q, int max_keys, int 
 
 // Rows of a tile, grid and workspace of an attention call.
 struct CattSplit {
-    int rows;    // rows per tile: 8, 16, 32 or 64
+    int rows;    // rows per tile: 8, 16 or 32
     int blocks, grid, slots;
     size_t off_tiles, off_ms, off_o, bytes;
 };
@@ -84,11 +84,15 @@ tbik_status plan_cache_attention(int tokens, int batch, int max_q, int max_keys,
     if (tokens == 0 || batch == 0) return TBIK_OK;
     const int group = heads / kv_heads;
     const long long most = (long long)(max_q < tokens ? max_q : tokens) * group;  // rows of a sequence that share a kv head
-    c.rows = most <= 8 ? 8 : most <= 16 ? 16 : most <= 32 ? 32 : 64;
+    // The smallest tile that holds them, up to 32.  32 sequences of 8192 keys, 4 kv heads of 128 dims: 8 rows 78 us in
+    // tiles of 8 and 88 us in tiles of 16; 16 rows 61 us in tiles of 16, 76 us in tiles of 32 and 74 us in two of 8;
+    // 32 rows 125 us, 150 us in two tiles of 16.  (Tiles of 64 rows by eight warps in one block an SM instead of
+    // four warps in two were slower: 512 rows 1370 us against 1290 us.)
+    c.rows = most <= 8 ? 8 : most <= 16 ? 16 : 32;
     c.blocks = ((max_q < tokens ? max_q : tokens) + 126) / 128 + 1;
     const long long items = (long long)batch * c.blocks;
     if (items > (1 << 30)) return TBIK_ERR_SHAPE;
-    const int ctas = c.rows == 8 ? 3 : c.rows == 64 ? 1 : 2;
+    const int ctas = c.rows == 8 ? 3 : 2;
     const long long leaves = (max_keys + CATT_LEAF - 1) / CATT_LEAF;
     const long long tiles = (long long)kv_heads * ((long long)tokens * group / c.rows + (items < tokens ? items : tokens));
     const long long work = tiles * leaves;
@@ -111,19 +115,19 @@ tbik_status plan_cache_attention(int tokens, int batch, int max_q, int max_keys,
     return TBIK_OK;
 }
 
-template <int D, int RW, int NWG>
+template <int D, int R>
 tbik_status launch_cache_attention(const CacheAttParams& p, const CattSplit& c, const DeviceInfo* info, int dev, cudaStream_t s) {
-    using C = CattCfg<D, RW, NWG>;
+    using C = CattCfg<D, R>;
     static bool ready[kMaxDevices];
     {
         std::lock_guard<std::mutex> lk(g_mu);
         if (!ready[dev]) {
-            if (cudaFuncSetAttribute(cache_attention_kernel<D, RW, NWG>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) != cudaSuccess)
+            if (cudaFuncSetAttribute(cache_attention_kernel<D, R>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) != cudaSuccess)
                 return TBIK_ERR_CUDA;
             ready[dev] = true;
         }
     }
-    cache_attention_kernel<D, RW, NWG><<<c.grid, C::THREADS, C::SMEM, s>>>(p);
+    cache_attention_kernel<D, R><<<c.grid, C::THREADS, C::SMEM, s>>>(p);
     tbik_status st = launch_status();
     if (st != TBIK_OK || !c.slots) return st;
     // the second kernel's blocks may be set up while the first one ends; they wait for its results themselves
@@ -137,17 +141,16 @@ tbik_status launch_cache_attention(const CacheAttParams& p, const CattSplit& c, 
     at[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, cache_attention_join_kernel<D, C::R>, p) != cudaSuccess) return TBIK_ERR_CUDA;
+    if (cudaLaunchKernelEx(&cfg, cache_attention_join_kernel<D, R>, p) != cudaSuccess) return TBIK_ERR_CUDA;
     return launch_status();
 }
 
 template <int D>
 tbik_status dispatch_cache_attention(const CacheAttParams& p, const CattSplit& c, const DeviceInfo* info, int dev, cudaStream_t s) {
     switch (c.rows) {
-        case 8: return launch_cache_attention<D, 8, 1>(p, c, info, dev, s);
-        case 16: return launch_cache_attention<D, 16, 1>(p, c, info, dev, s);
-        case 32: return launch_cache_attention<D, 32, 1>(p, c, info, dev, s);
-        default: return launch_cache_attention<D, 32, 2>(p, c, info, dev, s);
+        case 8: return launch_cache_attention<D, 8>(p, c, info, dev, s);
+        case 16: return launch_cache_attention<D, 16>(p, c, info, dev, s);
+        default: return launch_cache_attention<D, 32>(p, c, info, dev, s);
     }
 }
 
@@ -155,6 +158,8 @@ template <typename T>
 tbik_status launch_sample(SampleParams& p, const DeviceInfo* info, int dev, cudaStream_t s) {
     // Blocks per row: as few as hold the row in 80 KB each, more (up to 8) while the device holds all of them at once (two
     // to an SM) and a block has at least 4096 tokens.
+    // 97 rows of 32000 in bf16: 37 us with one block each, 33 us with two, 39 us with four; 40 rows of 20000: 31 us with
+    // two, 29 us with four, 33 us with eight.
     int cl = 1;
     while (cl < SMP_MAX_CLUSTER && ((long long)p.vocab * (int)sizeof(T) > 80000LL * cl ||
                                     ((long long)p.batch * cl <= info->sms && p.vocab > 4096 * cl)))
