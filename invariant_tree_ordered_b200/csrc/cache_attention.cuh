@@ -1138,7 +1138,7 @@ __global__ void __launch_bounds__(CattCfg<D, R>::THREADS, CattCfg<D, R>::CTAS) c
 // ------------------------------------------------------------------ the tree above the units
 //
 // A group of D / 4 threads per row, four dims each.  Trees that are cut a few levels deep are one group's work; for deeper
-// ones (few rows over long contexts) the groups of a block take one subtree each.  Eight nodes are in flight at a time.
+// ones (few rows over long contexts) the groups of a block take one subtree each.  Several nodes are in flight at a time.
 // Empty nodes are passed over.
 
 constexpr int CATT_JOIN_THREADS = 256;
@@ -1172,29 +1172,28 @@ __device__ __forceinline__ CattSum catt_node_sum(const CacheAttParams& p, size_t
     return x;
 }
 
-// The tree over nodes v0 .. v0 + n - 1 (n a power of two) of a tile's 2^d; PEND: log2(n / 8) at most.
-template <int D, int R, int PEND>
+// The tree over nodes v0 .. v0 + n - 1 of a tile's 2^d, n a power of two, STEP nodes at a time (n a multiple of it);
+// PEND: log2(n / STEP) at most.
+template <int D, int R, int STEP, int PEND>
 __device__ __forceinline__ CattSum catt_join_nodes(const CacheAttParams& p, int slot, int L, int d, int v0, int n, int row, int part) {
     CattSum st[PEND + 1], r;
     r.any = false;
     int depth = 0;
-    const int step = min(n, 8);
 #pragma unroll 1
-    for (int v = 0; v < n; v += step) {
-        CattSum x[8];
+    for (int v = 0; v < n; v += STEP) {
+        CattSum x[STEP];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
+        for (int k = 0; k < STEP; ++k) {
             x[k].any = false;
-            if (k < step && catt_node_size(L, d, v0 + v + k)) x[k] = catt_node_sum(p, (size_t)(slot + v0 + v + k) * R + row, D, part);
+            if (catt_node_size(L, d, v0 + v + k)) x[k] = catt_node_sum(p, (size_t)(slot + v0 + v + k) * R + row, D, part);
         }
 #pragma unroll
-        for (int h = 1; h < 8; h <<= 1)
-            if (h < step)
+        for (int h = 1; h < STEP; h <<= 1)
 #pragma unroll
-                for (int k = 0; k + h < 8; k += 2 * h) x[k] = catt_join(x[k], x[k + h]);
+            for (int k = 0; k + h < STEP; k += 2 * h) x[k] = catt_join(x[k], x[k + h]);
         r = x[0];
-        for (int c = v / step; c & 1; c >>= 1) r = catt_join(st[--depth], r);
-        if (v + step < n) st[depth++] = r;
+        for (int c = v / STEP; c & 1; c >>= 1) r = catt_join(st[--depth], r);
+        if (v + STEP < n) st[depth++] = r;
     }
     return r;
 }
@@ -1202,7 +1201,7 @@ __device__ __forceinline__ CattSum catt_join_nodes(const CacheAttParams& p, int 
 template <int D, int R>
 __global__ void __launch_bounds__(CATT_JOIN_THREADS) cache_attention_join_kernel(const __grid_constant__ CacheAttParams p) {
     constexpr int LANES = D / 4, GROUPS = CATT_JOIN_THREADS / LANES;
-    static_assert((1 << CATT_JOIN_DEPTH) >= GROUPS, "deeper trees have a subtree for every group");
+    static_assert((2 << CATT_JOIN_DEPTH) >= 2 * GROUPS, "deeper trees have two nodes for every group");
     __shared__ CattSum sums[GROUPS][LANES];
     const int part = threadIdx.x % LANES, grp = threadIdx.x / LANES;
     asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -1227,7 +1226,12 @@ __global__ void __launch_bounds__(CATT_JOIN_THREADS) cache_attention_join_kernel
         const int4 t0 = p.tiles[2 * (w / R)], t1 = p.tiles[2 * (w / R) + 1];  // slot, d, L, rows; token, first row, kv head
         const int row = (int)(w % R);
         if (!sound(t0, t1) || row >= t0.w || t0.y > CATT_JOIN_DEPTH) continue;
-        put(t1, row, catt_join_nodes<D, R, 1>(p, t0.x, t0.z, t0.y, 0, 1 << t0.y, row, part));
+        if (t0.y == 1)
+            put(t1, row, catt_join_nodes<D, R, 2, 0>(p, t0.x, t0.z, 1, 0, 2, row, part));
+        else if (t0.y == 2)
+            put(t1, row, catt_join_nodes<D, R, 4, 0>(p, t0.x, t0.z, 2, 0, 4, row, part));
+        else
+            put(t1, row, catt_join_nodes<D, R, 8, CATT_JOIN_DEPTH - 3>(p, t0.x, t0.z, t0.y, 0, 1 << t0.y, row, part));
     }
     if (!deep) return;
 #pragma unroll 1
@@ -1235,8 +1239,10 @@ __global__ void __launch_bounds__(CATT_JOIN_THREADS) cache_attention_join_kernel
         const int4 t0 = p.tiles[2 * (w / R)], t1 = p.tiles[2 * (w / R) + 1];
         const int row = (int)(w % R);
         if (!sound(t0, t1) || row >= t0.w || t0.y <= CATT_JOIN_DEPTH) continue;  // the same for the whole block
+        // as many nodes for each group: 4 (8 groups) or 2 (16 groups) at least
+        constexpr int LEAST = (2 << CATT_JOIN_DEPTH) / GROUPS;
         const int per = (1 << t0.y) / GROUPS;
-        const CattSum r = catt_join_nodes<D, R, 14>(p, t0.x, t0.z, t0.y, grp * per, per, row, part);
+        const CattSum r = catt_join_nodes<D, R, LEAST, 14>(p, t0.x, t0.z, t0.y, grp * per, per, row, part);
         __syncthreads();
         sums[grp][part] = r;
         __syncthreads();
