@@ -170,9 +170,12 @@ def _need_out(t, dtype, shape, name="out"):
 
 
 def _need(t, dtype, name):
+    try:
+        if t.is_cuda and t.dtype is dtype and t.is_contiguous():
+            return
+    except AttributeError:
+        pass
     torch = _torch()
-    if isinstance(t, torch.Tensor) and t.is_cuda and t.dtype is dtype and t.is_contiguous():
-        return
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
     if t.dtype != dtype:
@@ -577,14 +580,13 @@ def _pool(pages, scales, layered):
     torch = _torch()
     _need(pages, torch.float8_e4m3fn, "pages")
     _need(scales, torch.float32, "scales")
-    s = pages.shape
-    if not layered:
-        s = (1, *s)
-    if len(s) != 8 or s[1] != 2 or s[6] != 8 or s[7] != 16:
+    s, c, k = pages.shape, scales.shape, 1 if layered else 0
+    if len(s) != 7 + k or s[k] != 2 or s[k + 5] != 8 or s[k + 6] != 16:
         raise ValueError("pages must be [%s2, num_pages, kv_heads, page/8, head_dim/16, 8, 16]" % ("layers, " if layered else ""))
-    if scales.shape != pages.shape[:-4]:
+    layers, num_pages, kv_heads = s[0] if layered else 1, s[k + 1], s[k + 2]
+    if len(c) != 3 + k or c[k] != 2 or c[k + 1] != num_pages or c[k + 2] != kv_heads or (layered and c[0] != layers):
         raise ValueError("scales must be [%s2, num_pages, kv_heads]" % ("layers, " if layered else ""))
-    return s[0], s[2], s[3], s[4] * 8, s[5] * 16
+    return layers, num_pages, kv_heads, s[k + 3] * 8, s[k + 4] * 16
 
 
 def _meta(table, lens, refs):
@@ -767,11 +769,11 @@ def cache_attention(q, pages, scales, table, start, *, cu=None, rows=None, max_q
             _attention_bytes[key] = nbytes
     if out is None:
         # tokens outside every sequence are left as they are: zeros in a new tensor
-        out = _new(q.shape, q.dtype, q.device, stream)
-        if cu is not None:
-            if stream is None:
-                out.zero_()
-            else:
+        if stream is None:
+            out = torch.empty_like(q) if cu is None else torch.zeros_like(q)
+        else:
+            out = _new(q.shape, q.dtype, q.device, stream)
+            if cu is not None:
                 with torch.cuda.stream(stream):
                     out.zero_()
     else:
