@@ -24,7 +24,7 @@
 //
 // Measured: 256 rows of 151936 fp32 logits, every row with its own settings, 165 us (an HBM read takes 24 us; at two blocks
 // an SM the row's steps are a chain of some 25 to 60 thousand cycles, of which the sweeps are half and the five meetings
-// of the cluster a quarter); one row 24 us; 97 rows of 32000 in bf16 34 us.  A row read again from memory by one block for
+// of the cluster a quarter); one row 24 us; 97 rows of 32000 in bf16 30 us.  A row read again from memory by one block for
 // each sweep, without meetings, measured 172 us for the first and is not kept.
 #pragma once
 
@@ -126,10 +126,12 @@ __device__ __forceinline__ uint4 ld_cluster_v4(uint32_t addr) {
     return v;
 }
 
+// Modulo 2^64, by three reductions of 32-bit integers: 22, 21 and 21 bits, 32 of which stay below 2^32.
 __device__ __forceinline__ unsigned long long warp_sum_u64(unsigned long long v) {
-#pragma unroll
-    for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-    return v;
+    const uint32_t a = __reduce_add_sync(0xffffffffu, (uint32_t)v & 0x3fffffu);
+    const uint32_t b = __reduce_add_sync(0xffffffffu, (uint32_t)(v >> 22) & 0x1fffffu);
+    const uint32_t c = __reduce_add_sync(0xffffffffu, (uint32_t)(v >> 43));
+    return a + ((unsigned long long)b << 22) + ((unsigned long long)c << 43);
 }
 
 template <typename T>
@@ -679,11 +681,13 @@ __device__ bool sample_fast(const SampleParams& p, SampleShared& sh, uint8_t* ra
         cluster_sync();
         total = sure = in = 0;
         bool fits = true;
-        for (uint32_t r = 0; r < cl; ++r) {
-            total += sh.from[r].total;
-            sure += sh.from[r].above;
-            in += sh.from[r].in;
-            fits &= sh.from[r].lists <= SMP_LIST;
+#pragma unroll
+        for (uint32_t r = 0; r < SMP_MAX_CLUSTER; ++r) {
+            const bool there = r < cl;
+            total += there ? sh.from[r].total : 0ull;
+            sure += there ? sh.from[r].above : 0ull;
+            in += there ? sh.from[r].in : 0ull;
+            fits &= !there || sh.from[r].lists <= SMP_LIST;
         }
         bool rest;
         unsigned long long limit = share_of(tp > 0.0f ? tp : 0.0f, total, rest);
@@ -796,8 +800,9 @@ __device__ bool sample_fast(const SampleParams& p, SampleShared& sh, uint8_t* ra
     }
     cluster_sync();  // the last access to another block's memory lies before this
     unsigned long long before = 0, all = 0, own = 0;
-    for (uint32_t r = 0; r < cl; ++r) {
-        const unsigned long long t = sh.from[r].kept;
+#pragma unroll
+    for (uint32_t r = 0; r < SMP_MAX_CLUSTER; ++r) {
+        const unsigned long long t = r < cl ? sh.from[r].kept : 0ull;
         if (r < rank) before += t;
         if (r == rank) own = t;
         all += t;
@@ -938,10 +943,12 @@ __global__ void __launch_bounds__(SMP_THREADS, 2) sample_kernel(const SamplePara
         }
         cluster_sync();
         m = -INFINITY;
-        for (uint32_t r = 0; r < cl; ++r) {
-            m = fmaxf(m, sh.from[r].max);
-            nan |= sh.from[r].nan != 0;
-        }
+#pragma unroll
+        for (uint32_t r = 0; r < SMP_MAX_CLUSTER; ++r)
+            if (r < cl) {
+                m = fmaxf(m, sh.from[r].max);
+                nan |= sh.from[r].nan != 0;
+            }
     }
     if (nan || m == -INFINITY) {  // nothing to choose from
         if (rank == 0 && tid == 0) {
