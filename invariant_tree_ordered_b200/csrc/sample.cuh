@@ -581,8 +581,10 @@ __device__ bool sample_fast(const SampleParams& p, SampleShared& sh, uint8_t* ra
     auto bin_of = [&](float z) { return (int)(__fmul_rn(__fsub_rn(__fmul_rn(__fsub_rn(m, z), scale), above), spread)); };
 #pragma unroll 1
     for (int c = 0; c < chunks; ++c) {
-        // weights below 2^-9: 2^32 w rounds to an integer in the addition of 2^23; 16 of them fit 27 bits.  Larger
-        // ones and those in the bracket (few) are set aside.
+        // units below 2^23 (weights below about 2^-9): 2^32 w rounds to an integer in the addition of 2^23; 16 of them
+        // fit 27 bits, and 32 lanes' 32.  Larger ones (their q is 2^23 or more, if not their units) and those in the
+        // bracket (few) are set aside.  The limit is on the rounded units: the largest weight below 2^-9 rounds up to
+        // 2^23 of them, and a warp full of it would sum to 2^32.
         uint32_t s_all = 0, s_up = 0, s_kept = 0, large = 0, between = 0;
 #pragma unroll
         for (int r = 0; r < ROUNDS; ++r) {
@@ -597,7 +599,7 @@ __device__ bool sample_fast(const SampleParams& p, SampleShared& sh, uint8_t* ra
                 for (int e = 0; e < PER; ++e) {
                     const float w = ws[e], y = __fmul_rn(__fsub_rn(m, z[e]), scale);
                     const uint32_t q = __float_as_uint(__fmaf_rn(w, 0x1p32f, 0x1p23f)) - 0x4b000000u;
-                    const bool up = y < above, mid = !up && y < inside && q, big = !mid && w >= 0x1p-9f;
+                    const bool up = y < above, mid = !up && y < inside && q, big = !mid && q >= 1u << 23;
                     if (mid) between |= 1u << (r * PER + e);
                     if (big) large |= 1u << (r * PER + e);
                     if (!mid && !big) s_all += q;
@@ -637,7 +639,7 @@ __device__ bool sample_fast(const SampleParams& p, SampleShared& sh, uint8_t* ra
                 ++first;
             }
         }
-        // 32 lanes x 16 values below 2^23: below 2^32
+        // 32 lanes x 16 values of at most 2^23 - 1: below 2^32
         unsigned long long t = __reduce_add_sync(0xffffffffu, s_kept);
         if (__any_sync(0xffffffffu, kept != 0)) t += warp_sum_u64(kept);
         if (lane == 0) sh.sweep[c][warp] = t;

@@ -225,3 +225,14 @@ def test_more_rows_than_the_device_holds(B, V, half):
     out = tbik.sample(z, f(uni(4, B), torch.float32), top_p=f(p, torch.float32))
     assert tbik.get_error() == tbik.TBIK_ERR_VALUE
     assert out[6].item() == -1 and out[8].item() == -1 and out[9].item() == 7
+
+
+@pytest.mark.parametrize("temp,back", [(0.97, -6.051175), (0.98, -6.1135583), (1.11, -6.9245405), (1.94, -12.10235)])
+@pytest.mark.parametrize("p", [None, 0.9])
+def test_a_background_of_2_to_the_minus_9(temp, back, p):
+    """Thousands of equal weights of 2^-9 - 2^-33 of the largest, which is 2^23 units: 512 of them are 2^32."""
+    V = 151936
+    z = torch.full((8, V), back, device=DEV)
+    z[:, 123] = 0.0
+    check(z, np.linspace(0.02, 0.98, 8), temp=temp, p=p)
+    assert tbik.get_error() == tbik.TBIK_OK
