@@ -430,7 +430,9 @@ TBIK_API tbik_status tbik_logprob_noalloc(const uint16_t* hidden, const uint16_t
  * Everything is device memory of the caller (tables and arrays start filled
  * with -1, 0 and 0).  Limits: slots <= 65536, num_pages <= 1048576, max_pages
  * <= 1048576, sequences per call <= 8192.  `rows` lists the slots of a call's
- * sequences; NULL means slot b for sequence b.  refs 16-byte aligned.
+ * sequences; NULL means slot b for sequence b.  pages, refs, k, v, q, out and
+ * the workspaces are 16-byte aligned, everything else to its elements (a
+ * layer's part of pages and scales is as good as the whole).
  *
  * The page operations are all or nothing: when an argument cannot be (a slot
  * out of range or named twice, a length that does not fit max_pages, too few

@@ -38,6 +38,9 @@ CacheMoveParams move_params(uint8_t* pages, float* scales, int layers, int num_p
     return p;
 }
 
+// Scales are read one by one, and one layer of a pool's scales starts at any multiple of 4 bytes.
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
 // Shared memory of a plan kernel: prefix sums over the call's sequences and a bit per slot.
 size_t plan_smem(int count, int slots) { return ((size_t)count + 1) * 4 + ((size_t)slots + 31) / 32 * 4; }
 
@@ -227,7 +230,7 @@ tbik_status tbik_cache_fork(uint8_t* pages, float* scales, int32_t* table, int32
     if ((st = check_data(layers, num_pages, kv_heads, head_dim, page)) != TBIK_OK) return st;
     if (count == 0) return TBIK_OK;
     if (!pages || !scales || !table || !lens || !refs || !parents || !children) return TBIK_ERR_ARG;
-    if (!aligned16(pages) || !aligned16(scales) || !aligned16(refs) || (ws && !aligned16(ws))) return TBIK_ERR_ALIGN;
+    if (!aligned16(pages) || !aligned4(scales) || !aligned16(refs) || (ws && !aligned16(ws))) return TBIK_ERR_ALIGN;
     if (!ws || ws_bytes < tbik_cache_fork_workspace(count)) return TBIK_ERR_WORKSPACE;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     const CacheMetaParams m = meta_params(table, lens, refs, slots, max_pages, num_pages, page);
@@ -270,7 +273,7 @@ tbik_status tbik_cache_compact(uint8_t* pages, float* scales, int32_t* table, co
     if ((st = check_meta(0, slots, max_pages, num_pages, page)) != TBIK_OK) return st;
     if ((st = check_data(layers, num_pages, kv_heads, head_dim, page)) != TBIK_OK) return st;
     if (!pages || !scales || !table || !lens || !refs || !live) return TBIK_ERR_ARG;
-    if (!aligned16(pages) || !aligned16(scales) || !aligned16(refs) || (ws && !aligned16(ws))) return TBIK_ERR_ALIGN;
+    if (!aligned16(pages) || !aligned4(scales) || !aligned16(refs) || (ws && !aligned16(ws))) return TBIK_ERR_ALIGN;
     if (!ws || ws_bytes < tbik_cache_compact_workspace(num_pages)) return TBIK_ERR_WORKSPACE;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     const CacheMetaParams m = meta_params(table, lens, refs, slots, max_pages, num_pages, page);
@@ -292,7 +295,7 @@ tbik_status tbik_cache_copy(uint8_t* pages, float* scales, const int32_t* src, c
     if ((st = check_data(layers, num_pages, kv_heads, head_dim, page)) != TBIK_OK) return st;
     if (count == 0) return TBIK_OK;
     if (!pages || !scales || !src || !dst) return TBIK_ERR_ARG;
-    if (!aligned16(pages) || !aligned16(scales) || (ws && !aligned16(ws))) return TBIK_ERR_ALIGN;
+    if (!aligned16(pages) || !aligned4(scales) || (ws && !aligned16(ws))) return TBIK_ERR_ALIGN;
     if (!ws || ws_bytes < tbik_cache_fork_workspace(count)) return TBIK_ERR_WORKSPACE;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     const size_t smem = ((size_t)num_pages + 31) / 32 * 4;
@@ -321,7 +324,7 @@ tbik_status tbik_cache_append(const uint16_t* k, const uint16_t* v, uint8_t* pag
     if ((!cu && tokens != batch) || (!rows && batch > slots)) return TBIK_ERR_SHAPE;
     if (tokens == 0 || batch == 0) return TBIK_OK;
     if (!k || !v || !pages || !scales || !table || !refs || !start) return TBIK_ERR_ARG;
-    if (!aligned16(k) || !aligned16(v) || !aligned16(pages) || !aligned16(scales)) return TBIK_ERR_ALIGN;
+    if (!aligned16(k) || !aligned16(v) || !aligned16(pages) || !aligned4(scales)) return TBIK_ERR_ALIGN;
     CacheAppendParams p;
     p.k = k, p.v = v, p.pages = pages, p.scales = scales, p.table = table, p.refs = refs, p.start = start;
     p.cu = cu, p.rows = rows, p.tokens = tokens, p.batch = batch, p.slots = slots, p.max_pages = max_pages;
@@ -360,7 +363,7 @@ tbik_status tbik_cache_attention(const uint16_t* q, const uint8_t* pages, const 
     if ((st = plan_cache_attention(tokens, batch, max_q, max_keys, heads, kv_heads, head_dim, info->sms, c)) != TBIK_OK) return st;
     if (tokens == 0 || batch == 0) return TBIK_OK;
     if (!q || !pages || !scales || !table || !start || !out) return TBIK_ERR_ARG;
-    if (!aligned16(q) || !aligned16(pages) || !aligned16(scales) || !aligned16(out)) return TBIK_ERR_ALIGN;
+    if (!aligned16(q) || !aligned16(pages) || !aligned4(scales) || !aligned16(out)) return TBIK_ERR_ALIGN;
     if (c.bytes && (!ws || ws_bytes < c.bytes)) return TBIK_ERR_WORKSPACE;
     if (c.bytes && !aligned16(ws)) return TBIK_ERR_ALIGN;
     CacheAttParams p;

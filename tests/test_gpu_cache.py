@@ -578,6 +578,25 @@ def test_withheld_arrive_times_out_and_context_survives(heads, H, ctx, n):
     assert tbik.get_error() == tbik.TBIK_OK
 
 
+@pytest.mark.parametrize("num_pages,H", [(201, 1), (67, 3)])
+def test_a_layer_of_a_pool_with_an_odd_number_of_scales(num_pages, H):
+    """One layer's scales then start 8 bytes behind a 16-byte boundary."""
+    D, page, layers = 64, 16, 3
+    c = Cache(2, 6, num_pages, H, D, page, layers)
+    assert c.scales[1].data_ptr() % 16 == 8
+    n = [40, 90]
+    start = c.extend([0, 1], n)
+    q = torch.randn(2, 4 * H, D, device=DEV).to(torch.bfloat16)
+    for layer in range(layers):
+        k, v = tokens(layer, 130, H, D), tokens(layer + 9, 130, H, D)
+        c.append(k, v, start, n, [0, 1], layer=layer)
+        check_written(c, 0, k[:40], v[:40], layer)
+        check_written(c, 1, k[40:], v[40:], layer)
+        alone = tbik.cache_attention(q, c.pages[layer].clone(), c.scales[layer].clone(), c.table, i32([39, 89]), rows=i32([0, 1]))
+        assert torch.equal(c.attend(q, i32([39, 89]), [1, 1], [0, 1], layer=layer, packed=False), alone)
+    assert tbik.get_error() == tbik.TBIK_OK
+
+
 # ------------------------------------------------- together, as a rollout uses them
 
 def test_a_rollout_and_its_replay():
