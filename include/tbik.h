@@ -465,7 +465,8 @@ TBIK_API tbik_status tbik_cache_fork(uint8_t* pages, float* scales, int32_t* tab
 /*
  * Gives up the pages of each listed sequence and empties its slot; a page is
  * free when its last reference goes.  A slot named twice is freed once, an
- * empty one is left as it is.
+ * empty one is left as it is.  Entries of a row that name no page in use are
+ * emptied like the others, and TBIK_ERR_PAGE is recorded.
  */
 TBIK_API tbik_status tbik_cache_free(int32_t* table, int32_t* lens, int32_t* refs, const int32_t* rows, int batch,
                                      int slots, int max_pages, int num_pages, int page, void* stream);

@@ -652,25 +652,33 @@ __global__ void __launch_bounds__(CACHE_MOVE_THREADS) cache_compact_kernel(const
     move_pages(p);
 }
 
-// One block per sequence.  Taking the length out by an exchange makes a row that is named twice give up its pages once.
-__global__ void __launch_bounds__(128) cache_free_kernel(const CacheMetaParams m, const int32_t* rows) {
+// Every block looks at all of the call's slots before it empties any, so that a slot out of range leaves the others
+// alone; the grid is bounded, so that the looks stay in proportion to the call (128 threads read 8192 slots in 64 steps).
+// Taking the length out by an exchange makes a row that is named twice give up its pages once.
+__global__ void __launch_bounds__(128) cache_free_kernel(const CacheMetaParams m, const int32_t* rows, int batch) {
     __shared__ int len;
-    const int r = rows ? rows[blockIdx.x] : blockIdx.x;
-    if (r < 0 || r >= m.slots) {
+    bool bad = false;
+    if (rows)
+        for (int b = threadIdx.x; b < batch; b += 128) bad |= rows[b] < 0 || rows[b] >= m.slots;
+    if (__syncthreads_or(bad)) {
         if (threadIdx.x == 0) set_error(TBIK_ERR_PAGE);
         return;
     }
-    if (threadIdx.x == 0) len = atomicExch(&m.lens[r], 0);
-    __syncthreads();
-    int used = (int)(((long long)max(len, 0) + m.page - 1) / m.page);
-    if (used > m.max_pages) used = m.max_pages;
-    for (int j = threadIdx.x; j < used; j += 128) {
-        int32_t* e = &m.table[(size_t)r * m.max_pages + j];
-        const int id = *e;
-        *e = -1;
-        if (id < 0 || id >= m.num_pages || atomicSub(&m.refs[id], 1) <= 0) {
-            if (id >= 0 && id < m.num_pages) atomicAdd(&m.refs[id], 1);
-            set_error(TBIK_ERR_PAGE);
+    for (int b = blockIdx.x; b < batch; b += gridDim.x) {
+        const int r = rows ? rows[b] : b;
+        __syncthreads();  // the length of the sequence before has been read
+        if (threadIdx.x == 0) len = atomicExch(&m.lens[r], 0);
+        __syncthreads();
+        int used = (int)(((long long)max(len, 0) + m.page - 1) / m.page);
+        if (used > m.max_pages) used = m.max_pages;
+        for (int j = threadIdx.x; j < used; j += 128) {
+            int32_t* e = &m.table[(size_t)r * m.max_pages + j];
+            const int id = *e;
+            *e = -1;
+            if (id < 0 || id >= m.num_pages || atomicSub(&m.refs[id], 1) <= 0) {
+                if (id >= 0 && id < m.num_pages) atomicAdd(&m.refs[id], 1);
+                set_error(TBIK_ERR_PAGE);
+            }
         }
     }
 }

@@ -253,8 +253,8 @@ tbik_status tbik_cache_free(int32_t* table, int32_t* lens, int32_t* refs, const 
     if (!rows && batch > slots) return TBIK_ERR_SHAPE;
     if (batch == 0) return TBIK_OK;
     if (!table || !lens || !refs) return TBIK_ERR_ARG;
-    cache_free_kernel<<<batch, 128, 0, reinterpret_cast<cudaStream_t>(stream)>>>(
-        meta_params(table, lens, refs, slots, max_pages, num_pages, page), rows);
+    cache_free_kernel<<<move_grid(info, batch), 128, 0, reinterpret_cast<cudaStream_t>(stream)>>>(
+        meta_params(table, lens, refs, slots, max_pages, num_pages, page), rows, batch);
     return launch_status();
 }
 

@@ -482,6 +482,38 @@ def test_page_operations_refuse_without_a_trace():
             f()
 
 
+def test_free_with_one_slot_out_of_range_changes_nothing():
+    c = Cache(300, 3, 900, 1, 64, 16)
+    assert c.extend(range(300), [17 + i % 30 for i in range(300)])[0] == 0
+    for rows in ([0, 300], [300, 0], [5, 7, -1, 9], list(range(299)) + [300], [2 ** 31 - 1] + list(range(299))):
+        tbik.cache_free(c.table, c.lens, c.refs, i32(rows), page=16)
+        assert tbik.get_error() == tbik.TBIK_ERR_PAGE
+        c.check()
+    rows = [4, 5, 4, 5] + list(range(100, 300))  # slots named twice
+    tbik.cache_free(c.table, c.lens, c.refs, i32(rows), page=16)
+    c.book.free(rows)
+    c.check()
+    assert tbik.get_error() == tbik.TBIK_OK
+
+
+def test_free_of_more_sequences_than_blocks():
+    """8192 sequences of one or two pages, some slots empty: the grid takes several of them a block."""
+    slots = 8192
+    c = Cache(slots, 2, 2 * slots, 1, 64, 16, fill=0)
+    n = [(7 * i) % 33 for i in range(slots)]
+    start = tbik.cache_extend(c.table, c.lens, c.refs, i32(n), page=16)
+    assert c.book.extend(list(range(slots)), n) == start.tolist() == [0] * slots
+    c.check()
+    rows = np.random.RandomState(0).permutation(slots)[:8000].tolist() + [3] * 100
+    tbik.cache_free(c.table, c.lens, c.refs, i32(rows), page=16)
+    c.book.free(rows)
+    c.check()
+    tbik.cache_free(c.table, c.lens, c.refs, i32([0] * slots), page=16)  # mostly nothing, no slot twice in effect
+    c.book.free([0])
+    c.check()
+    assert tbik.get_error() == tbik.TBIK_OK
+
+
 def test_a_large_pool():
     """Page numbers over many scan steps, and page bytes behind 2^32."""
     H, D, page, num = 8, 128, 128, 20000  # 5.2 GB
