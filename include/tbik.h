@@ -435,9 +435,10 @@ TBIK_API tbik_status tbik_logprob_noalloc(const uint16_t* hidden, const uint16_t
  * layer's part of pages and scales is as good as the whole).
  *
  * The page operations are all or nothing: when an argument cannot be (a slot
- * out of range or named twice, a length that does not fit max_pages, too few
- * free pages), they change nothing and record TBIK_ERR_PAGE.  New pages are the
- * lowest free ones, in the order of the call's sequences.
+ * out of range or named twice, a length that does not fit max_pages, a parent
+ * whose row names a page that is not in use, too few free pages), they change
+ * nothing and record TBIK_ERR_PAGE.  New pages are the lowest free ones, in the
+ * order of the call's sequences.
  */
 
 /*

@@ -427,8 +427,35 @@ __global__ void __launch_bounds__(CACHE_PLAN_THREADS)
 // Page moves that a plan kernel leaves for cache_move_kernel: word 0 is their number, then (from, to) pairs.
 __device__ __forceinline__ int2* move_list(int* ws) { return reinterpret_cast<int2*>(ws) + 1; }
 
+// Whether the first n pages of a row are in use, a warp's lanes each for some of them (`lane` of `step`).
+__device__ __forceinline__ bool pages_in_use(const CacheMetaParams& m, int row, int n, int lane, int step) {
+    bool all = true;
+    for (int j = lane; j < n; j += step) {
+        const int id = m.table[(size_t)row * m.max_pages + j];
+        all &= id >= 0 && id < m.num_pages && m.refs[id] > 0;
+    }
+    return all;
+}
+
+// For the plan kernels that look at many table entries: they run as a cluster whose blocks share the looking, and block 0
+// goes on alone with the answer.  True in every thread of block 0 if some thread of the cluster has `bad`; the other
+// blocks are done when this returns.
+constexpr int CACHE_PLAN_CLUSTER = 8;
+__device__ __forceinline__ bool plan_any(bool bad, uint32_t rank, uint32_t cl) {
+    __shared__ uint32_t from[CACHE_PLAN_CLUSTER];
+    bad = __syncthreads_or(bad);
+    cluster_sync();  // block 0 runs: its memory may be written
+    if (threadIdx.x == 0) st_cluster_u32(mapa_shared(smem_u32(&from[rank]), 0), bad);
+    cluster_sync();
+    if (rank == 0)
+        for (uint32_t r = 0; r < cl; ++r) bad |= from[r] != 0;
+    return bad;
+}
+
 // children[i] becomes a copy of parents[i]: full pages are shared, a page that is partly filled gets a copy, since
 // both sequences will write into it.  Words 0 and 1 of ws: the number of copies and whether the call is granted.
+// A warp per parent looks at its row (in a cluster of up to 8 blocks: 32 parents to a block), so that a row that names no
+// page in use is found before anything changes; then one block plans.
 __global__ void __launch_bounds__(CACHE_PLAN_THREADS)
     cache_fork_plan_kernel(const CacheMetaParams m, const int32_t* parents, const int32_t* children, int count, int* ws) {
     extern __shared__ int sm[];
@@ -436,9 +463,19 @@ __global__ void __launch_bounds__(CACHE_PLAN_THREADS)
     uint32_t* child = reinterpret_cast<uint32_t*>(sm + count + 1);
     __shared__ int warp_sums[32];
     const int tid = threadIdx.x;
+    uint32_t cl;
+    asm volatile("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(cl));
+    const uint32_t rank = cluster_rank();
     for (int i = tid; i < (m.slots + 31) / 32; i += CACHE_PLAN_THREADS) child[i] = 0;
-    __syncthreads();
     bool bad = false;
+    for (int i = (int)rank * 32 + (tid >> 5); i < count; i += (int)cl * 32) {
+        const int p = parents[i];
+        if (p < 0 || p >= m.slots) continue;  // refused below, and so is a length that cannot be
+        const int l = m.lens[p];
+        if (l > 0) bad |= !pages_in_use(m, p, min(m.max_pages, (int)(((long long)l + m.page - 1) / m.page)), tid & 31, 32);
+    }
+    bad = plan_any(bad, rank, cl);
+    if (rank != 0) return;
     for (int i = tid; i < count; i += CACHE_PLAN_THREADS) {
         const int p = parents[i], c = children[i];
         int k = 0;
@@ -449,11 +486,8 @@ __global__ void __launch_bounds__(CACHE_PLAN_THREADS)
             if (atomicOr(&child[c >> 5], bit) & bit) bad = true;
             const int l = m.lens[p];
             if (m.lens[c] != 0 || l < 0 || (long long)l > (long long)m.max_pages * m.page) bad = true;
-            else if (l % m.page) {
-                k = 1;
-                const int src = m.table[(size_t)p * m.max_pages + l / m.page];
-                if (src < 0 || src >= m.num_pages) bad = true;
-            }
+            else
+                k = l % m.page != 0;
         }
         need[i] = k;
     }
@@ -621,12 +655,9 @@ __global__ void __launch_bounds__(CACHE_MOVE_THREADS)
     for (int i = blockIdx.x; i < count; i += gridDim.x) {
         const int par = parents[i], c = children[i], l = m.lens[par], full = l / m.page;
         for (int j = threadIdx.x; j < full; j += CACHE_MOVE_THREADS) {
-            const int id = m.table[(size_t)par * m.max_pages + j];
+            const int id = m.table[(size_t)par * m.max_pages + j];  // in use: the plan has looked
             m.table[(size_t)c * m.max_pages + j] = id;
-            if (id >= 0 && id < m.num_pages)
-                atomicAdd(&m.refs[id], 1);
-            else
-                set_error(TBIK_ERR_PAGE);
+            atomicAdd(&m.refs[id], 1);
         }
         if (threadIdx.x == 0) m.lens[c] = l;
     }

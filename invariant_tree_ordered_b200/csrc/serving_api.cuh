@@ -44,6 +44,24 @@ bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0
 // Shared memory of a plan kernel: prefix sums over the call's sequences and a bit per slot.
 size_t plan_smem(int count, int slots) { return ((size_t)count + 1) * 4 + ((size_t)slots + 31) / 32 * 4; }
 
+// A plan kernel as one cluster of `blocks` blocks.
+template <typename... P, typename... A>
+tbik_status launch_plan(void (*kernel)(P...), int blocks, size_t smem, cudaStream_t s, A... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)blocks);
+    cfg.blockDim = dim3(CACHE_PLAN_THREADS);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = (unsigned)blocks;
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, kernel, P(args)...) != cudaSuccess) return TBIK_ERR_CUDA;
+    return launch_status();
+}
+
 // Blocks of a kernel that walks over page data: eight of 256 threads fill an SM.
 int move_grid(const DeviceInfo* info, long long most) {
     const long long full = (long long)info->sms * 8;
@@ -235,9 +253,10 @@ tbik_status tbik_cache_fork(uint8_t* pages, float* scales, int32_t* table, int32
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     const CacheMetaParams m = meta_params(table, lens, refs, slots, max_pages, num_pages, page);
     const CacheMoveParams p = move_params(pages, scales, layers, num_pages, kv_heads, head_dim, page, ws);
-    cache_fork_plan_kernel<<<1, CACHE_PLAN_THREADS, plan_smem(count, slots), s>>>(m, parents, children, count,
-                                                                                   reinterpret_cast<int*>(ws));
-    if ((st = launch_status()) != TBIK_OK) return st;
+    int blocks = 1;
+    while (blocks < CACHE_PLAN_CLUSTER && 32 * blocks < count) blocks *= 2;
+    st = launch_plan(cache_fork_plan_kernel, blocks, plan_smem(count, slots), s, m, parents, children, count, reinterpret_cast<int*>(ws));
+    if (st != TBIK_OK) return st;
     const long long most = (long long)count * p.planes * ((p.page_bytes + CACHE_MOVE_BYTES - 1) / CACHE_MOVE_BYTES);
     cache_fork_kernel<<<move_grid(info, most), CACHE_MOVE_THREADS, 0, s>>>(p, m, parents, children, count);
     return launch_status();

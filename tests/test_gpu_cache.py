@@ -514,6 +514,35 @@ def test_free_of_more_sequences_than_blocks():
     assert tbik.get_error() == tbik.TBIK_OK
 
 
+@pytest.mark.parametrize("copies", [1, 50, 300])
+def test_fork_of_a_row_that_names_no_page_changes_nothing(copies):
+    """A bad entry anywhere among a parent's pages: outside the pool, none, or a free page."""
+    page, parents = 16, 6
+    c = Cache(parents + copies, 40, 700, 1, 64, page, layers=2)
+    c.extend(range(parents), [16 * (3 + i) + i for i in range(parents)])
+    before = stamp(c)
+    par = [i % parents for i in range(copies)][::-1]
+    children = list(range(parents, parents + copies))
+    saved = c.table.clone()
+    victim = par[-1]
+    last = c.book.pages_of(c.book.lens[victim]) - 1
+    for j in (0, 1, last):
+        for value in (-1, 700, 2 ** 31 - 1, 699):  # 699 is free
+            c.table[victim, j] = value
+            c.book.table[victim, j] = value
+            tbik.cache_fork(c.pages, c.scales, c.table, c.lens, c.refs, i32(par), i32(children))
+            assert tbik.get_error() == tbik.TBIK_ERR_PAGE
+            c.check()
+            check_moves(c, before, [])
+            c.table.copy_(saved)
+            c.book.table[:] = saved.cpu().numpy()
+    tbik.cache_fork(c.pages, c.scales, c.table, c.lens, c.refs, i32(par), i32(children))
+    moves = c.book.fork(par, children)
+    c.check()
+    check_moves(c, before, moves)
+    assert tbik.get_error() == tbik.TBIK_OK
+
+
 def test_a_large_pool():
     """Page numbers over many scan steps, and page bytes behind 2^32."""
     H, D, page, num = 8, 128, 128, 20000  # 5.2 GB
