@@ -435,9 +435,9 @@ TBIK_API tbik_status tbik_logprob_noalloc(const uint16_t* hidden, const uint16_t
  * layer's part of pages and scales is as good as the whole).
  *
  * The page operations are all or nothing: when an argument cannot be (a slot
- * out of range or named twice, a length that does not fit max_pages, a parent
- * whose row names a page that is not in use, too few free pages), they change
- * nothing and record TBIK_ERR_PAGE.  New pages are the lowest free ones, in the
+ * out of range or named twice, a length that does not fit max_pages, a row to
+ * fork or to compact that names a page not in use, too few free pages), they
+ * change nothing and record TBIK_ERR_PAGE.  New pages are the lowest free ones, in the
  * order of the call's sequences.
  */
 
@@ -475,7 +475,8 @@ TBIK_API tbik_status tbik_cache_free(int32_t* table, int32_t* lens, int32_t* ref
 /*
  * Moves live pages to the front of the pool: with n live pages, the k-th live
  * page at index >= n goes to the k-th free index below n, in all layers; table
- * and refs follow.  live (int32 [1]) receives n: indices >= n are free.
+ * and refs follow.  live (int32 [1]) receives n: indices >= n are free (-1 when
+ * the call is refused).
  * ws: tbik_cache_compact_workspace().
  */
 TBIK_API size_t tbik_cache_compact_workspace(int num_pages);

@@ -514,15 +514,39 @@ __global__ void __launch_bounds__(CACHE_PLAN_THREADS)
 }
 
 // Compaction: the k-th live page at or behind index n = (number of live pages) moves to the k-th free index below n.
-// Sources and targets are disjoint, so the copies need no order.  ws: count, n, moves, then the new index of each
-// moved page.
+// Sources and targets are disjoint, so the copies need no order.  ws: count, n (-1 when refused), moves, then the new
+// index of each moved page.  A cluster of 8 blocks first looks whether every page of every row is in use: a warp takes
+// `per` slots at a time, few when there are few, and at most the 32 lengths that its lanes load at once.
 __global__ void __launch_bounds__(CACHE_PLAN_THREADS)
     cache_compact_plan_kernel(const CacheMetaParams m, int32_t* live_out, int* ws) {
     __shared__ int warp_sums[32];
     __shared__ int n_live;
     const int tid = threadIdx.x, lane = tid & 31;
+    uint32_t cl;
+    asm volatile("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(cl));
+    const uint32_t rank = cluster_rank();
+    const int warps = (int)cl * 32, per = min(32, (m.slots + warps - 1) / warps);
+    bool bad = false;
+    for (int r0 = ((int)rank * 32 + (tid >> 5)) * per; r0 < m.slots; r0 += warps * per) {
+        const int l = lane < per && r0 + lane < m.slots ? m.lens[r0 + lane] : 0;
+        bad |= l < 0 || (long long)l > (long long)m.max_pages * m.page;
+        for (uint32_t some = __ballot_sync(0xffffffffu, l > 0); some; some &= some - 1) {
+            const int k = __ffs((int)some) - 1, lk = __shfl_sync(0xffffffffu, l, k);
+            bad |= !pages_in_use(m, r0 + k, min(m.max_pages, (int)(((long long)lk + m.page - 1) / m.page)), lane, 32);
+        }
+    }
     if (tid == 0) n_live = 0;
-    __syncthreads();
+    bad = plan_any(bad, rank, cl);
+    if (rank != 0) return;
+    if (bad) {
+        if (tid == 0) {
+            set_error(TBIK_ERR_PAGE);
+            ws[0] = 0;
+            ws[1] = -1;
+            live_out[0] = -1;
+        }
+        return;
+    }
     int cnt = 0;
     for (int i = tid; 4 * i < m.num_pages; i += CACHE_PLAN_THREADS) {
         const int4 r = load_refs4(m.refs, i, m.num_pages, 0);
@@ -552,7 +576,6 @@ __global__ void __launch_bounds__(CACHE_PLAN_THREADS)
         for (int q = 0; q < 4; ++q) {
             if (p0 + q < n && v[q] == 0) moves[rh++].y = p0 + q;
             if (p0 + q >= n && v[q] != 0) moves[ri++].x = p0 + q;
-            if (p0 + q >= n && p0 + q < m.num_pages && v[q] == 0) map[p0 + q] = -1;  // no page to speak of
         }
         holes += th;
         highs += ti;
@@ -667,6 +690,7 @@ __global__ void __launch_bounds__(CACHE_MOVE_THREADS)
 // The second kernel of a compaction: table entries of moved pages, and the copies.
 __global__ void __launch_bounds__(CACHE_MOVE_THREADS) cache_compact_kernel(const CacheMoveParams p, const CacheMetaParams m) {
     const int n = p.ws[1];
+    if (n < 0) return;
     const int* map = p.ws + 2 + 2 * ((m.num_pages + 1) / 2);
     const long long entries = (long long)m.slots * m.max_pages;
     for (long long e = (long long)blockIdx.x * CACHE_MOVE_THREADS + threadIdx.x; e < entries; e += (long long)gridDim.x * CACHE_MOVE_THREADS) {
@@ -674,11 +698,7 @@ __global__ void __launch_bounds__(CACHE_MOVE_THREADS) cache_compact_kernel(const
         if (id < n) continue;  // below the front, or none
         const int r = (int)(e / m.max_pages), j = (int)(e % m.max_pages);
         if (j >= (m.lens[r] + m.page - 1) / m.page) continue;
-        const int to = id < m.num_pages ? map[id] : -1;
-        if (to < 0)
-            set_error(TBIK_ERR_PAGE);  // the table names a page that no reference counts
-        else
-            m.table[e] = to;
+        m.table[e] = map[id];  // in use: the plan has looked
     }
     move_pages(p);
 }

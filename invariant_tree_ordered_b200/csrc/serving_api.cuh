@@ -297,8 +297,8 @@ tbik_status tbik_cache_compact(uint8_t* pages, float* scales, int32_t* table, co
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     const CacheMetaParams m = meta_params(table, lens, refs, slots, max_pages, num_pages, page);
     const CacheMoveParams p = move_params(pages, scales, layers, num_pages, kv_heads, head_dim, page, ws);
-    cache_compact_plan_kernel<<<1, CACHE_PLAN_THREADS, 0, s>>>(m, live, reinterpret_cast<int*>(ws));
-    if ((st = launch_status()) != TBIK_OK) return st;
+    st = launch_plan(cache_compact_plan_kernel, slots > 32 ? CACHE_PLAN_CLUSTER : 1, 0, s, m, live, reinterpret_cast<int*>(ws));
+    if (st != TBIK_OK) return st;
     const long long most = (long long)(num_pages / 2 + 1) * p.planes * ((p.page_bytes + CACHE_MOVE_BYTES - 1) / CACHE_MOVE_BYTES);
     cache_compact_kernel<<<move_grid(info, most), CACHE_MOVE_THREADS, 0, s>>>(p, m);
     return launch_status();

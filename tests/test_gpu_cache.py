@@ -543,6 +543,47 @@ def test_fork_of_a_row_that_names_no_page_changes_nothing(copies):
     assert tbik.get_error() == tbik.TBIK_OK
 
 
+@pytest.mark.parametrize("slots", [5, 40, 700, 20000])
+def test_compaction_of_a_table_that_names_no_page_changes_nothing(slots):
+    """A row with a page outside the pool, none, or a free one, or a length that cannot be."""
+    page, num = 16, 900
+    c = Cache(slots, 9, num, 1, 64, page, layers=2)
+    r = np.random.RandomState(slots)
+    rows = r.permutation(slots)[:min(slots, 200)].tolist()
+    c.extend(rows, r.randint(1, 5 * page if slots < 700 else page * 4, len(rows)).tolist())
+    gone = rows[::3]
+    tbik.cache_free(c.table, c.lens, c.refs, i32(gone), page=page)
+    c.book.free(gone)
+    live = [x for x in rows if x not in gone]
+    before = stamp(c)
+    free = int(np.flatnonzero(c.book.refs == 0)[0])  # below the front
+    table, lens = c.table.clone(), c.lens.clone()
+
+    def refused():
+        c.book.table, c.book.lens = c.table.cpu().numpy(), c.lens.cpu().numpy()
+        assert tbik.cache_compact(c.pages, c.scales, c.table, c.lens, c.refs).item() == -1
+        assert tbik.get_error() == tbik.TBIK_ERR_PAGE
+        c.check()
+        check_moves(c, before, [])
+        c.table.copy_(table)
+        c.lens.copy_(lens)
+
+    for x in (live[0], live[-1], max(live)):
+        last = -(-int(lens[x]) // page) - 1
+        for j, value in ((last, -1), (0, num), (last, 2 ** 31 - 1), (0, free), (last, num - 1), (0, -7)):
+            c.table[x, j] = value
+            refused()
+        for value in (-1, 9 * page + 1, 2 ** 31 - 1):
+            c.lens[x] = value
+            refused()
+    c.book.table, c.book.lens = table.cpu().numpy(), lens.cpu().numpy()
+    n, moves = c.book.compact()
+    assert tbik.cache_compact(c.pages, c.scales, c.table, c.lens, c.refs).item() == n
+    c.check()
+    check_moves(c, before, moves)
+    assert tbik.get_error() == tbik.TBIK_OK
+
+
 def test_a_large_pool():
     """Page numbers over many scan steps, and page bytes behind 2^32."""
     H, D, page, num = 8, 128, 128, 20000  # 5.2 GB
