@@ -108,152 +108,199 @@ struct CacheAppendParams {
 // looked up, so that the chain of loads is sequence, start, tokens.  Bound by integer instructions (about six per value
 // for rounding, cutting, sign and packing) ahead of HBM: 32 prompts of 100 to 4096 tokens, 8 heads of 128 dims, 58 us,
 // 3.9 TB/s.  128 threads with eight loads each measured 58 us there, 256 with four 65 us.  A decode step (one token each:
-// one warp per token, head and operand) takes 2.8 us for 64 sequences.
+// one warp per token, head and operand, eight to a block) takes 2.3 us for 64 sequences and 39 us for 8192 (8 heads of
+// 128; blocks of one warp took 2.5 and 70 us).
 //
 // Which page a block has: sequence b's pages start at virtual index cu[b] / page + 2 b.  n tokens touch at most
-// n / page + 2 pages, so the ranges do not overlap, and the grid is known without reading `start`.
-template <int D, int THREADS, int CH>
-__global__ void __launch_bounds__(THREADS) cache_append_kernel(const CacheAppendParams p) {
-    const int tid = threadIdx.x;
+// n / page + 2 pages, so the ranges do not overlap, and the grid is known without reading `start`.  The sequence is
+// found in two steps of THREADS looks, whatever the batch (8192 at most; as many steps as it takes to see all of them
+// were 1128 us for 8192 sequences of one token, two are 263 us).
+//
+// With `rows`, a slot that is named twice would be written by two blocks at once.  Up to APPEND_FEW * THREADS sequences a
+// block compares its slot with all of the call's.  For more (and for single tokens, GROUPS warps a block) the grid is what
+// the device holds; each block marks all slots once, in two maps of a bit per slot, and takes several pages or tokens in
+// turn, so that the looks stay in proportion to the call: 8192 single tokens 51 us (356 us with all blocks comparing),
+// with `cu` 372 us (1348 us).  Up to 4 looks a thread the comparison is as fast or faster: 512 sequences 22 us either way,
+// 64 4.6 us (5.3 us with maps).
+constexpr int APPEND_FEW = 4;
+template <int THREADS>
+__device__ __forceinline__ int append_sequence(const CacheAppendParams& p, int x) {
+    static_assert(THREADS * THREADS >= CACHE_MAX_BATCH, "two steps");
+    const int tid = threadIdx.x, stride = (p.batch + THREADS - 1) / THREADS;
+    auto before = [&](int i) { return i < p.batch && (p.cu[i] >> p.page_shift) + 2 * i <= x; };
+    const int b = (__syncthreads_count(before(tid * stride)) - 1) * stride;  // of the looked at, the last that starts at or before x
+    if (stride == 1 || b < 0) return b;
+    return b + __syncthreads_count(tid + 1 < stride && before(b + tid + 1));
+}
+
+// (The ROWS form's bounds on registers keep as many blocks on an SM as the other's: left alone it takes up to 152, and 32
+// prompts 76 us in place of 55.)
+template <int D, int THREADS, int CH, int GROUPS, bool ROWS>
+__global__ void __launch_bounds__(THREADS * GROUPS, ROWS && GROUPS == 1 ? (CH == 8 ? 768 : CH == 4 ? 1024 : 1536) / THREADS : 0) cache_append_kernel(const CacheAppendParams p) {
+    static_assert(GROUPS == 1 || THREADS == 32, "groups are warps");
+    const int tid = threadIdx.x % THREADS;
     const int head = blockIdx.y, kv = blockIdx.z;
-    int b, t0, n, j;  // sequence, its first token, its tokens, page number among the touched ones
-    if (p.cu) {
-        const int x = blockIdx.x;
-        b = -1;  // the last b with its first virtual page <= x: they are counted, a load per thread at a time
-        for (int base = 0; base < p.batch; base += THREADS) {
-            const int i = base + tid;
-            const int c = __syncthreads_count(i < p.batch && (p.cu[i] >> p.page_shift) + 2 * i <= x);
-            b += c;
-            if (c < THREADS) break;
-        }
-        if (b < 0) return;  // cu[0] > 0 and before the first page
-        t0 = p.cu[b];
-        n = p.cu[b + 1] - t0;
-        j = x - ((t0 >> p.page_shift) + 2 * b);
-        if (t0 < 0 || n < 0 || t0 > p.tokens - n) {
-            if (tid == 0) set_error(TBIK_ERR_POSITION);
-            return;
-        }
-    } else {
-        b = blockIdx.x;
-        t0 = b;
-        n = 1;
-        j = 0;
-    }
-    const int s = p.start[b];
-    const int first = s >> p.page_shift;  // the page of the first new token
-    if (n <= 0 || j < 0 || s < 0) return;
-    const long long end = (long long)s + n;
-    const long long pg = (long long)first + j;
-    const long long pg0 = pg * p.page;
-    if (pg0 >= end) return;  // fewer pages than the bound allows
-    const int o0 = pg0 >= s ? 0 : (int)(s - pg0);                          // first new token's place in the page
-    const int o1 = (int)(end - pg0 < p.page ? end - pg0 : p.page);         // behind the last
-    const int src0 = t0 + (int)(pg0 + o0 - s);                             // its packed token
-    const int chunks = (o1 - o0) * (D / 8);
-    const uint16_t* x = (kv ? p.v : p.k) + ((size_t)src0 * p.kv_heads + head) * D;
-    const size_t tstride = (size_t)p.kv_heads * D;
-    uint4 w[CH];
-#pragma unroll
-    for (int c = 0; c < CH; ++c) {
-        const int i = c * THREADS + tid;
-        w[c] = make_uint4(0, 0, 0, 0);
-        if (i < chunks) w[c] = __ldg(reinterpret_cast<const uint4*>(x + (size_t)(i / (D / 8)) * tstride) + i % (D / 8));
-    }
-    // the tokens are on their way while the page is looked up
-    const int row = p.rows ? p.rows[b] : b;
-    bool bad = row < 0 || row >= p.slots || pg >= p.max_pages;
-    if (!bad && p.rows) {  // the same row twice would be written by two blocks at once
-        bool dup = false;
-        for (int i = tid; i < p.batch; i += THREADS) dup |= (i != b && p.rows[i] == row);
-        bad = __syncthreads_or(dup);
-    }
-    int id = -1;
-    if (!bad) {
-        id = p.table[(size_t)row * p.max_pages + pg];
-        bad = id < 0 || id >= p.num_pages || p.refs[id] != 1;  // a shared page is never written
-    }
-    if (bad) {
-        if (tid == 0) set_error(TBIK_ERR_PAGE);
-        return;
-    }
-    uint32_t top2 = 0;  // largest magnitudes of the even and the odd dims
-#pragma unroll
-    for (int c = 0; c < CH; ++c)
-        top2 = __vmaxu2(__vmaxu2(top2, __vmaxu2(w[c].x & 0x7fff7fffu, w[c].y & 0x7fff7fffu)),
-                        __vmaxu2(w[c].z & 0x7fff7fffu, w[c].w & 0x7fff7fffu));
-    uint32_t top = max(top2 & 0xffffu, top2 >> 16);
-    const bool odd = top >= 0x7F80u;
-    if (odd) {  // what is not finite does not count
-        top = 0;
-#pragma unroll
-        for (int c = 0; c < CH; ++c) {
-            const uint32_t a[4] = {w[c].x, w[c].y, w[c].z, w[c].w};
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const uint32_t l = a[q] & 0x7FFFu, h = (a[q] >> 16) & 0x7FFFu;
-                if (l < 0x7F80u) top = max(top, l);
-                if (h < 0x7F80u) top = max(top, h);
+    extern __shared__ uint32_t append_maps[];  // slots that the call names, and those it names twice
+    uint32_t* twice = append_maps + (p.slots + 31) / 32;
+    const bool maps = ROWS && (GROUPS > 1 || p.batch > APPEND_FEW * THREADS);
+    if (maps) {
+        for (int i = threadIdx.x; i < 2 * ((p.slots + 31) / 32); i += THREADS * GROUPS) append_maps[i] = 0;
+        __syncthreads();
+        for (int i = threadIdx.x; i < p.batch; i += THREADS * GROUPS) {
+            const int r = p.rows[i];
+            if (r >= 0 && r < p.slots) {
+                const uint32_t bit = 1u << (r & 31);
+                if (atomicOr(&append_maps[r >> 5], bit) & bit) atomicOr(&twice[r >> 5], bit);
             }
         }
+        __syncthreads();
     }
     __shared__ uint32_t red[THREADS / 32];
-    top = __reduce_max_sync(0xffffffffu, top);
-    if (THREADS > 32) {
-        if ((tid & 31) == 0) red[tid >> 5] = top;
-        __syncthreads();
+    auto page = [&](int vp) {  // of the touched pages, or (without cu) of the tokens
+        int b, t0, n, j;  // sequence, its first token, its tokens, page number among the touched ones
+        if constexpr (GROUPS == 1) {
+            b = append_sequence<THREADS>(p, vp);
+            if (b < 0) return;  // cu[0] > 0 and before the first page
+            t0 = p.cu[b];
+            n = p.cu[b + 1] - t0;
+            j = vp - ((t0 >> p.page_shift) + 2 * b);
+            if (t0 < 0 || n < 0 || t0 > p.tokens - n) {
+                if (tid == 0) set_error(TBIK_ERR_POSITION);
+                return;
+            }
+        } else {
+            b = vp;
+            t0 = b;
+            n = 1;
+            j = 0;
+        }
+        const int s = p.start[b];
+        const int first = s >> p.page_shift;  // the page of the first new token
+        if (n <= 0 || j < 0 || s < 0) return;
+        const long long end = (long long)s + n;
+        const long long pg = (long long)first + j;
+        const long long pg0 = pg * p.page;
+        if (pg0 >= end) return;  // fewer pages than the bound allows
+        const int o0 = pg0 >= s ? 0 : (int)(s - pg0);                          // first new token's place in the page
+        const int o1 = (int)(end - pg0 < p.page ? end - pg0 : p.page);         // behind the last
+        const int src0 = t0 + (int)(pg0 + o0 - s);                             // its packed token
+        const int chunks = (o1 - o0) * (D / 8);
+        const uint16_t* x = (kv ? p.v : p.k) + ((size_t)src0 * p.kv_heads + head) * D;
+        const size_t tstride = (size_t)p.kv_heads * D;
+        uint4 w[CH];
 #pragma unroll
-        for (int i = 0; i < THREADS / 32; ++i) top = max(top, red[i]);
-    }
-    if (odd) set_error(TBIK_ERR_VALUE);
-    int E = cache_need(cache_round4(top));  // rounding is monotone: the largest magnitude rounds to the largest
-    const size_t ph = ((size_t)kv * p.num_pages + id) * p.kv_heads + head;
-    uint8_t* dst = p.pages + ph * ((size_t)p.page * D);
-    if (o0 > 0) {
-        const int was = cache_exponent(p.scales[ph]);
-        if (THREADS > 32)
-            __syncthreads();  // every thread has read the old scale before it is replaced
-        else
-            __syncwarp();
-        if (E <= was) {
-            E = was;
-        } else {  // older tokens follow the larger scale
-            const int d = E - was;
-            for (int i = tid; i < o0 * (D / 16); i += THREADS) {
-                const int t = i / (D / 16), g = i % (D / 16);
-                uint4* q = reinterpret_cast<uint4*>(dst + (t >> 3) * (D * 8) + g * 128 + (t & 7) * 16);
-                uint4 y = *q;
-                uint32_t* a = reinterpret_cast<uint32_t*>(&y);
+        for (int c = 0; c < CH; ++c) {
+            const int i = c * THREADS + tid;
+            w[c] = make_uint4(0, 0, 0, 0);
+            if (i < chunks) w[c] = __ldg(reinterpret_cast<const uint4*>(x + (size_t)(i / (D / 8)) * tstride) + i % (D / 8));
+        }
+        // the tokens are on their way while the page is looked up
+        const int row = ROWS ? p.rows[b] : b;
+        bool bad = row < 0 || row >= p.slots || pg >= p.max_pages;
+        if (maps) {
+            if (!bad) bad = (twice[row >> 5] >> (row & 31)) & 1u;
+        } else if (ROWS && !bad) {
+            bool dup = false;
+            for (int i = tid; i < p.batch; i += THREADS) dup |= i != b && p.rows[i] == row;
+            bad = __syncthreads_or(dup);
+        }
+        int id = -1;
+        if (!bad) {
+            id = p.table[(size_t)row * p.max_pages + pg];
+            bad = id < 0 || id >= p.num_pages || p.refs[id] != 1;  // a shared page is never written
+        }
+        if (bad) {
+            if (tid == 0) set_error(TBIK_ERR_PAGE);
+            return;
+        }
+        uint32_t top2 = 0;  // largest magnitudes of the even and the odd dims
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const uint32_t v = a[k];
-                    a[k] = cache_down(v & 255u, d) | cache_down((v >> 8) & 255u, d) << 8 |
-                           cache_down((v >> 16) & 255u, d) << 16 | cache_down(v >> 24, d) << 24;
+        for (int c = 0; c < CH; ++c)
+            top2 = __vmaxu2(__vmaxu2(top2, __vmaxu2(w[c].x & 0x7fff7fffu, w[c].y & 0x7fff7fffu)),
+                            __vmaxu2(w[c].z & 0x7fff7fffu, w[c].w & 0x7fff7fffu));
+        uint32_t top = max(top2 & 0xffffu, top2 >> 16);
+        const bool odd = top >= 0x7F80u;
+        if (odd) {  // what is not finite does not count
+            top = 0;
+#pragma unroll
+            for (int c = 0; c < CH; ++c) {
+                const uint32_t a[4] = {w[c].x, w[c].y, w[c].z, w[c].w};
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const uint32_t l = a[q] & 0x7FFFu, h = (a[q] >> 16) & 0x7FFFu;
+                    if (l < 0x7F80u) top = max(top, l);
+                    if (h < 0x7F80u) top = max(top, h);
                 }
-                *q = y;
             }
         }
-    }
-    if (tid == 0) p.scales[ph] = cache_pow2(E);
-    const float down = cache_pow2(-E);
+        top = __reduce_max_sync(0xffffffffu, top);
+        if (THREADS > 32) {
+            if ((tid & 31) == 0) red[tid >> 5] = top;
+            __syncthreads();
 #pragma unroll
-    for (int c = 0; c < CH; ++c) {
-        const int i = c * THREADS + tid;
-        if (i < chunks) {
-            const int t = o0 + i / (D / 8), g = i % (D / 8);
-            const uint32_t a[4] = {w[c].x, w[c].y, w[c].z, w[c].w};
-            uint2 y;
-            if (!odd && E < 120) {  // at 120 the largest rounded value is 2^128
-                y.x = cache_quant2(a[0], down) | cache_quant2(a[1], down) << 16;
-                y.y = cache_quant2(a[2], down) | cache_quant2(a[3], down) << 16;
-            } else {
-                y.x = cache_quant(a[0] & 0xffffu, E) | cache_quant(a[0] >> 16, E) << 8 |
-                      cache_quant(a[1] & 0xffffu, E) << 16 | cache_quant(a[1] >> 16, E) << 24;
-                y.y = cache_quant(a[2] & 0xffffu, E) | cache_quant(a[2] >> 16, E) << 8 |
-                      cache_quant(a[3] & 0xffffu, E) << 16 | cache_quant(a[3] >> 16, E) << 24;
-            }
-            *reinterpret_cast<uint2*>(dst + (t >> 3) * (D * 8) + (g >> 1) * 128 + (t & 7) * 16 + (g & 1) * 8) = y;
+            for (int i = 0; i < THREADS / 32; ++i) top = max(top, red[i]);
         }
+        if (odd) set_error(TBIK_ERR_VALUE);
+        int E = cache_need(cache_round4(top));  // rounding is monotone: the largest magnitude rounds to the largest
+        const size_t ph = ((size_t)kv * p.num_pages + id) * p.kv_heads + head;
+        uint8_t* dst = p.pages + ph * ((size_t)p.page * D);
+        if (o0 > 0) {
+            const int was = cache_exponent(p.scales[ph]);
+            if (THREADS > 32)
+                __syncthreads();  // every thread has read the old scale before it is replaced
+            else
+                __syncwarp();
+            if (E <= was) {
+                E = was;
+            } else {  // older tokens follow the larger scale
+                const int d = E - was;
+                for (int i = tid; i < o0 * (D / 16); i += THREADS) {
+                    const int t = i / (D / 16), g = i % (D / 16);
+                    uint4* q = reinterpret_cast<uint4*>(dst + (t >> 3) * (D * 8) + g * 128 + (t & 7) * 16);
+                    uint4 y = *q;
+                    uint32_t* a = reinterpret_cast<uint32_t*>(&y);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const uint32_t v = a[k];
+                        a[k] = cache_down(v & 255u, d) | cache_down((v >> 8) & 255u, d) << 8 |
+                               cache_down((v >> 16) & 255u, d) << 16 | cache_down(v >> 24, d) << 24;
+                    }
+                    *q = y;
+                }
+            }
+        }
+        if (tid == 0) p.scales[ph] = cache_pow2(E);
+        const float down = cache_pow2(-E);
+#pragma unroll
+        for (int c = 0; c < CH; ++c) {
+            const int i = c * THREADS + tid;
+            if (i < chunks) {
+                const int t = o0 + i / (D / 8), g = i % (D / 8);
+                const uint32_t a[4] = {w[c].x, w[c].y, w[c].z, w[c].w};
+                uint2 y;
+                if (!odd && E < 120) {  // at 120 the largest rounded value is 2^128
+                    y.x = cache_quant2(a[0], down) | cache_quant2(a[1], down) << 16;
+                    y.y = cache_quant2(a[2], down) | cache_quant2(a[3], down) << 16;
+                } else {
+                    y.x = cache_quant(a[0] & 0xffffu, E) | cache_quant(a[0] >> 16, E) << 8 |
+                          cache_quant(a[1] & 0xffffu, E) << 16 | cache_quant(a[1] >> 16, E) << 24;
+                    y.y = cache_quant(a[2] & 0xffffu, E) | cache_quant(a[2] >> 16, E) << 8 |
+                          cache_quant(a[3] & 0xffffu, E) << 16 | cache_quant(a[3] >> 16, E) << 24;
+                }
+                *reinterpret_cast<uint2*>(dst + (t >> 3) * (D * 8) + (g >> 1) * 128 + (t & 7) * 16 + (g & 1) * 8) = y;
+            }
+        }
+    };
+    if constexpr (GROUPS > 1) {
+        for (int x = blockIdx.x * GROUPS + (int)threadIdx.x / THREADS; x < p.batch; x += gridDim.x * GROUPS) page(x);
+    } else if constexpr (ROWS) {
+        const int pages = p.tokens / p.page + 2 * p.batch;
+        for (int x = blockIdx.x; x < pages; x += gridDim.x) {
+            page(x);
+            __syncthreads();  // `red` and the page's old scale have been read
+        }
+    } else {
+        page(blockIdx.x);
     }
 }
 

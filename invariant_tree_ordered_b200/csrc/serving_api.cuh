@@ -68,19 +68,29 @@ int move_grid(const DeviceInfo* info, long long most) {
     return (int)(most < 1 ? 1 : most < full ? most : full);
 }
 
-template <int D>
-void launch_append(const CacheAppendParams& p, cudaStream_t s) {
-    if (!p.cu) {
-        cache_append_kernel<D, 32, 1><<<dim3(p.batch, p.kv_heads, 2), 32, 0, s>>>(p);
+template <int D, int THREADS, int CH, int GROUPS>
+void launch_append(const CacheAppendParams& p, const DeviceInfo* info, cudaStream_t s) {
+    long long x = GROUPS > 1 ? (p.batch + GROUPS - 1) / GROUPS : p.tokens / p.page + 2 * p.batch;
+    if (!p.rows) {
+        cache_append_kernel<D, THREADS, CH, GROUPS, false><<<dim3((unsigned)x, p.kv_heads, 2), THREADS * GROUPS, 0, s>>>(p);
         return;
     }
-    const dim3 grid(p.tokens / p.page + 2 * p.batch, p.kv_heads, 2);
+    const long long most = (2048 / (THREADS * GROUPS) * (long long)info->sms + 2 * p.kv_heads - 1) / (2 * p.kv_heads);
+    const bool maps = GROUPS > 1 || p.batch > APPEND_FEW * THREADS;
+    if (maps && x > most) x = most;
+    cache_append_kernel<D, THREADS, CH, GROUPS, true>
+        <<<dim3((unsigned)x, p.kv_heads, 2), THREADS * GROUPS, maps ? ((size_t)p.slots + 31) / 32 * 8 : 0, s>>>(p);
+}
+
+template <int D>
+void dispatch_append(const CacheAppendParams& p, const DeviceInfo* info, cudaStream_t s) {
+    if (!p.cu) return launch_append<D, 32, 1, 8>(p, info, s);
     switch (p.page * D / 8 / 128) {
-        case 1: cache_append_kernel<D, 128, 1><<<grid, 128, 0, s>>>(p); break;
-        case 2: cache_append_kernel<D, 128, 2><<<grid, 128, 0, s>>>(p); break;
-        case 4: cache_append_kernel<D, 128, 4><<<grid, 128, 0, s>>>(p); break;
-        case 8: cache_append_kernel<D, 128, 8><<<grid, 128, 0, s>>>(p); break;
-        default: cache_append_kernel<D, 256, 8><<<grid, 256, 0, s>>>(p); break;
+        case 1: return launch_append<D, 128, 1, 1>(p, info, s);
+        case 2: return launch_append<D, 128, 2, 1>(p, info, s);
+        case 4: return launch_append<D, 128, 4, 1>(p, info, s);
+        case 8: return launch_append<D, 128, 8, 1>(p, info, s);
+        default: return launch_append<D, 256, 8, 1>(p, info, s);
     }
 }
 
@@ -350,9 +360,9 @@ tbik_status tbik_cache_append(const uint16_t* k, const uint16_t* v, uint8_t* pag
     p.num_pages = num_pages, p.kv_heads = kv_heads, p.page = page;
     p.page_shift = page == 16 ? 4 : page == 32 ? 5 : page == 64 ? 6 : 7;
     if (head_dim == 128)
-        launch_append<128>(p, reinterpret_cast<cudaStream_t>(stream));
+        dispatch_append<128>(p, info, reinterpret_cast<cudaStream_t>(stream));
     else
-        launch_append<64>(p, reinterpret_cast<cudaStream_t>(stream));
+        dispatch_append<64>(p, info, reinterpret_cast<cudaStream_t>(stream));
     return launch_status();
 }
 

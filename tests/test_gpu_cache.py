@@ -167,6 +167,93 @@ def test_append_refuses_pages_it_must_not_write(packed):
     assert not attempt([0], start[:1].contiguous(), tbik.TBIK_OK)
 
 
+@pytest.mark.parametrize("batch,slots,lens", [(300, 65536, 1), (8192, 8192, 1), (8192, 9000, 40), (129, 140, 200), (1000, 1000, 7)])
+@pytest.mark.parametrize("D,page", [(64, 16), (128, 128)])
+def test_append_of_many_sequences_in_any_slots(batch, slots, lens, D, page):
+    """What a call with `rows` and `cu` writes, against the same tokens written without them into slots 0, 1, ...; slots
+    named twice, wherever in the call, are not written."""
+    if batch * lens * D > 2 ** 25:
+        lens = 10
+    H = 1
+    r = np.random.RandomState(batch + lens)
+    n = np.maximum(0, r.randint(0, lens + 1, batch)) if lens > 1 else np.ones(batch, int)
+    at = r.randint(0, 2 * page, batch)
+    most = 3 + lens // page
+    pool = int(sum(-(-int(a + m) // page) for a, m in zip(at, n))) + 5
+    pages, scales, refs = tbik.cache_pages(pool, H, D, page)
+    table, lensd = tbik.cache_table(slots, most)
+    tbik.cache_extend(table, lensd, refs, i32(at + n), page=page, rows=i32(range(batch)))
+    g = torch.Generator(device=DEV).manual_seed(1)
+    raw(pages).copy_(torch.randint(0, 127, pages.shape, dtype=torch.uint8, device=DEV, generator=g))
+    scales.copy_(torch.exp2(torch.randint(-9, 3, scales.shape, device=DEV, generator=g).float()))
+    k, v = tokens(1, int(n.sum()), H, D), tokens(2, int(n.sum()), H, D)
+    start = i32(at)
+    assert tbik.get_error() == tbik.TBIK_OK
+
+    def wrote(table, rows, packed):
+        pg, sc = pages.clone(), scales.clone()
+        tbik.cache_append(k, v, pg[0], sc[0], table, refs, start, cu=cu_of(n) if packed else None, rows=None if rows is None else i32(rows))
+        return raw(pg), sc
+
+    for packed in ([True, False] if lens == 1 else [True]):
+        ref = wrote(table, None, packed)
+        assert tbik.get_error() == tbik.TBIK_OK
+        assert not torch.equal(ref[0], raw(pages))
+        rows = r.permutation(slots)[:batch]
+        moved = torch.full_like(table, -1)
+        moved[torch.from_numpy(rows).to(DEV)] = table[:batch]
+        got = wrote(moved, rows, packed)
+        assert tbik.get_error() == tbik.TBIK_OK
+        assert torch.equal(got[0], ref[0]) and torch.equal(got[1], ref[1])
+        # the first, the last and a few others name the slot of another sequence; both of a pair stay unwritten
+        twice = rows.copy()
+        pairs = [(0, batch - 1), (batch // 2, batch // 2 + 1), (17, batch - 30)]
+        for a, b in pairs:
+            twice[b] = twice[a]
+        got = wrote(moved, twice, packed)
+        assert tbik.get_error() == tbik.TBIK_ERR_PAGE
+        want = [x.clone() for x in ref]
+        for b in [x for p in pairs for x in p]:
+            ids = table[b][table[b] >= 0].long()
+            want[0][0][:, ids] = raw(pages)[0][:, ids]
+            want[1][0][:, ids] = scales[0][:, ids]
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+@pytest.mark.parametrize("packed", [True, False])
+@pytest.mark.parametrize("with_rows", [True, False])
+def test_the_time_of_a_write_grows_with_the_call(packed, with_rows):
+    """8 times the sequences take about 8 times as long, not 8 times 8 (a search over the whole call in every block): less
+    than twice that, in a captured graph."""
+    H, D, page = 8, 128, 16
+    times = []
+    for B in (1024, 8192):
+        pages, scales, refs = tbik.cache_pages(B, H, D, page)
+        table, lens = tbik.cache_table(B, 2)
+        start = tbik.cache_extend(table, lens, refs, i32([1] * B), page=page)
+        k = torch.randn(B, H, D, device=DEV).to(torch.bfloat16)
+        kw = dict(cu=cu_of([1] * B) if packed else None, rows=i32(range(B)) if with_rows else None)
+        side = torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            g = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(g, stream=side):
+                for _ in range(10):
+                    tbik.cache_append(k, k, pages[0], scales[0], table, refs, start, **kw)
+        torch.cuda.current_stream().wait_stream(side)
+        best = 1e9
+        for _ in range(5):
+            ev = [torch.cuda.Event(enable_timing=True) for _ in range(2)]
+            ev[0].record()
+            g.replay()
+            ev[1].record()
+            torch.cuda.synchronize()
+            best = min(best, ev[0].elapsed_time(ev[1]))
+        times.append(best)
+    assert tbik.get_error() == tbik.TBIK_OK
+    assert times[1] < 16 * times[0], times
+
+
 # ---------------------------------------------------------------- attention
 
 def filled(ctx, H, D, page, seed, slots=None, spare=3):
