@@ -66,7 +66,6 @@ struct CacheAttParams {
     int group;       // heads / kv_heads
     int page_shift;  // log2(page)
     uint32_t group_inv;  // ceil(2^31 / group)
-    int blocks;      // 128-position blocks that a sequence's new tokens can touch
     float scale;     // log2(e) / sqrt(head_dim)
     // workspace: number of cut tiles, their descriptors, and the nodes' summaries
     int* count;      // [2]: cut tiles, whether a tree was cut deeper than CATT_JOIN_DEPTH
@@ -304,29 +303,40 @@ __device__ __forceinline__ int catt_usable(const CacheAttParams& p, int s, int s
     lim = min(min(lim, (long long)n), (long long)p.max_q);
     return lim > 0 ? (int)lim : 0;
 }
-__device__ __forceinline__ CattItem catt_item(const CacheAttParams& p, int i, bool& bad) {
-    CattItem t;
+// What can be answered of sequence b: its first `use` tokens, from packed token `first` and position s on (use = 0: s = 0).
+struct CattSeq {
+    int b, slot, first, s, use;
+};
+__device__ __forceinline__ CattSeq catt_seq(const CacheAttParams& p, int b, bool& bad) {
+    CattSeq q;
     int n;
-    t.b = p.blocks == 1 ? i : i / p.blocks;
-    const int kb = i - t.b * p.blocks;
-    const int first = catt_tokens(p, t.b, n);
-    const int s = p.start[t.b];
-    t.slot = p.rows ? p.rows[t.b] : t.b;
-    const int use = catt_usable(p, s, t.slot, n);
-    bad |= use < n || (p.cu && n == 0 && (first < 0 || p.cu[t.b + 1] < first || p.cu[t.b + 1] > p.tokens));
-    const int blk = (use > 0 ? s >> 7 : 0) + kb;
-    const int lo = max(0, blk * CATT_LEAF - s), hi = (int)min((long long)use, (long long)(blk + 1) * CATT_LEAF - s);
+    q.b = b;
+    q.first = catt_tokens(p, b, n);
+    q.s = p.start[b];
+    q.slot = p.rows ? p.rows[b] : b;
+    q.use = catt_usable(p, q.s, q.slot, n);
+    bad |= q.use < n || (p.cu && n == 0 && (q.first < 0 || p.cu[b + 1] < q.first || p.cu[b + 1] > p.tokens));
+    if (q.use == 0) q.s = 0;
+    return q;
+}
+// Its tokens in block blk of 128 positions.
+__device__ __forceinline__ CattItem catt_item(const CacheAttParams& p, const CattSeq& q, int blk) {
+    CattItem t;
+    const int lo = max(0, blk * CATT_LEAF - q.s), hi = min(q.use, (blk + 1) * CATT_LEAF - q.s);
+    t.b = q.b;
+    t.slot = q.slot;
     t.L = blk + 1;
-    t.tok0 = first + lo;
-    t.i0 = s + lo;
-    t.rows = use > 0 && hi > lo ? (hi - lo) * p.group : 0;
+    t.tok0 = q.first + lo;
+    t.i0 = q.s + lo;
+    t.rows = hi > lo ? (hi - lo) * p.group : 0;
     return t;
 }
 
 // Where a CTA begins: set by the whole block, read by every role.
 struct CattPlan {
     long long x0, x1, at;  // the CTA's run of the weight axis, and the weight before its first item
-    int item, slot_base, tile_base, T;
+    int b, blk;            // that item: sequence (-1: none) and block of 128 positions
+    int slot_base, tile_base, T;
 };
 
 // A unit: node v of tile `tau` of kv head h of an item (in this order, the nodes of a tile one after the other, so that
@@ -334,13 +344,12 @@ struct CattPlan {
 template <int R>
 struct CattUnits {
     CattItem it;
-    int item, h, tau, tiles, d, v, lo, size;
+    int h, tau, tiles, d, v, lo, size;
     int slot_base, tile_base, T;
     long long at, end;
 
-    __device__ __forceinline__ void enter(const CacheAttParams& p) {
-        bool bad = false;
-        it = catt_item(p, item, bad);
+    __device__ __forceinline__ void enter(const CacheAttParams& p, const CattSeq& q, int blk) {
+        it = catt_item(p, q, blk);
         tiles = (it.rows + R - 1) / R;
         d = catt_depth(it.L, T);
     }
@@ -348,16 +357,16 @@ struct CattUnits {
     __device__ __forceinline__ int imin(const CacheAttParams& p) const { return it.i0 + catt_div(p, tau * R); }
     __device__ __forceinline__ int imax(const CacheAttParams& p) const { return it.i0 + catt_div(p, min(it.rows, (tau + 1) * R) - 1); }
     __device__ __forceinline__ int slot() const { return slot_base + ((h * tiles + tau) << d) + v; }
-    __device__ __forceinline__ bool same_tile(const CattUnits& o) const { return item == o.item && h == o.h && tau == o.tau; }
+    __device__ __forceinline__ bool same_tile(const CattUnits& o) const { return it.b == o.it.b && it.L == o.it.L && h == o.h && tau == o.tau; }
     // The first unit that starts at or behind x0.
     __device__ __forceinline__ bool first(const CacheAttParams& p, const CattPlan& pl) {
-        item = pl.item;
         slot_base = pl.slot_base;
         tile_base = pl.tile_base;
         T = pl.T;
         end = pl.x1;
-        if (item < 0 || pl.x0 >= pl.x1) return false;
-        enter(p);
+        if (pl.b < 0 || pl.x0 >= pl.x1) return false;
+        bool bad = false;
+        enter(p, catt_seq(p, pl.b, bad), pl.blk);
         // a tile weighs its leaves and a start for each node that is not empty; of these there are min(v, lo) before v
         const int cost = it.L + CATT_START * min(it.L, 1 << d);
         const long long y = pl.x0 - pl.at, tile = y < (1ll << 31) ? (long long)((uint32_t)y / (uint32_t)cost) : y / cost;
@@ -399,11 +408,17 @@ struct CattUnits {
             slot_base += (p.kv_heads * tiles) << d;
             tile_base += p.kv_heads * tiles;
         }
+        // the sequence's next block, or the next sequence that has something to do
+        bool bad = false;
+        int blk = it.L;
+        CattSeq q = catt_seq(p, it.b, bad);
 #pragma unroll 1
-        do {
-            if (++item >= p.batch * p.blocks) return false;
-            enter(p);
-        } while (it.rows == 0);
+        while (blk * CATT_LEAF >= q.s + q.use) {
+            if (q.b + 1 >= p.batch) return false;
+            q = catt_seq(p, q.b + 1, bad);
+            blk = q.s / CATT_LEAF;
+        }
+        enter(p, q, blk);
         v = lo = 0;
         size = catt_node_size(it.L, d, 0);
         return true;
@@ -453,76 +468,100 @@ __device__ __forceinline__ void catt_scan(long long& w, long long& c, int& flags
     c = bc + sc - c;
 }
 
-// Fills `pl`; true if some token of the call has no answer.  One item per thread and step; with as many threads as
-// items (the usual case) every item is looked at once.
+// Fills `pl`; true if some token of the call has no answer.  Every thread takes a run of a sequence's blocks of 128
+// positions: `per` threads share a sequence when there are fewer sequences than threads, and with as many threads as runs
+// (the usual case) every sequence is read once.  Only blocks that hold tokens are looked at, so the work does not depend on
+// max_q (a call with 1024 sequences of 8 tokens and max_q left at its default took 943 us with one look per sequence and
+// block that max_q allows, and 161 us with a tight max_q).
 template <int R, int MAX_NODE>
 __device__ __forceinline__ bool catt_plan(const CacheAttParams& p, CattPlan* pl, CattScan* buf) {
-    const int items = p.batch * p.blocks, tid = threadIdx.x, nt = blockDim.x;
+    const int tid = threadIdx.x, nt = blockDim.x;
+    int shift = 0;
+    while (p.cu && (long long)p.batch << (shift + 1) <= nt) ++shift;
+    const int runs = p.batch << shift;
     bool bad = false;
-    int L = 0, flags = 0;
-    long long ht = 0, leaves = 0, total = 0, t0, t1;
+    int flags = 0;
+    CattSeq q;
+    int k0 = 0, k1 = 0;  // blocks of the run
+    auto load = [&](int i) {
+        q = catt_seq(p, i >> shift, bad);
+        const int f = q.s / CATT_LEAF, blocks = q.use ? (q.s + q.use - 1) / CATT_LEAF + 1 - f : 0, sub = i & ((1 << shift) - 1);
+        k0 = f + (int)((long long)blocks * sub >> shift);
+        k1 = f + (int)((long long)blocks * (sub + 1) >> shift);
+    };
+    auto tiles = [&](int k) { return (long long)p.kv_heads * ((catt_item(p, q, k).rows + R - 1) / R); };
+    long long leaves = 0, total = 0, t0, t1;
 #pragma unroll 1
-    for (int i = tid; i < items; i += nt) {
-        const CattItem t = catt_item(p, i, bad);
-        L = t.L;
-        ht = t.rows ? (long long)p.kv_heads * ((t.rows + R - 1) / R) : 0;
-        leaves += ht * L;
+    for (int i = tid; i < runs; i += nt) {
+        load(i);
+#pragma unroll 1
+        for (int k = k0; k < k1; ++k) leaves += tiles(k) * (k + 1);
     }
     long long unused = 0;
     catt_scan(leaves, unused, flags, buf, t0, t1);
     const long long aim = catt_div_up(t0, (int)gridDim.x * CATT_UNITS);
     const int T = (int)min((long long)MAX_NODE, max(1ll, aim));
-    // weight of a unit: its leaves and its start
-    auto weight = [&](int L, long long ht, int& d) {
-        d = catt_depth(L, T);
-        return (long long)(L + CATT_START * min(L, 1 << d)) * ht;
+    // A block's weight, which is that of its units (their leaves and their start), added to w; its slots and tiles, if its
+    // trees are cut, to c: (slots << 32) + tiles.
+    auto add = [&](int k, long long& w, long long& c) {
+        const long long ht = tiles(k);
+        const int L = k + 1, d = catt_depth(L, T);
+        w += (L + CATT_START * min(L, 1 << d)) * ht;
+        if (d) {
+            c += ((ht << d) << 32) + ht;
+            if (d > CATT_JOIN_DEPTH) flags |= 2;
+        }
     };
-    int d;
-    if (items > nt) {
+    if (runs > nt) {
         long long w = 0;
 #pragma unroll 1
-        for (int i = tid; i < items; i += nt) {
-            const CattItem t = catt_item(p, i, bad);
-            if (t.rows) w += weight(t.L, (long long)p.kv_heads * ((t.rows + R - 1) / R), d);
+        for (int i = tid; i < runs; i += nt) {
+            load(i);
+#pragma unroll 1
+            for (int k = k0; k < k1; ++k) add(k, w, unused);
         }
+        unused = 0;
         catt_scan(w, unused, flags, buf, total, t1);
     }
     if (tid == 0) {
-        pl->item = -1;
+        pl->b = -1;
         pl->T = T;
     }
-    long long at = 0, cut = 0, step = 0;  // cut: (slots << 32) + tiles of the cut ones
+    long long at = 0, cut = 0, step = 0;
     flags = 0;
 #pragma unroll 1
-    for (int base = 0; base < items; base += nt) {
-        const int i = base + tid;
+    for (int base = 0; base < runs; base += nt) {
         long long w = 0, c = 0, wt, ct;
-        if (i < items) {
-            if (items > nt) {
-                const CattItem t = catt_item(p, i, bad);
-                L = t.L;
-                ht = t.rows ? (long long)p.kv_heads * ((t.rows + R - 1) / R) : 0;
-            }
-            w = weight(L, ht, d);
-            if (d && ht) {
-                c = ((ht << d) << 32) + ht;
-                if (d > CATT_JOIN_DEPTH) flags |= 2;
-            }
+        if (base + tid < runs) {
+            if (runs > nt) load(base + tid);
+#pragma unroll 1
+            for (int k = k0; k < k1; ++k) add(k, w, c);
         }
         int f = flags | (bad ? 1 : 0);
         const long long mine = w;
         catt_scan(w, c, f, buf, wt, ct);
         flags = f;
         if (base == 0) {
-            if (items <= nt) total = wt;
+            if (runs <= nt) total = wt;
             step = catt_div_up(total, (int)gridDim.x);
         }
         const long long x0 = step * blockIdx.x;
         if (mine && at + w <= x0 && x0 < at + w + mine) {
-            pl->item = i;
-            pl->at = at + w;
-            pl->slot_base = (int)((cut + c) >> 32);
-            pl->tile_base = (int)((cut + c) & 0xffffffff);
+            long long a = at + w, e = cut + c, next = a;
+            int k = k0;
+#pragma unroll 1
+            for (;; ++k) {
+                long long ne = e;
+                add(k, next, ne);
+                if (x0 < next) break;
+                a = next;
+                e = ne;
+            }
+            pl->b = q.b;
+            pl->blk = k;
+            pl->at = a;
+            pl->slot_base = (int)(e >> 32);
+            pl->tile_base = (int)(e & 0xffffffff);
         }
         at += wt;
         cut += ct;

@@ -105,7 +105,7 @@ tbik_status check_attention(int tokens, int batch, int max_q, int max_keys, int 
 // Rows of a tile, grid and workspace of an attention call.
 struct CattSplit {
     int rows;    // rows per tile: 8, 16 or 32
-    int blocks, grid, slots;
+    int grid, slots;
     size_t off_tiles, off_ms, off_o, bytes;
 };
 
@@ -120,9 +120,8 @@ tbik_status plan_cache_attention(int tokens, int batch, int max_q, int max_keys,
     // 32 rows 125 us, 150 us in two tiles of 16.  (Tiles of 64 rows by eight warps in one block an SM instead of
     // four warps in two were slower: 512 rows 1370 us against 1290 us.)
     c.rows = most <= 8 ? 8 : most <= 16 ? 16 : 32;
-    c.blocks = ((max_q < tokens ? max_q : tokens) + 126) / 128 + 1;
-    const long long items = (long long)batch * c.blocks;
-    if (items > (1 << 30)) return TBIK_ERR_SHAPE;
+    // blocks of 128 positions that hold tokens: a sequence's touch one more than they fill, and each holds one
+    const long long items = (long long)batch * (((max_q < tokens ? max_q : tokens) + 126) / 128 + 1);
     const int ctas = c.rows == 8 ? 3 : 2;
     const long long leaves = (max_keys + CATT_LEAF - 1) / CATT_LEAF;
     const long long tiles = (long long)kv_heads * ((long long)tokens * group / c.rows + (items < tokens ? items : tokens));
@@ -403,7 +402,6 @@ tbik_status tbik_cache_attention(const uint16_t* q, const uint8_t* pages, const 
     p.group = heads / kv_heads;
     p.group_inv = ((1u << 31) + (unsigned)p.group - 1) / (unsigned)p.group;
     p.page_shift = page == 16 ? 4 : page == 32 ? 5 : page == 64 ? 6 : 7;
-    p.blocks = c.blocks;
     p.scale = (float)(1.4426950408889634 / std::sqrt((double)head_dim));
     if (c.slots) {
         uint8_t* w = reinterpret_cast<uint8_t*>(ws);

@@ -731,6 +731,55 @@ def test_attention_bounds_that_are_too_tight_and_offsets_that_cannot_be():
         assert torch.equal(out[which], good[which]) and (out[rest] == 3.0).all()
 
 
+def captured_time(f, calls=5):
+    """Device time of `calls` calls in a captured graph, the best of five replays."""
+    f()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=side):
+            for _ in range(calls):
+                f()
+    torch.cuda.current_stream().wait_stream(side)
+    best = 1e9
+    for _ in range(5):
+        ev = [torch.cuda.Event(enable_timing=True) for _ in range(2)]
+        ev[0].record()
+        g.replay()
+        ev[1].record()
+        torch.cuda.synchronize()
+        best = min(best, ev[0].elapsed_time(ev[1]))
+    return best
+
+
+@pytest.mark.parametrize("batch,n,ctx", [(1024, 8, 100), (3000, 5, 60), (3, 700, 900), (1, 5000, 300), (191, 3, 500), (193, 130, 140)])
+def test_bounds_left_at_their_defaults(batch, n, ctx):
+    """max_q = all tokens: the same bits, in about the same time (the output's fill and a larger workspace come on top)."""
+    H, heads, D, page = 1, 2, 64, 64
+    r = np.random.RandomState(batch)
+    new = r.randint(0, n + 1, batch)
+    new[-1] = n
+    before = r.randint(0, ctx + 1, batch)
+    c, rows = filled((before + new).tolist(), H, D, page, seed=batch) if batch < 1000 else (None, None)
+    if c is None:  # one page run for all
+        c = Cache(batch, -(-(ctx + n) // page), 40, H, D, page)
+        raw(c.pages).copy_(torch.randint(0, 120, c.pages.shape, dtype=torch.uint8, device=DEV))
+        c.table.copy_(torch.from_numpy(r.randint(0, 40, c.table.shape)).to(DEV))
+        rows = list(range(batch))
+    T = int(new.sum())
+    q = torch.randn(T, heads, D, device=DEV).to(torch.bfloat16)
+    args = (q, c.pages[0], c.scales[0], c.table, i32(before))
+    kw = dict(cu=cu_of(new), rows=i32(rows))
+    tight = dict(max_q=int(new.max()), max_keys=int((before + new).max()))
+    want = tbik.cache_attention(*args, **kw, **tight)
+    assert torch.equal(tbik.cache_attention(*args, **kw), want) and not torch.isnan(want).any()
+    assert tbik.get_error() == tbik.TBIK_OK
+    out = torch.empty_like(q)
+    times = [captured_time(lambda: tbik.cache_attention(*args, out=out, **kw, **b)) for b in (tight, {})]
+    assert times[1] < 1.5 * times[0] + 0.05, times  # ms for five calls
+
+
 def test_the_same_slot_for_many_sequences_and_two_streams_at_once():
     """Reading needs no slot of its own: 300 queries over one sequence, in two calls that run side by side."""
     H, heads, D, page = 1, 4, 128, 64
