@@ -780,6 +780,21 @@ def test_bounds_left_at_their_defaults(batch, n, ctx):
     assert times[1] < 1.5 * times[0] + 0.05, times  # ms for five calls
 
 
+def test_default_bounds_take_the_tiles_of_short_sequences():
+    """24 sequences with a few drafted tokens each: with max_q = all tokens in the time of the tight bound."""
+    H, D, page, batch = 16, 64, 32, 24
+    new = [1 + i % 5 for i in range(batch)]
+    before = [300 + 150 * i for i in range(batch)]
+    c, rows = filled([a + b for a, b in zip(before, new)], H, D, page, seed=1)
+    q = torch.randn(sum(new), H, D, device=DEV).to(torch.bfloat16)
+    out = torch.empty_like(q)
+    args, kw = (q, c.pages[0], c.scales[0], c.table, i32(before)), dict(cu=cu_of(new), rows=i32(rows), max_keys=4096)
+    want = tbik.cache_attention(*args, max_q=5, **kw)
+    assert torch.equal(tbik.cache_attention(*args, **kw), want)
+    times = [captured_time(lambda: tbik.cache_attention(*args, out=out, **b, **kw)) for b in (dict(max_q=5), {})]
+    assert times[1] < 1.25 * times[0], times
+
+
 def test_the_same_slot_for_many_sequences_and_two_streams_at_once():
     """Reading needs no slot of its own: 300 queries over one sequence, in two calls that run side by side."""
     H, heads, D, page = 1, 4, 128, 64
