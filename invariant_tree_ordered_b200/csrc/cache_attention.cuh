@@ -335,7 +335,7 @@ __device__ __forceinline__ CattItem catt_item(const CacheAttParams& p, const Cat
 // Where a CTA begins: set by the whole block, read by every role.
 struct CattPlan {
     long long x0, x1, at;  // the CTA's run of the weight axis, and the weight before its first item
-    int b, blk;            // that item: sequence (-1: none) and block of 128 positions
+    CattItem it;           // that item (no rows: none)
     int slot_base, tile_base, T;
 };
 
@@ -348,8 +348,8 @@ struct CattUnits {
     int slot_base, tile_base, T;
     long long at, end;
 
-    __device__ __forceinline__ void enter(const CacheAttParams& p, const CattSeq& q, int blk) {
-        it = catt_item(p, q, blk);
+    __device__ __forceinline__ void enter(const CattItem& i) {
+        it = i;
         tiles = (it.rows + R - 1) / R;
         d = catt_depth(it.L, T);
     }
@@ -364,9 +364,8 @@ struct CattUnits {
         tile_base = pl.tile_base;
         T = pl.T;
         end = pl.x1;
-        if (pl.b < 0 || pl.x0 >= pl.x1) return false;
-        bool bad = false;
-        enter(p, catt_seq(p, pl.b, bad), pl.blk);
+        if (pl.it.rows == 0 || pl.x0 >= pl.x1) return false;
+        enter(pl.it);
         // a tile weighs its leaves and a start for each node that is not empty; of these there are min(v, lo) before v
         const int cost = it.L + CATT_START * min(it.L, 1 << d);
         const long long y = pl.x0 - pl.at, tile = y < (1ll << 31) ? (long long)((uint32_t)y / (uint32_t)cost) : y / cost;
@@ -418,7 +417,7 @@ struct CattUnits {
             q = catt_seq(p, q.b + 1, bad);
             blk = q.s / CATT_LEAF;
         }
-        enter(p, q, blk);
+        enter(catt_item(p, q, blk));
         v = lo = 0;
         size = catt_node_size(it.L, d, 0);
         return true;
@@ -524,7 +523,7 @@ __device__ __forceinline__ bool catt_plan(const CacheAttParams& p, CattPlan* pl,
         catt_scan(w, unused, flags, buf, total, t1);
     }
     if (tid == 0) {
-        pl->b = -1;
+        pl->it.rows = 0;
         pl->T = T;
     }
     long long at = 0, cut = 0, step = 0;
@@ -550,15 +549,14 @@ __device__ __forceinline__ bool catt_plan(const CacheAttParams& p, CattPlan* pl,
             long long a = at + w, e = cut + c, next = a;
             int k = k0;
 #pragma unroll 1
-            for (;; ++k) {
+            for (; k + 1 < k1; ++k) {
                 long long ne = e;
                 add(k, next, ne);
                 if (x0 < next) break;
                 a = next;
                 e = ne;
             }
-            pl->b = q.b;
-            pl->blk = k;
+            pl->it = catt_item(p, q, k);
             pl->at = a;
             pl->slot_base = (int)(e >> 32);
             pl->tile_base = (int)(e & 0xffffffff);
