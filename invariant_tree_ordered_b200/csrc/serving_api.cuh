@@ -127,14 +127,18 @@ tbik_status plan_cache_attention(int tokens, int batch, int max_q, int max_keys,
     const long long items = (long long)batch * (((max_q < tokens ? max_q : tokens) + 126) / 128 + 1);
     const int ctas = c.rows == 8 ? 3 : 2;
     const long long leaves = (max_keys + CATT_LEAF - 1) / CATT_LEAF;
-    const long long tiles = (long long)kv_heads * ((long long)tokens * group / c.rows + (items < tokens ? items : tokens));
+    // tiles: one for each of the blocks where a block's rows fit one, else a full one for every c.rows rows and one more for
+    // each block
+    const long long held = items < tokens ? items : tokens, rows = (long long)(max_q < 128 ? max_q : 128) * group;
+    const long long tiles = kv_heads * (rows <= c.rows ? held : ((long long)tokens * group + held * (c.rows - 1)) / c.rows);
     const long long work = tiles * leaves;
     const long long full = (long long)sms * ctas;
     c.grid = (int)(work < full ? work : full);
     if (leaves > 1) {
-        // a cut tile of L leaves has fewer than 2 L / T nodes, T >= all leaves / (grid * CATT_UNITS) or the cap
-        // (32 or 64)
-        const long long by_grid = 2ll * c.grid * CATT_UNITS, by_cap = 2 * work / 32;
+        // a cut tile of L leaves has fewer than 2 L / T nodes; T is at least all leaves / (grid * CATT_UNITS), or the
+        // kernel's cap (CattCfg::MAX_NODE)
+        const long long by_grid = 2ll * c.grid * CATT_UNITS, by_cap = 2 * work / (c.rows == 32 ? CattCfg<128, 32>::MAX_NODE : CattCfg<128, 8>::MAX_NODE);
+        static_assert(CattCfg<128, 8>::MAX_NODE == CattCfg<128, 16>::MAX_NODE && CattCfg<64, 32>::MAX_NODE == CattCfg<128, 32>::MAX_NODE, "caps");
         long long slots = by_grid > by_cap ? by_grid : by_cap;
         if (slots > 2 * work) slots = 2 * work;
         slots += 2;

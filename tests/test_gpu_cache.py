@@ -795,6 +795,27 @@ def test_default_bounds_take_the_tiles_of_short_sequences():
     assert times[1] < 1.25 * times[0], times
 
 
+def test_workspace_of_a_loose_bound():
+    """64 sequences over a table of 131072 positions: 8 heads x 64 tiles of 1024 leaves in nodes of 32 to 64 make up to 2 x 16
+    of them, of 8 rows and 128 dims in fp32 (67 MB) and a little more."""
+    nodes = 8 * 64 * 32
+    need = tbik.cache_attention_workspace(64, 64, 1, 131072, 32, 8, 128, 64)
+    assert nodes * 8 * 128 * 4 <= need <= 1.03 * nodes * 8 * 128 * 4
+    # a call that makes the most of it: every sequence a little above 64 or 128 leaves, so that nodes are small
+    for batch, ctx in ((300, 64 * 128 + 1), (200, 128 * 128 + 1)):
+        H, heads, D, page = 1, 8, 64, 128
+        c = Cache(batch, -(-(ctx + 1) // page), 50, H, D, page)
+        raw(c.pages).copy_(torch.randint(0, 120, c.pages.shape, dtype=torch.uint8, device=DEV))
+        c.scales.fill_(2.0 ** -7)
+        c.table.copy_(torch.from_numpy(np.random.RandomState(1).randint(0, 50, c.table.shape)).to(DEV))
+        q = torch.randn(batch, heads, D, device=DEV).to(torch.bfloat16)
+        got = tbik.cache_attention(q, c.pages[0], c.scales[0], c.table, i32([ctx] * batch), max_keys=ctx + 1)
+        for b in (0, batch // 2, batch - 1):
+            one = tbik.cache_attention(q[b:b + 1].contiguous(), c.pages[0], c.scales[0], c.table, i32([ctx]), rows=i32([b]), max_keys=ctx + 1)
+            assert torch.equal(one[0], got[b])
+        assert tbik.get_error() == tbik.TBIK_OK and torch.isfinite(got).all()
+
+
 def test_the_same_slot_for_many_sequences_and_two_streams_at_once():
     """Reading needs no slot of its own: 300 queries over one sequence, in two calls that run side by side."""
     H, heads, D, page = 1, 4, 128, 64
