@@ -62,7 +62,8 @@ typedef enum {
     TBIK_ERR_CUDA = 5,        /* a CUDA runtime/driver call failed */
     TBIK_ERR_TIMEOUT = 6,     /* a device-side bounded wait expired (kernel returned early) */
     TBIK_ERR_TARGET = 7,      /* a logprob target outside [0, V) (its output is NaN) */
-    TBIK_ERR_POSITION = 8,    /* a RoPE position outside [0, max_pos) (its outputs are NaN) */
+    TBIK_ERR_POSITION = 8,    /* a RoPE position outside [0, max_pos) (its outputs are NaN), or packed offsets (cu)
+                                 outside the tokens of a cache call */
     TBIK_ERR_UNSUPPORTED = 9, /* not a B200-class device (sm_100) */
     TBIK_ERR_PAGE = 10,       /* cache: a table row, page number, length or reference that cannot be, or no room */
     TBIK_ERR_VALUE = 11       /* an input that is not finite where a number is needed (cache writes, logits) */
@@ -498,7 +499,8 @@ TBIK_API tbik_status tbik_cache_copy(uint8_t* pages, float* scales, const int32_
  * Writes new tokens of one layer.  k, v bf16 [tokens][kv_heads][head_dim]; the
  * tokens of sequence b are cu[b] .. cu[b+1]-1 (cu int32 [batch+1], ascending;
  * NULL: token b is sequence b's only one) at positions start[b], start[b]+1, ...
- * (start[b] < 0: nothing is written for b).  The value stored for x is
+ * (start[b] < 0: nothing is written for b; a range outside the tokens is passed
+ * over with TBIK_ERR_POSITION).  The value stored for x is
  *   cut(round4(x) * 2^-E) * 2^E:  round4 to 4 significant bits (nearest even),
  *   cut = truncation to e4m3's grid (spacing 2^-9 below 2^-6);  2^E the page's
  *   scale: the smallest with max |round4| <= 448 * 2^E over the tokens the page

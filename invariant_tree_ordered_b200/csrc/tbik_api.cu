@@ -671,7 +671,7 @@ const char* tbik_status_string(tbik_status s) {
         case TBIK_ERR_CUDA: return "CUDA error";
         case TBIK_ERR_TIMEOUT: return "device wait timed out";
         case TBIK_ERR_TARGET: return "target index out of range";
-        case TBIK_ERR_POSITION: return "RoPE position out of range";
+        case TBIK_ERR_POSITION: return "RoPE position or packed token offset out of range";
         case TBIK_ERR_UNSUPPORTED: return "device is not sm_100";
         case TBIK_ERR_PAGE: return "cache row, page or length out of range, or no room";
         case TBIK_ERR_VALUE: return "input is not finite";

@@ -89,3 +89,9 @@ def test_host_only_queries_and_refusals():
         tbik.cache_compact(pages, scales, table, lens, refs)
     with pytest.raises(ValueError):
         tbik.cache_pages(4, 2, 64, 24, device="cpu")
+
+
+def test_the_position_status_names_packed_offsets():
+    """The cache's calls return it for offsets outside the tokens, RoPE for positions outside the table."""
+    text = tbik.status_string(B.TBIK_ERR_POSITION)
+    assert "RoPE position" in text and "packed token offset" in text and "out of range" in text

@@ -167,6 +167,20 @@ def test_append_refuses_pages_it_must_not_write(packed):
     assert not attempt([0], start[:1].contiguous(), tbik.TBIK_OK)
 
 
+def test_append_passes_over_offsets_that_cannot_be():
+    H, D, page = 2, 64, 16
+    for cu in ([0, 5, 10], [0, 5, 4], [-1, 5, 9]):  # beyond the tokens, descending, before the first
+        c = Cache(2, 2, 6, H, D, page)
+        start = c.extend([0, 1], [5, 4])
+        k, v = tokens(1, 9, H, D), tokens(2, 9, H, D)
+        untouched = raw(c.pages).clone()
+        tbik.cache_append(k, v, c.pages[0], c.scales[0], c.table, c.refs, start, cu=i32(cu))
+        assert tbik.get_error() == tbik.TBIK_ERR_POSITION
+        good, a, b = (0, 0, 5) if cu[0] == 0 else (1, 5, 9)
+        check_written(c, good, k[a:b], v[a:b])
+        assert torch.equal(raw(c.pages)[0][:, int(c.table[1 - good, 0])], untouched[0][:, int(c.table[1 - good, 0])])
+
+
 @pytest.mark.parametrize("batch,slots,lens", [(300, 65536, 1), (8192, 8192, 1), (8192, 9000, 40), (129, 140, 200), (1000, 1000, 7)])
 @pytest.mark.parametrize("D,page", [(64, 16), (128, 128)])
 def test_append_of_many_sequences_in_any_slots(batch, slots, lens, D, page):
