@@ -629,6 +629,8 @@ def _bytes_on(nbytes, device, workspace, stream):
         if nbytes == 0:
             return None, None, 0
         workspace = _new(nbytes, torch.uint8, device, stream)
+    elif not workspace.is_contiguous():  # the bytes of an expanded tensor are fewer than its elements
+        raise ValueError("workspace must be contiguous")
     return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 

@@ -66,3 +66,26 @@ def test_logprob_attention_embedding_transpose():
     with pytest.raises(ValueError):
         tbik.transpose(z(3, 5), out=z(3, 5))
     assert tbik.get_error() == tbik.TBIK_OK
+
+
+def test_cache_workspaces_hold_as_many_bytes_as_they_say():
+    """An expanded tensor has one element's memory."""
+    pages, scales, refs = tbik.cache_pages(64, kv_heads=1, head_dim=64, page=16)
+    table, lens = tbik.cache_table(2, 60)
+    i32 = lambda *v: torch.tensor(v, dtype=torch.int32, device="cuda")  # noqa: E731
+    start = tbik.cache_extend(table, lens, refs, i32(700), page=16)
+    thin = torch.zeros(1, dtype=torch.uint8, device="cuda").expand(1 << 22)
+    odd = torch.zeros(1 << 22, dtype=torch.uint8, device="cuda")[::2]
+    for ws in (thin, odd):
+        with pytest.raises(ValueError):
+            tbik.cache_attention(z(1, 4, 64), pages[0], scales[0], table, start, workspace=ws)
+        with pytest.raises(ValueError):
+            tbik.cache_fork(pages, scales, table, lens, refs, i32(0), i32(1), workspace=ws)
+        with pytest.raises(ValueError):
+            tbik.cache_compact(pages, scales, table, lens, refs, workspace=ws)
+        with pytest.raises(ValueError):
+            tbik.cache_copy(pages, scales, i32(0), i32(60), workspace=ws)
+    with pytest.raises(ValueError):  # on another device
+        tbik.cache_copy(pages, scales, i32(0), i32(60), workspace=torch.zeros(1 << 10, dtype=torch.uint8))
+    tbik.cache_attention(z(1, 4, 64), pages[0], scales[0], table, i32(699), workspace=torch.zeros(1 << 22, dtype=torch.uint8, device="cuda"))
+    assert tbik.get_error() == tbik.TBIK_OK
