@@ -446,7 +446,10 @@ TBIK_API tbik_status tbik_logprob_noalloc(const uint16_t* hidden, const uint16_t
  * Room for n_new[b] (>= 0) more tokens of sequence b: start[b] = its length
  * before the call (the position of the first new token) and lens grows, or
  * start[b] = -1 for every b when the call is refused.  Once per step, before
- * the layers write and read.
+ * the layers write and read.  A caller that shortens a sequence itself (lens
+ * lowered after a draft was rejected) also gives up the pages behind the new
+ * length, refs less one and table -1 for each: extend puts new pages there
+ * without looking at the entries.
  */
 TBIK_API tbik_status tbik_cache_extend(int32_t* table, int32_t* lens, int32_t* refs, const int32_t* rows,
                                        const int32_t* n_new, int32_t* start, int batch, int slots, int max_pages,
@@ -507,9 +510,15 @@ TBIK_API tbik_status tbik_cache_copy(uint8_t* pages, float* scales, const int32_
  *   holds so far, E >= -100.
  * When a token raises E, the page's older bytes are cut again under the larger
  * scale (a query that ran before saw them under the smaller one: a replay that
- * wants its bits writes and attends in the same steps).  A page's contents therefore depend on its tokens only, not on how
- * they were split into calls.  Bytes of positions that no token has reached
- * stay as they are.  Infinities are stored as +-448 * 2^E and NaN as 0, neither
+ * wants its bits writes and attends in the same steps).  As long as positions
+ * are written once and in order, a page's contents therefore depend on its
+ * tokens only, not on how they were split into calls.  A position that is
+ * written again (the token of a draft that was rejected) holds the new token,
+ * but the page keeps a scale that the old one raised, and with it the coarser
+ * grid.  Only a call that begins at the page's first position sets the scale
+ * anew; bytes behind its tokens are then still those of the old scale, to be
+ * written again before they are read.  Bytes of positions that no token has
+ * reached stay as they are.  Infinities are stored as +-448 * 2^E and NaN as 0, neither
  * counts for E, and TBIK_ERR_VALUE is recorded.  A page that is not in the
  * pool, that another sequence shares (refs != 1) or whose slot the call names
  * twice is not written, and TBIK_ERR_PAGE is recorded.
@@ -528,9 +537,11 @@ TBIK_API tbik_status tbik_cache_append(const uint16_t* k, const uint16_t* v, uin
  * multiple of kv_heads, at most 64 times it, and consecutive heads share a kv
  * head.  Leaves of 128 positions, each a (max, sum, weighted sum) summary,
  * combined by TREE over the ceil((i+1)/128) leaves like in tbik_attention_tc.
- * A row's bits depend on its query and on the cache's contents at positions
- * 0..i, not on the batch, the other queries, page numbers or the device's load.
- * The weights are rounded to 2^-9 relative, or 2^-18 of the leaf's largest times
+ * A row's bits depend on its query and on the bytes at positions 0..i and the
+ * scales of their pages (the last page's covers what else it holds by then), not
+ * on the batch, the other queries, page numbers or the device's load.  Scores
+ * and weighted sums are fp32: keys beyond 2^100, or values whose weighted sum
+ * passes 2^127, may give infinities or NaN.  The weights are rounded to 2^-9 relative, or 2^-18 of the leaf's largest times
  * the ratio of its value scales, the output once; checked against the binary64
  * definition by tolerance.
  *   max_q     no sequence has more than max_q new tokens

@@ -27,8 +27,9 @@ __device__ __forceinline__ int cache_exponent(float s) { return (int)(__float_as
 // even) and cut = truncation to e4m3's grid, which only matters below 2^-6 (spacing 2^-9).  E is the smallest
 // exponent with max |r| <= 448 * 2^E over the page's tokens so far, at least CACHE_EMIN.  When a later token raises
 // E, the older bytes are cut again on the coarser grid.  Truncations on nested grids compose (cut after cut is the
-// coarser cut), and r does not depend on E, so a page's bytes are a function of its tokens alone and not of how the
-// tokens were split into calls; rounding twice to nearest would not have that property.  Everything below is integer
+// coarser cut), and r does not depend on E, so the bytes of a page whose positions are written once and in order are a
+// function of its tokens alone and not of how the tokens were split into calls; rounding twice to nearest would not have
+// that property.  (A position written again leaves the scale that its first token raised.)  Everything below is integer
 // arithmetic on the bit patterns, hence exact.
 
 // bf16 magnitude bits (15) -> magnitude bits rounded to 3 mantissa bits (the low 4 bits are zero afterwards; a carry

@@ -167,6 +167,57 @@ def test_append_refuses_pages_it_must_not_write(packed):
     assert not attempt([0], start[:1].contiguous(), tbik.TBIK_OK)
 
 
+@pytest.mark.parametrize("page,D", [(16, 64), (64, 128)])
+def test_rejected_drafts_are_written_over(page, D):
+    """Drafts are written, some rejected and other tokens written over them from there, at places inside a page and at its
+    first position, with sizes over many binades: the new tokens are held, and a scale that a rejected one raised stays
+    until the page begins anew.  lens is lowered, and pages behind it given up, as the header says."""
+    H, r = 2, np.random.RandomState(page)
+    c = Cache(1, 8, 8, H, D, page)
+    vals = np.full((2, 8 * page, H, D), np.nan)  # in units of the page's scale; nan: not reached
+    E = np.zeros((2, 8, H), int)
+    n = 0
+    for step in range(30):
+        m = int(r.choice([1, 3, 5, page - 1, page + 2]))
+        if n + m > 8 * page:
+            break
+        start = c.extend([0], [m])
+        x = [tokens(2 * step + kv, m, H, D) for kv in (0, 1)]
+        c.append(*x, start, [m], [0])
+        for kv in (0, 1):
+            xs = x[kv].double().cpu().numpy()
+            for pg in range(n // page, (n + m - 1) // page + 1):
+                o0, o1 = max(n - pg * page, 0), min(n + m - pg * page, page)
+                for h in range(H):
+                    new = cm.round4(xs[pg * page + o0 - n:pg * page + o1 - n, h])
+                    e = cm.need(np.abs(new).max())
+                    v = vals[kv, pg * page:(pg + 1) * page, h]
+                    if o0:
+                        e = max(e, E[kv, pg, h])
+                        v[:o0] = cm.cut(v[:o0] * 2.0 ** (E[kv, pg, h] - e))
+                    v[o0:o1] = cm.cut(new * 2.0 ** -e)
+                    E[kv, pg, h] = e
+        n += m
+        held = c.book.table[0, :c.book.pages_of(n)]
+        got = cm.unpack(raw(c.pages)[0][:, held].cpu().numpy())  # [2, pages, H, page, D]
+        sc = c.scales[0][:, held].cpu().numpy()
+        assert np.array_equal(sc, np.exp2(E[:, :len(held)]).astype(np.float32))
+        got = got.transpose(0, 1, 3, 2, 4).reshape(2, -1, H, D)[:, :n]
+        assert np.array_equal(got, vals[:, :n])
+        # some of the step's tokens are rejected
+        n -= int(r.randint(0, m + 1))
+        keep = c.book.pages_of(n)
+        for j in range(keep, 8):
+            if c.book.table[0, j] >= 0:
+                c.book.refs[c.book.table[0, j]] -= 1
+                c.book.table[0, j] = -1
+        c.book.lens[0] = n
+        c.table.copy_(torch.from_numpy(c.book.table).to(DEV))
+        c.refs.copy_(torch.from_numpy(c.book.refs).to(DEV))
+        c.lens.fill_(n)
+    assert step > 8 and tbik.get_error() == tbik.TBIK_OK
+
+
 def test_append_passes_over_offsets_that_cannot_be():
     H, D, page = 2, 64, 16
     for cu in ([0, 5, 10], [0, 5, 4], [-1, 5, 9]):  # beyond the tokens, descending, before the first
