@@ -408,6 +408,77 @@ def test_attention_matches_binary64(H, heads, D, page, before, n):
         assert torch.equal(one, got[:T])
 
 
+def weighted_reference(c, q, rows, start, n):
+    """float64 attention, the sums of |weight x value|, the square sums of them, and what the weights' floor can take: 2^-18 of
+    the leaf's largest weight for each of its keys, in units of the largest value that the leaf's pages can hold."""
+    q = q.double().cpu().numpy()
+    T, NH, D = q.shape
+    G = NH // c.H
+    out, av, sq, floor, at = np.zeros(q.shape), np.zeros(q.shape), np.zeros(q.shape), np.zeros((T, NH)), 0
+    for r, s, m in zip(rows, start, n):
+        if m == 0:
+            continue
+        kv = c.stored(r, s + m)
+        ids = c.book.table[r, :c.book.pages_of(s + m)]
+        vs = 448 * c.scales[0][1, ids].double().cpu().numpy()
+        for h in range(NH):
+            k, v = kv[0, h // G], kv[1, h // G]
+            a = q[at:at + m, h] @ k.T / np.sqrt(D)
+            a[np.arange(s + m)[None] > s + np.arange(m)[:, None]] = -np.inf
+            a = np.exp(a - a.max(1, keepdims=True))
+            a /= a.sum(1, keepdims=True)
+            out[at:at + m, h], av[at:at + m, h], sq[at:at + m, h] = a @ v, a @ np.abs(v), (a * a) @ (v * v)
+            big = np.repeat(vs[:, h // G], c.page)[:s + m]
+            for l in range(0, s + m, 128):
+                floor[at:at + m, h] += 2.0 ** -18 * a[:, l:l + 128].max(1) * big[l:l + 128].max() * min(128, s + m - l)
+        at += m
+    return out, av, sq, floor
+
+
+@pytest.mark.parametrize("H,heads,D,page,before,n", [
+    (2, 8, 128, 64, [4100, 15, 1000], [1, 1, 1]), (1, 16, 128, 32, [10, 2000], [3, 140]), (2, 2, 64, 16, [0, 9000], [300, 2]),
+    (4, 16, 64, 128, [20000], [5]), (2, 16, 128, 16, [700, 127, 128], [1, 2, 1])])
+def test_attention_is_as_close_as_its_weights(H, heads, D, page, before, n):
+    """Each output within the bound of its own weights, and all of them together as close as roundings that do not know of
+    one another.
+
+    A weight p is two e4m3 terms: off by 2^-9 p at most, or by the floor.  Scores are off by less than 2^-13 (fp32 sums and the
+    hardware's exponential at |s| < 100), which moves a weight and the sum of the weights by 2^-13 each, and with them the
+    output by 2^-12 sum(p |v|); fp32 sums of values add less than 2^-14 of it.  The output is rounded to bf16: 2^-8.
+    The errors of the roundings are spread evenly, a third of their largest square each: over n outputs the mean square is
+    sum((2^-9 p v)^2) / 3 + (2^-8 out)^2 / 3, whose estimate strays by less than a quarter for the 768 and more outputs here."""
+    c, rows = filled([b + m for b, m in zip(before, n)], H, D, page, seed=page + D, slots=len(before) + 1)
+    g = torch.Generator(device=DEV).manual_seed(3)
+    q = (torch.randn(sum(n), heads, D, device=DEV, generator=g) * 2).to(torch.bfloat16)
+    got = c.attend(q, i32(before), n, rows).double().cpu().numpy()
+    assert tbik.get_error() == tbik.TBIK_OK
+    ref, av, sq, floor = weighted_reference(c, q, rows, before, n)
+    err = np.abs(got - ref)
+    lim = (2.0 ** -9 + 2.0 ** -12 + 2.0 ** -14) * av + floor[..., None] + 2.0 ** -8 * np.abs(ref)
+    assert (err <= lim).all(), float((err / lim).max())
+    rms, want = (err ** 2).mean(), (sq * 2.0 ** -18 / 3 + ref ** 2 * 2.0 ** -16 / 3).mean()
+    assert rms <= 1.25 * want, rms / want
+
+
+def test_queries_that_are_not_finite():
+    """A row whose query holds an infinity or a NaN anywhere is NaN; every other row keeps its bits, in tiles of every
+    size, in cut and uncut trees."""
+    H, D, page = 2, 64, 16
+    for heads, before, n in ((8, [5, 3000, 90], [1, 1, 1]), (8, [5, 2000], [3, 40]), (32, [700], [1])):
+        c, rows = filled([b + m for b, m in zip(before, n)], H, D, page, seed=7)
+        q = torch.randn(sum(n), heads, D, device=DEV).to(torch.bfloat16)
+        good = c.attend(q, i32(before), n, rows)
+        bad = torch.zeros(sum(n), heads, dtype=torch.bool, device=DEV)
+        x = q.clone()
+        for i, value in enumerate((float("nan"), float("inf"), float("-inf"), float("nan"))):
+            t, h, d = (5 * i) % sum(n), (3 * i + 1) % heads, (17 * i) % D
+            x[t, h, d] = value
+            bad[t, h] = True
+        got = c.attend(x, i32(before), n, rows)
+        assert torch.isnan(got[bad]).all() and torch.equal(got[~bad], good[~bad])
+        assert tbik.get_error() == tbik.TBIK_OK
+
+
 def test_attention_bits_do_not_depend_on_batch_split_or_pages():
     H, heads, D = 2, 8, 128
     before, n = [0, 60, 127, 500, 2600, 1023, 9000], [1, 80, 2, 33, 40, 1, 5]

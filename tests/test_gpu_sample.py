@@ -236,3 +236,96 @@ def test_a_background_of_2_to_the_minus_9(temp, back, p):
     z[:, 123] = 0.0
     check(z, np.linspace(0.02, 0.98, 8), temp=temp, p=p)
     assert tbik.get_error() == tbik.TBIK_OK
+
+
+# ------------------------------------------------- the kept set itself
+
+SLACK = 2.0 ** -20  # of the row's mass: fp32 weights off by a few 2^-24 each, all one way at worst, and units of 2^-32
+
+
+def strict(logits, u, temp=None, k=None, p=None, mp=None):
+    """Every token is one that the filters keep.  Only a token whose mass before it (top-p) or whose weight (min-p) is within
+    the slack of the limit may be kept or not; top-k and ties are exact.  Returns how many of the rows had no such token."""
+    B, V = logits.shape
+    f = lambda x, dt: None if x is None else torch.tensor(np.broadcast_to(x, B).copy(), dtype=dt, device=DEV)  # noqa: E731
+    ut = f(u, torch.float32)
+    t, kk, pp, mm = f(temp, torch.float32), f(k, torch.int32), f(p, torch.float32), f(mp, torch.float32)
+    got = tbik.sample(logits, ut, temperature=t, top_k=kk, top_p=pp, min_p=mm).cpu().numpy()
+    z = logits.float().cpu().numpy().astype(np.float64)
+    sure = 0
+    for b in range(B):
+        T, K = (1.0 if t is None else float(t[b])), (0 if kk is None else int(kk[b]))
+        P, M = (1.0 if pp is None else float(pp[b])), (0.0 if mm is None else float(mm[b]))
+        order = np.lexsort((np.arange(V), -z[b]))
+        if not T > 0 or K == 1:
+            assert got[b] == order[0]
+            continue
+        w = np.exp((z[b] - z[b].max()) / T)
+        w[w < 2.0 ** -33] = 0
+        keep = np.zeros(V, bool)
+        keep[order[:K] if 0 < K < V else order] = True
+        amb = np.zeros(V, bool)
+        if P < 1:
+            ws = (w * keep)[order]
+            S, before = ws.sum(), np.cumsum(ws) - ws
+            sel = before < P * S
+            sel[0] = True
+            near = (np.abs(before - P * S) <= SLACK * S) & keep[order] & (ws > 0)
+            near[0] = False
+            amb[order[near]] = True
+            keep[order] &= sel
+        if M > 0:
+            # an exponent is off by a rounding of the difference, 2^-24 of |x|, and the hardware's 2^-22
+            amb |= keep & (np.abs(w - M) <= M * (2.0 ** -21 + 2.0 ** -22 * np.abs(np.log(max(M, 1e-30))))) & (z[b] != z[b].max())
+            keep &= (w >= M) | (z[b] == z[b].max())
+        keep &= w > 0
+        c = np.cumsum(w * (keep | amb))
+        slack = SLACK * c[-1] + (w * amb).sum()
+        assert keep[got[b]] or amb[got[b]], (b, int(got[b]))
+        x = min(max(float(ut[b]), 0.0), 1.0) * c[-1]
+        assert c[got[b]] - w[got[b]] - slack <= x <= c[got[b]] + slack, (b, int(got[b]))
+        if not amb.any():
+            sure += 1
+            if float(ut[b]) >= 1:
+                assert got[b] == np.flatnonzero(keep)[-1], (b, int(got[b]))
+    return sure
+
+
+@pytest.mark.parametrize("half", [False, True])
+@pytest.mark.parametrize("V", [700, 4097, 32000, 151936])
+def test_every_token_is_one_that_the_filters_keep(V, half):
+    """u = 1 takes the last kept token by index, u = 0 the first, and numbers between come near the borders."""
+    B = 8
+    ends = np.resize([1.0, 0.0, 0.999999, 0.5, 1.0], B)
+    for seed, std in ((1, 2.5), (2, 0.3), (3, 6.0)):
+        z = rows(seed + V, B, V, std=std, half=half)
+        assert strict(z, ends, k=np.resize([2, 3, 50, 1000, V - 1, 2047, 2049, 5], B)) == B
+        assert strict(z, ends, k=np.resize([50, V // 2], B), temp=np.linspace(0.3, 3, B)) == B
+        sure = strict(z, ends, p=np.resize([0.9, 0.5, 0.999, 0.05], B))
+        sure += strict(z, ends, p=np.resize([0.9, 0.5, 0.99], B), k=np.resize([40, 3000, 7], B), temp=np.linspace(0.5, 1.5, B))
+        assert sure >= B // 2 or half or V > 10000
+        strict(z, ends, mp=np.resize([0.01, 0.3, 0.001, 0.9], B))
+        strict(z, ends, mp=0.02, p=0.97, k=2000, temp=np.linspace(0.5, 5, B))
+    assert tbik.get_error() == tbik.TBIK_OK
+
+
+def test_the_last_kept_token_for_u_of_one_and_more():
+    z = rows(11, 4, 777)
+    for u in (1.0, 7.0, float("inf")):
+        assert strict(z, [u] * 4) == 4
+        assert strict(z, [u] * 4, k=30) == 4
+        got = tbik.sample(z, torch.full((4,), u, device=DEV), top_k=torch.full((4,), 30, dtype=torch.int32, device=DEV)).tolist()
+        assert got == z.topk(30, dim=1).indices.max(1).values.tolist()  # no ties among the largest here
+
+
+@pytest.mark.parametrize("B,V,half", [(400, 33001, False), (150, 151936, True)])
+def test_rows_of_all_kinds_when_clusters_come_in_waves(B, V, half):
+    """More clusters than the device holds at once: masked tokens, flat rows, hot and cold temperatures among others."""
+    z = rows(B, B, V, half=half)
+    z[1::7, : V // 2] = -1e30
+    z[2::7] *= 0.001
+    z[3] = -1.25
+    z[5::9] -= 300
+    strict(z, uni(1, B), temp=np.resize([1.0, 0.7, 0.2, 1.3, 0.0, 5.0, 0.05], B), k=np.resize([0, 50, 1000, 0, V // 2, 2, 0, 0], B),
+           p=np.resize([0.95, 1.0, 0.9, 0.999, 0.3], B), mp=np.resize([0.0, 0.05, 0.0], B))
+    assert tbik.get_error() == tbik.TBIK_OK
