@@ -1007,6 +1007,136 @@ def test_a_layer_of_a_pool_with_an_odd_number_of_scales(num_pages, H):
     assert tbik.get_error() == tbik.TBIK_OK
 
 
+def test_pools_and_tables_of_the_largest_size():
+    """2^20 pages, 65536 slots, 8192 sequences a call (the model's loops as array operations)."""
+    num, slots, page, B = 1 << 20, 65536, 16, 8192
+    c = Cache(slots, 140, num, 1, 64, page, fill=0)
+    book, r = c.book, np.random.RandomState(0)
+    order = r.permutation(slots)
+    rows, more, children = order[:B], order[B:2 * B], order[2 * B:2 * B + 500]
+    pages_of = lambda n: -(-n // page)  # noqa: E731
+
+    def extend(rows, n):
+        start = tbik.cache_extend(c.table, c.lens, c.refs, i32(n), page=page, rows=i32(rows))
+        have = pages_of(book.lens[rows])
+        want = pages_of(book.lens[rows] + n) - have
+        free = np.flatnonzero(book.refs == 0)
+        if want.sum() > len(free):
+            assert (start == -1).all() and tbik.get_error() == tbik.TBIK_ERR_PAGE
+        else:
+            assert np.array_equal(start.cpu().numpy(), book.lens[rows])
+            who = np.repeat(np.arange(len(rows)), want)
+            ids = free[:len(who)]
+            book.table[rows[who], have[who] + np.arange(len(who)) - (np.cumsum(want) - want)[who]] = ids
+            book.refs[ids] = 1
+            book.lens[rows] += n
+        c.check()
+        return want.sum() <= len(free)
+
+    n = r.randint(0, 127 * page, B)
+    assert extend(rows, n)
+    raw(c.pages).copy_(torch.randint(0, 127, c.pages.shape, dtype=torch.uint8, device=DEV))
+    assert not extend(more, np.full(B, 130 * page))  # more pages than are left
+    assert extend(more, n[::-1].copy())
+    before, sc = raw(c.pages).clone(), c.scales.clone()
+    parents = rows[:500]
+    tbik.cache_fork(c.pages, c.scales, c.table, c.lens, c.refs, i32(parents), i32(children))
+    moves = book.fork(parents.tolist(), children.tolist())
+    c.check()
+    a, b = (torch.tensor(x, device=DEV) for x in zip(*moves))
+    before[:, :, b] = before[:, :, a]
+    sc[:, :, b] = sc[:, :, a]
+    assert torch.equal(raw(c.pages), before) and torch.equal(c.scales, sc)
+    tbik.cache_free(c.table, c.lens, c.refs, i32(rows), page=page)
+    np.subtract.at(book.refs, book.table[rows][book.table[rows] >= 0], 1)
+    book.table[rows], book.lens[rows] = -1, 0
+    c.check()
+    live = tbik.cache_compact(c.pages, c.scales, c.table, c.lens, c.refs)
+    n_live = int((book.refs > 0).sum())
+    assert live.item() == n_live
+    hole, high = np.flatnonzero(book.refs[:n_live] == 0), n_live + np.flatnonzero(book.refs[n_live:] > 0)
+    to = np.arange(num, dtype=np.int32)
+    to[high] = hole
+    book.refs[hole], book.refs[high] = book.refs[high], 0
+    book.table = np.where(book.table >= 0, to[book.table], -1).astype(np.int32)
+    c.check()
+    before[:, :, torch.from_numpy(hole).to(DEV)] = before[:, :, torch.from_numpy(high).to(DEV)]
+    assert len(hole) > 100000 and torch.equal(raw(c.pages), before)
+    assert tbik.get_error() == tbik.TBIK_OK
+    # copies between the two ends of the pool
+    tbik.cache_copy(c.pages, c.scales, i32(range(100)), i32(range(num - 100, num)))
+    before[:, :, num - 100:] = before[:, :, :100]
+    assert torch.equal(raw(c.pages), before) and tbik.get_error() == tbik.TBIK_OK
+    # one sequence with every page of a pool
+    del before, a, b
+    one = Cache(2, num, num, 1, 64, page, fill=0)
+    assert one.pages.shape[2] == num
+    start = tbik.cache_extend(one.table, one.lens, one.refs, i32([num * page - 3]), page=page, rows=i32([1]))
+    assert start.item() == 0 and one.table[1].tolist() == list(range(num)) and (one.refs == 1).all()
+    k = torch.randn(3, 1, 64, device=DEV).to(torch.bfloat16)
+    start = tbik.cache_extend(one.table, one.lens, one.refs, i32([3]), page=page, rows=i32([1]))
+    tbik.cache_append(k, k, one.pages[0], one.scales[0], one.table, one.refs, start, cu=i32([0, 3]), rows=i32([1]))
+    q = torch.randn(1, 8, 64, device=DEV).to(torch.bfloat16)
+    out = tbik.cache_attention(q, one.pages[0], one.scales[0], one.table, i32([num * page - 1]), rows=i32([1]))
+    assert tbik.get_error() == tbik.TBIK_OK and torch.isfinite(out).all()
+    v = one.pages[0][1, num - 1, 0].float().permute(0, 2, 1, 3).reshape(page, 64)[-3:] * one.scales[0][1, num - 1, 0]
+    s = (q[0].float() @ (one.pages[0][0, num - 1, 0].float().permute(0, 2, 1, 3).reshape(page, 64)[-3:] * one.scales[0][0, num - 1, 0]).T) / 8
+    w = torch.exp(s.double())  # every other score is 0, its value too
+    want = (w @ v.double()) / (w.sum(1, keepdim=True) + num * page - 3)
+    assert (out[0].double() - want).abs().max() <= 2.0 ** -7 * want.abs().max()
+
+
+def test_a_decode_step_in_a_graph():
+    """Room, write, attention with its default bounds, choice, captured once on a side stream and replayed, against the same
+    steps called one by one: the same pages, tokens and bits, also where a page fills up and where the pool runs out."""
+    H, heads, D, page, V, B = 2, 8, 64, 16, 3000, 5
+    g = torch.Generator(device=DEV).manual_seed(0)
+    rnd = lambda *s: torch.randn(*s, device=DEV, generator=g).to(torch.bfloat16)  # noqa: E731
+    kv, head, us = rnd(V, 2, H, D), rnd(heads * D, V) / 8, torch.rand(60, B, device=DEV, generator=g)
+    qs = rnd(V, heads, D)
+    rows, one = i32([6, 0, 3, 7, 1]), i32([1] * B)
+    full = lambda x: torch.full((B,), x, device=DEV)  # noqa: E731
+    temp, top_p = full(0.9), full(0.95)
+
+    def fresh():
+        c = Cache(8, 5, 16, H, D, page)
+        return c, torch.arange(B, device=DEV, dtype=torch.int32), torch.zeros(B, device=DEV), torch.zeros(B, heads, D, device=DEV, dtype=torch.bfloat16)
+
+    def step(c, tok, u, out):
+        start = tbik.cache_extend(c.table, c.lens, c.refs, one, page=page, rows=rows)
+        x = kv[tok.long()]
+        tbik.cache_append(x[:, 0].contiguous(), x[:, 1].contiguous(), c.pages[0], c.scales[0], c.table, c.refs, start, rows=rows)
+        tbik.cache_attention(qs[tok.long()], c.pages[0], c.scales[0], c.table, start, rows=rows, out=out)
+        z = torch.nan_to_num(out.float().reshape(B, -1)) @ head.float()
+        tbik.sample(z, u, temperature=temp, top_p=top_p, out=tok)
+
+    c1, tok1, u1, out1 = fresh()
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        step(*fresh())  # nothing is set up while the graph is captured
+        side.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=side):
+            step(c1, tok1, u1, out1)
+    torch.cuda.synchronize()
+    c2, tok2, u2, out2 = fresh()
+    refused = 0
+    for s in range(60):  # 16 pages for 5 sequences: refused from position 48 on
+        u1.copy_(us[s])
+        u2.copy_(us[s])
+        graph.replay()
+        step(c2, tok2, u2, out2)
+        torch.cuda.synchronize()
+        assert torch.equal(tok1, tok2) and torch.equal(out1.view(torch.int16), out2.view(torch.int16))
+        assert torch.equal(c1.table, c2.table) and torch.equal(c1.lens, c2.lens) and torch.equal(c1.refs, c2.refs)
+        assert torch.equal(raw(c1.pages), raw(c2.pages)) and torch.equal(c1.scales, c2.scales)
+        code = tbik.get_error()
+        assert code == (tbik.TBIK_OK if s < 48 else tbik.TBIK_ERR_PAGE), (s, code)
+        assert torch.isnan(out1).any().item() == (s >= 48)
+        refused += code != tbik.TBIK_OK
+    assert refused == 12
+
+
 # ------------------------------------------------- together, as a rollout uses them
 
 def test_a_rollout_and_its_replay():
