@@ -548,7 +548,9 @@ TBIK_API tbik_status tbik_cache_append(const uint16_t* k, const uint16_t* v, uin
  *   max_keys  no query sees more than max_keys keys (start[b] + n_b <= max_keys)
  * Rows of sequences with start[b] < 0, beyond max_q or max_keys, or with a page
  * number outside the pool are NaN, the latter three with TBIK_ERR_PAGE; a range
- * cu[b] .. cu[b+1] outside the tokens is passed over with TBIK_ERR_POSITION.
+ * cu[b] .. cu[b+1] outside the tokens is passed over with TBIK_ERR_POSITION, and
+ * so is the whole call when the ranges overlap such that they hold more tokens
+ * than there are.
  * Tokens outside every sequence's range are left as they are.  Bytes at positions
  * that a row does not see leave it alone, whatever they hold.  Sequences may name
  * the same slot.  out may alias q.

@@ -306,16 +306,16 @@ __device__ __forceinline__ int catt_usable(const CacheAttParams& p, int s, int s
 // What can be answered of sequence b: its first `use` tokens, from packed token `first` and position s on (use = 0: s = 0).
 struct CattSeq {
     int b, slot, first, s, use;
+    int n;  // its tokens
 };
 __device__ __forceinline__ CattSeq catt_seq(const CacheAttParams& p, int b, bool& bad) {
     CattSeq q;
-    int n;
     q.b = b;
-    q.first = catt_tokens(p, b, n);
+    q.first = catt_tokens(p, b, q.n);
     q.s = p.start[b];
     q.slot = p.rows ? p.rows[b] : b;
-    q.use = catt_usable(p, q.s, q.slot, n);
-    bad |= q.use < n || (p.cu && n == 0 && (q.first < 0 || p.cu[b + 1] < q.first || p.cu[b + 1] > p.tokens));
+    q.use = catt_usable(p, q.s, q.slot, q.n);
+    bad |= q.use < q.n || (p.cu && q.n == 0 && (q.first < 0 || p.cu[b + 1] < q.first || p.cu[b + 1] > p.tokens));
     if (q.use == 0) q.s = 0;
     return q;
 }
@@ -409,15 +409,18 @@ struct CattUnits {
         }
         // the sequence's next block, or the next sequence that has something to do
         bool bad = false;
-        int blk = it.L;
-        CattSeq q = catt_seq(p, it.b, bad);
+        int blk = it.L, b = it.b;
 #pragma unroll 1
-        while (blk * CATT_LEAF >= q.s + q.use) {
-            if (q.b + 1 >= p.batch) return false;
-            q = catt_seq(p, q.b + 1, bad);
-            blk = q.s / CATT_LEAF;
+        for (;;) {
+            const CattSeq q = catt_seq(p, b, bad);
+            if (blk < 0) blk = q.s / CATT_LEAF;
+            if (blk * CATT_LEAF < q.s + q.use) {
+                enter(catt_item(p, q, blk));
+                break;
+            }
+            if (++b >= p.batch) return false;
+            blk = -1;
         }
-        enter(catt_item(p, q, blk));
         v = lo = 0;
         size = catt_node_size(it.L, d, 0);
         return true;
@@ -470,10 +473,11 @@ __device__ __forceinline__ void catt_scan(long long& w, long long& c, int& flags
 // Fills `pl`; true if some token of the call has no answer.  Every thread takes a run of a sequence's blocks of 128
 // positions: `per` threads share a sequence when there are fewer sequences than threads, and with as many threads as runs
 // (the usual case) every sequence is read once.  Only blocks that hold tokens are looked at, so the work does not depend on
-// max_q (a call with 1024 sequences of 8 tokens and max_q left at its default took 943 us with one look per sequence and
-// block that max_q allows, and 161 us with a tight max_q).
+// max_q (a call with 1024 sequences of 8 tokens and max_q left at its default took 931 us with one look per sequence and
+// block that max_q allows; it takes 140 us).  Not inlined: the roles' registers are then laid out without it (chunks 855 us
+// in place of 866, drafted tokens 41.7 in place of 43.0; one query 13.5 in place of 13.3).
 template <int R, int MAX_NODE>
-__device__ __forceinline__ bool catt_plan(const CacheAttParams& p, CattPlan* pl, CattScan* buf) {
+__device__ __noinline__ bool catt_plan(const CacheAttParams& p, CattPlan* pl, CattScan* buf) {
     const int tid = threadIdx.x, nt = blockDim.x;
     int shift = 0;
     while (p.cu && (long long)p.batch << (shift + 1) <= nt) ++shift;
@@ -489,15 +493,28 @@ __device__ __forceinline__ bool catt_plan(const CacheAttParams& p, CattPlan* pl,
         k1 = f + (int)((long long)blocks * (sub + 1) >> shift);
     };
     auto tiles = [&](int k) { return (long long)p.kv_heads * ((catt_item(p, q, k).rows + R - 1) / R); };
-    long long leaves = 0, total = 0, t0, t1;
+    long long leaves = 0, tokens = 0, total = 0, t0, t1;
 #pragma unroll 1
     for (int i = tid; i < runs; i += nt) {
         load(i);
+        if (!(i & ((1 << shift) - 1))) tokens += q.n;
 #pragma unroll 1
         for (int k = k0; k < k1; ++k) leaves += tiles(k) * (k + 1);
     }
+    catt_scan(leaves, tokens, flags, buf, t0, t1);
+    if (t1 > p.tokens) {
+        // Ranges that overlap: their work, and the slots that it asks for, are not bounded by the call's sizes.
+        if (tid == 0) {
+            pl->it.rows = 0;
+            pl->x0 = pl->x1 = 0;
+            if (blockIdx.x == 0) {
+                set_error(TBIK_ERR_POSITION);
+                if (p.max_slots) p.count[0] = p.count[1] = 0;
+            }
+        }
+        return false;
+    }
     long long unused = 0;
-    catt_scan(leaves, unused, flags, buf, t0, t1);
     const long long aim = catt_div_up(t0, (int)gridDim.x * CATT_UNITS);
     const int T = (int)min((long long)MAX_NODE, max(1ll, aim));
     // A block's weight, which is that of its units (their leaves and their start), added to w; its slots and tiles, if its
@@ -567,7 +584,6 @@ __device__ __forceinline__ bool catt_plan(const CacheAttParams& p, CattPlan* pl,
     if (tid == 0) {
         pl->x0 = min(total, step * blockIdx.x);
         pl->x1 = min(total, step * (blockIdx.x + 1));
-        // cu that lets sequences overlap can ask for more slots than there are
         if (blockIdx.x == 0 && p.max_slots) {
             p.count[0] = (cut >> 32) > p.max_slots ? 0 : (int)(cut & 0xffffffff);
             p.count[1] = flags & 2;

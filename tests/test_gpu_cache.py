@@ -867,6 +867,22 @@ def test_attention_bounds_that_are_too_tight_and_offsets_that_cannot_be():
         assert torch.equal(out[which], good[which]) and (out[rest] == 3.0).all()
 
 
+@pytest.mark.parametrize("cu", [[0, 9, 0, 9], [0, 6, 3, 9, 5, 9], [0, 9, 8, 9] + [0, 9] * 300])
+def test_offsets_whose_ranges_overlap(cu):
+    """More tokens than there are: nothing is computed."""
+    H, D, page = 2, 64, 32
+    c, rows = filled([400], H, D, page, seed=7)
+    q = torch.randn(9, 4, D, device=DEV).to(torch.bfloat16)
+    out = torch.full_like(q, 3.0)
+    n = len(cu) - 1
+    for kw in (dict(max_q=9, max_keys=400), {}):
+        tbik.cache_attention(q, c.pages[0], c.scales[0], c.table, i32([300] * n), cu=i32(cu), rows=i32(rows * n), out=out, **kw)
+        assert tbik.get_error() == tbik.TBIK_ERR_POSITION and (out == 3.0).all()
+    # empty ranges at any place, and ranges that leave tokens out, are sound
+    got = tbik.cache_attention(q, c.pages[0], c.scales[0], c.table, i32([390, 100, 391, 392]), cu=i32([0, 0, 5, 5, 8]), rows=i32(rows * 4))
+    assert tbik.get_error() == tbik.TBIK_OK and (got[8] == 0).all() and not (got[:8] == 0).all(-1).any()
+
+
 def captured_time(f, calls=5):
     """Device time of `calls` calls in a captured graph, the best of five replays."""
     f()
