@@ -577,7 +577,9 @@ TBIK_API tbik_status tbik_cache_attention(const uint16_t* q, const uint8_t* page
  *   index, exceeds u[i] times their total.
  * The most likely token always stays; temperature[i] <= 0 takes it (the lowest
  * index of the largest logit).  NULL for temperature, top_k, top_p or min_p
- * means 1, off, 1, 0 for every row.  Logits of -inf are never chosen; a row
+ * means 1, off, 1, 0 for every row; a NaN temperature counts as 0, a NaN top_p
+ * or min_p as off, a u outside [0, 1) as the nearest number there (NaN as 0).
+ * Logits of -inf are never chosen; a row
  * that has nothing else, or a NaN (TBIK_ERR_VALUE), gives -1.  The weights' sums
  * are sums of integers, so a row's token depends on that row only.
  * vocab <= 393216.  logits 16-byte aligned.

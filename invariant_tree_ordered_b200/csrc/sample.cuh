@@ -972,7 +972,7 @@ __global__ void __launch_bounds__(SMP_THREADS, 2) sample_kernel(const SamplePara
         f.c_lo = c < 1e30 ? (float)(c - (double)f.c) : 0.0f;
         f.low = -__fdiv_rn(200.0f, f.c);
     }
-    f.min_w = p.min_p ? p.min_p[row] : 0.0f;
+    f.min_w = p.min_p ? fmaxf(p.min_p[row], 0.0f) : 0.0f;  // NaN is off
     f.lkey = 0;
     f.lidx = 0xffffffffu;
     const bool by_k = !f.greedy && k > 0 && k < p.vocab;

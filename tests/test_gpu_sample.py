@@ -329,3 +329,22 @@ def test_rows_of_all_kinds_when_clusters_come_in_waves(B, V, half):
     strict(z, uni(1, B), temp=np.resize([1.0, 0.7, 0.2, 1.3, 0.0, 5.0, 0.05], B), k=np.resize([0, 50, 1000, 0, V // 2, 2, 0, 0], B),
            p=np.resize([0.95, 1.0, 0.9, 0.999, 0.3], B), mp=np.resize([0.0, 0.05, 0.0], B))
     assert tbik.get_error() == tbik.TBIK_OK
+
+
+@pytest.mark.parametrize("V,std", [(3000, 2.5), (151936, 2.5), (40000, 0.0)])
+def test_settings_that_are_not_numbers(V, std):
+    """A NaN temperature takes the most likely token; NaN top_p and min_p (and a negative min_p) filter nothing."""
+    B = 12
+    z = rows(V, B, V, std=std, peaks=std > 0)
+    u = torch.from_numpy(uni(1, B)).to(DEV)
+    full = lambda x: torch.full((B,), x, device=DEV)  # noqa: E731
+    nan = float("nan")
+    for kw in ({}, dict(top_k=torch.full((B,), 300, dtype=torch.int32, device=DEV))):
+        plain = tbik.sample(z, u, **kw)
+        assert torch.equal(tbik.sample(z, u, min_p=full(nan), **kw), plain)
+        assert torch.equal(tbik.sample(z, u, min_p=full(-1.0), **kw), plain)
+        assert torch.equal(tbik.sample(z, u, top_p=full(nan), **kw), plain)
+        half = tbik.sample(z, u, top_p=full(0.5), **kw)
+        assert torch.equal(tbik.sample(z, u, top_p=full(0.5), min_p=full(nan), **kw), half)
+        assert torch.equal(tbik.sample(z, u, temperature=full(nan), **kw), tbik.sample(z, u, temperature=full(0.0), **kw))
+    assert tbik.get_error() == tbik.TBIK_OK
