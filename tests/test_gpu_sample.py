@@ -260,8 +260,9 @@ def strict(logits, u, temp=None, k=None, p=None, mp=None):
         if not T > 0 or K == 1:
             assert got[b] == order[0]
             continue
-        w = np.exp((z[b] - z[b].max()) / T)
-        w[w < 2.0 ** -33] = 0
+        with np.errstate(invalid="ignore"):
+            w = np.exp((z[b] - z[b].max()) / T)
+        w[(z[b] == -np.inf) | (w < 2.0 ** -33)] = 0
         keep = np.zeros(V, bool)
         keep[order[:K] if 0 < K < V else order] = True
         amb = np.zeros(V, bool)
