@@ -106,9 +106,9 @@ struct CacheAppendParams {
 // One block per (page that a sequence's new tokens touch, kv head, keys or values): the page's new tokens are read
 // once into registers (16-byte loads, CH of them in flight per thread), their largest magnitude fixes the scale, and
 // the bytes go out 8 at a time (two tokens of a warp fill a 32-byte sector).  The tokens are asked for before the page is
-// looked up, so that the chain of loads is sequence, start, tokens.  Bound by integer instructions (about six per value
-// for rounding, cutting, sign and packing) ahead of HBM: 32 prompts of 100 to 4096 tokens, 8 heads of 128 dims, 58 us,
-// 3.9 TB/s.  128 threads with eight loads each measured 58 us there, 256 with four 65 us.  A decode step (one token each:
+// looked up, so that the chain of loads is sequence, start, tokens.  Bound by integer instructions ahead of HBM: 32 prompts
+// of 100 to 4096 tokens, 8 heads of 128 dims, 58 us, 3.9 TB/s; 16 instructions a value (39 M by warps), 9.6 of them on the
+// ALU pipe, which is 75 % busy, with issue slots 64 % and DRAM 42 %.  128 threads with eight loads each measured 58 us there, 256 with four 65 us.  A decode step (one token each:
 // one warp per token, head and operand, eight to a block) takes 2.3 us for 64 sequences and 39 us for 8192 (8 heads of
 // 128; blocks of one warp took 2.5 and 70 us).
 //

@@ -7,8 +7,14 @@
 //
 // The bytes of a page go to the tensor cores as they lie in the cache (tcgen05 kind::f8f6f4, unswizzled operands), so
 // nothing is ever widened.  What is not 8 bits wide is given to them as two e4m3 terms of 4 significant bits:
-//   query   q 2^x = h + l / 32, x such that the row's largest |q| 2^x lies in [128, 256): exact down to 2^-14 of it;
+//   query   q 2^x = h + l / 32, x such that the row's largest |q| 2^x lies in [128, 256): exact down to 2^-14 of it, and
+//           below that to 2^-22 of it;
 //   weight  256 f p = h + l, rounded at 2^-9 relative or 2^-18 of the leaf's largest (f below).
+// Why two terms are enough for the weights: the output is rounded to bf16 once, by up to 2^-8, and the weights' roundings do
+// not know of one another, so that their mean over the keys is smaller still.  Against 64 bits the chunks below are off by
+// 1.666e-3 of the output's norm, and sums in fp32 rounded to bf16 by 1.659e-3.  A third term would make the products of the
+// values half as long again.  The sum s takes the weights before they are rounded: a key of a page with a small f keeps its
+// share of s in full where its 256 f p is cut, which a sum of the rounded ones would lose.
 // With keys as the 128 rows of an MMA and queries as its columns, few queries waste few columns, which suits a decode
 // step (G query heads of one token share a kv head):
 //   S^T = K [h | l]     M = 128 keys, N = 2 rows, K = head_dim
@@ -31,12 +37,12 @@
 // own tree, so the bits do not depend on the cut.
 //
 // What bounds it.  Few rows over long contexts: the cache's bytes (4 sequences of 120-131 thousand positions, 32 query and
-// 4 kv heads of 128 dims: 111 us with both kernels, 4.7 TB/s; under a profiler the first kernel's DRAM reads are the
-// cache's bytes and nothing more).  Mixed batches: the chain of a leaf (scores, maximum over four warps, weights, values,
-// tree: 3.7 thousand cycles alone, 6.5 with three CTAs on an SM) and the 10 us of planning, first loads and the second
-// kernel (64 sequences of 1 to 8192 positions: 53 us, 18 us of bytes).  Many rows: the same chain's instructions, about
-// 30 per row, key and lane (chunks of 300-512 queries over 5-8 thousand positions: 0.87 ms, 198 TFLOP/s); issue slots are
-// 40 % used, the tensor pipe 3 to 10 %.
+// 4 kv heads of 128 dims: 110 us with both kernels, 4.7 TB/s; the first one reads the cache's bytes and nothing more at
+// 5.0 TB/s, its planning included).  Mixed batches: the chain of a leaf (scores, maximum over four warps, weights, values,
+// tree: 4.6 thousand cycles in the long contexts, with three CTAs on an SM) and the 10 us of planning, first loads and the
+// second kernel (64 sequences of 1 to 8192 positions: 54 us, 18 us of bytes).  Many rows: the same chain's instructions, 36 per
+// row, key and lane over all six warps (chunks of 300-512 queries over 5-8 thousand positions: 0.87 ms, 198 TFLOP/s); issue
+// slots are 47 % used, the tensor pipe 3 to 11 %.
 #pragma once
 
 #include <cuda_fp16.h>
