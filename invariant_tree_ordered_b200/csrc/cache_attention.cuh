@@ -480,10 +480,9 @@ __device__ __forceinline__ void catt_scan(long long& w, long long& c, int& flags
 // positions: `per` threads share a sequence when there are fewer sequences than threads, and with as many threads as runs
 // (the usual case) every sequence is read once.  Only blocks that hold tokens are looked at, so the work does not depend on
 // max_q (a call with 1024 sequences of 8 tokens and max_q left at its default took 931 us with one look per sequence and
-// block that max_q allows; it takes 140 us).  Not inlined: the roles' registers are then laid out without it (chunks 855 us
-// in place of 866, drafted tokens 41.7 in place of 43.0; one query 13.5 in place of 13.3).
+// block that max_q allows; it takes 137 us).
 template <int R, int MAX_NODE>
-__device__ __noinline__ bool catt_plan(const CacheAttParams& p, CattPlan* pl, CattScan* buf) {
+__device__ __forceinline__ bool catt_plan_body(const CacheAttParams& p, CattPlan* pl, CattScan* buf) {
     const int tid = threadIdx.x, nt = blockDim.x;
     int shift = 0;
     while (p.cu && (long long)p.batch << (shift + 1) <= nt) ++shift;
@@ -596,6 +595,18 @@ __device__ __noinline__ bool catt_plan(const CacheAttParams& p, CattPlan* pl, Ca
         }
     }
     return flags & 1;
+}
+
+// A call of its own in the small tiles' kernels, whose roles' registers are then laid out without it (drafted tokens 41.6 us
+// in place of 43.0; one query 13.7 in place of 13.3), part of the kernel for 32 rows (chunks 852 us in place of 856).
+template <int R, int MAX_NODE>
+__device__ __noinline__ bool catt_plan_call(const CacheAttParams& p, CattPlan* pl, CattScan* buf) {
+    return catt_plan_body<R, MAX_NODE>(p, pl, buf);
+}
+template <int R, int MAX_NODE>
+__device__ __forceinline__ bool catt_plan(const CacheAttParams& p, CattPlan* pl, CattScan* buf) {
+    if constexpr (R == 32) return catt_plan_body<R, MAX_NODE>(p, pl, buf);
+    else return catt_plan_call<R, MAX_NODE>(p, pl, buf);
 }
 
 // Tokens without an answer: NaN, and an error unless the sequence was not granted (start < 0).
