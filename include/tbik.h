@@ -438,8 +438,8 @@ TBIK_API tbik_status tbik_logprob_noalloc(const uint16_t* hidden, const uint16_t
  * The page operations are all or nothing: when an argument cannot be (a slot
  * out of range or named twice, a length that does not fit max_pages, a row to
  * fork or to compact that names a page not in use, too few free pages), they
- * change nothing and record TBIK_ERR_PAGE.  New pages are the lowest free ones, in the
- * order of the call's sequences.
+ * change nothing and record TBIK_ERR_PAGE.  New pages are the lowest free ones,
+ * in the order of the call's sequences.
  */
 
 /*
@@ -518,10 +518,10 @@ TBIK_API tbik_status tbik_cache_copy(uint8_t* pages, float* scales, const int32_
  * grid.  Only a call that begins at the page's first position sets the scale
  * anew; bytes behind its tokens are then still those of the old scale, to be
  * written again before they are read.  Bytes of positions that no token has
- * reached stay as they are.  Infinities are stored as +-448 * 2^E and NaN as 0, neither
- * counts for E, and TBIK_ERR_VALUE is recorded.  A page that is not in the
- * pool, that another sequence shares (refs != 1) or whose slot the call names
- * twice is not written, and TBIK_ERR_PAGE is recorded.
+ * reached stay as they are.  Infinities are stored as +-448 * 2^E and NaN as 0,
+ * neither counts for E, and TBIK_ERR_VALUE is recorded.  A page that is not in
+ * the pool, that another sequence shares (refs != 1) or whose slot the call
+ * names twice is not written, and TBIK_ERR_PAGE is recorded.
  */
 TBIK_API tbik_status tbik_cache_append(const uint16_t* k, const uint16_t* v, uint8_t* pages, float* scales,
                                        const int32_t* table, const int32_t* refs, const int32_t* start,
@@ -541,9 +541,9 @@ TBIK_API tbik_status tbik_cache_append(const uint16_t* k, const uint16_t* v, uin
  * scales of their pages (the last page's covers what else it holds by then), not
  * on the batch, the other queries, page numbers or the device's load.  Scores
  * and weighted sums are fp32: keys beyond 2^100, or values whose weighted sum
- * passes 2^127, may give infinities or NaN.  The weights are rounded to 2^-9 relative, or 2^-18 of the leaf's largest times
- * the ratio of its value scales, the output once; checked against the binary64
- * definition by tolerance.
+ * passes 2^127, may give infinities or NaN.  The weights are rounded to 2^-9
+ * relative, or 2^-18 of the leaf's largest times the ratio of its value scales,
+ * the output once; checked against the binary64 definition by tolerance.
  *   max_q     no sequence has more than max_q new tokens
  *   max_keys  no query sees more than max_keys keys (start[b] + n_b <= max_keys)
  * Rows of sequences with start[b] < 0, beyond max_q or max_keys, or with a page
@@ -579,9 +579,9 @@ TBIK_API tbik_status tbik_cache_attention(const uint16_t* q, const uint8_t* page
  * index of the largest logit).  NULL for temperature, top_k, top_p or min_p
  * means 1, off, 1, 0 for every row; a NaN temperature counts as 0, a NaN top_p
  * or min_p as off, a u outside [0, 1) as the nearest number there (NaN as 0).
- * Logits of -inf are never chosen; a row
- * that has nothing else, or a NaN (TBIK_ERR_VALUE), gives -1.  The weights' sums
- * are sums of integers, so a row's token depends on that row only.
+ * Logits of -inf are never chosen; a row that has nothing else, or a NaN
+ * (TBIK_ERR_VALUE), gives -1.  The weights' sums are sums of integers, so a
+ * row's token depends on that row only.
  * vocab <= 393216.  logits 16-byte aligned.
  */
 TBIK_API tbik_status tbik_sample(const void* logits, const float* u, const float* temperature, const int32_t* top_k,

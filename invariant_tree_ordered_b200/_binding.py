@@ -665,7 +665,7 @@ def cache_free(table, lens, refs, rows, *, page: int, stream=None):
 
 
 def cache_compact(pages, scales, table, lens, refs, *, live=None, workspace=None, stream=None):
-    """Live pages to the front of the pool (tbik_cache_compact); returns their number as int32 [1]."""
+    """Live pages to the front of the pool (tbik_cache_compact); returns their number as int32 [1] (-1: refused)."""
     torch = _torch()
     lib = load_library()
     layers, num_pages, kv_heads, page, head_dim = _pool(pages, scales, True)

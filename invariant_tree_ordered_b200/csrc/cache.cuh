@@ -108,9 +108,9 @@ struct CacheAppendParams {
 // the bytes go out 8 at a time (two tokens of a warp fill a 32-byte sector).  The tokens are asked for before the page is
 // looked up, so that the chain of loads is sequence, start, tokens.  Bound by integer instructions ahead of HBM: 32 prompts
 // of 100 to 4096 tokens, 8 heads of 128 dims, 58 us, 3.9 TB/s; 16 instructions a value (39 M by warps), 9.6 of them on the
-// ALU pipe, which is 75 % busy, with issue slots 64 % and DRAM 42 %.  128 threads with eight loads each measured 58 us there, 256 with four 65 us.  A decode step (one token each:
-// one warp per token, head and operand, eight to a block) takes 2.3 us for 64 sequences and 39 us for 8192 (8 heads of
-// 128; blocks of one warp took 2.5 and 70 us).
+// ALU pipe, which is 75 % busy, with issue slots 64 % and DRAM 42 %.  128 threads with eight loads each measured 58 us
+// there, 256 with four 65 us.  A decode step (one token each: one warp per token, head and operand, eight to a block) takes
+// 2.3 us for 64 sequences and 39 us for 8192 (8 heads of 128; blocks of one warp took 2.5 and 70 us).
 //
 // Which page a block has: sequence b's pages start at virtual index cu[b] / page + 2 b.  n tokens touch at most
 // n / page + 2 pages, so the ranges do not overlap, and the grid is known without reading `start`.  The sequence is
@@ -137,7 +137,8 @@ __device__ __forceinline__ int append_sequence(const CacheAppendParams& p, int x
 // (The ROWS form's bounds on registers keep as many blocks on an SM as the other's: left alone it takes up to 152, and 32
 // prompts 76 us in place of 55.)
 template <int D, int THREADS, int CH, int GROUPS, bool ROWS>
-__global__ void __launch_bounds__(THREADS * GROUPS, ROWS && GROUPS == 1 ? (CH == 8 ? 768 : CH == 4 ? 1024 : 1536) / THREADS : 0) cache_append_kernel(const CacheAppendParams p) {
+__global__ void __launch_bounds__(THREADS * GROUPS, ROWS && GROUPS == 1 ? (CH == 8 ? 768 : CH == 4 ? 1024 : 1536) / THREADS : 0)
+    cache_append_kernel(const CacheAppendParams p) {
     static_assert(GROUPS == 1 || THREADS == 32, "groups are warps");
     const int tid = threadIdx.x % THREADS;
     const int head = blockIdx.y, kv = blockIdx.z;
