@@ -121,7 +121,7 @@ struct CacheAppendParams {
 // block compares its slot with all of the call's.  For more (and for single tokens, GROUPS warps a block) the grid is what
 // the device holds; each block marks all slots once, in two maps of a bit per slot, and takes several pages or tokens in
 // turn, so that the looks stay in proportion to the call: 8192 single tokens 51 us (356 us with all blocks comparing),
-// with `cu` 372 us (1348 us).  Up to 4 looks a thread the comparison is as fast or faster: 512 sequences 22 us either way,
+// with `cu` 389 us (1348 us).  Up to 4 looks a thread the comparison is as fast or faster: 512 sequences 22 us either way,
 // 64 4.6 us (5.3 us with maps).
 constexpr int APPEND_FEW = 4;
 template <int THREADS>

@@ -37,11 +37,11 @@
 // own tree, so the bits do not depend on the cut.
 //
 // What bounds it.  Few rows over long contexts: the cache's bytes (4 sequences of 120-131 thousand positions, 32 query and
-// 4 kv heads of 128 dims: 110 us with both kernels, 4.7 TB/s; the first one reads the cache's bytes and nothing more at
+// 4 kv heads of 128 dims: 111 us with both kernels, 4.7 TB/s; the first one reads the cache's bytes and nothing more at
 // 5.0 TB/s, its planning included).  Mixed batches: the chain of a leaf (scores, maximum over four warps, weights, values,
 // tree: 4.6 thousand cycles in the long contexts, with three CTAs on an SM) and the 10 us of planning, first loads and the
-// second kernel (64 sequences of 1 to 8192 positions: 54 us, 18 us of bytes).  Many rows: the same chain's instructions, 36 per
-// row, key and lane over all six warps (chunks of 300-512 queries over 5-8 thousand positions: 0.87 ms, 198 TFLOP/s); issue
+// second kernel (64 sequences of 1 to 8192 positions: 53 us, 18 us of bytes).  Many rows: the same chain's instructions, 36 per
+// row, key and lane over all six warps (chunks of 300-512 queries over 5-8 thousand positions: 0.86 ms, 199 TFLOP/s); issue
 // slots are 47 % used, the tensor pipe 3 to 11 %.
 #pragma once
 

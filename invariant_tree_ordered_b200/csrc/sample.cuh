@@ -24,7 +24,7 @@
 //
 // Measured: 256 rows of 151936 fp32 logits, every row with its own settings, 165 us (an HBM read takes 24 us; two blocks fit
 // an SM, and issue slots are 40 % used: of the 17 cycles between a warp's instructions 5 go to block barriers, which wait
-// for the cluster's too, 3 to loads and 2 to shared memory); one row 23 to 31 us; 97 rows of 32000 in bf16 32 us.  A row
+// for the cluster's too, 3 to loads and 2 to shared memory); one row 19 to 31 us; 97 rows of 32000 in bf16 29 to 34 us.  A row
 // read again from memory by one block for each sweep, without meetings, measured 172 us for the first and is not kept.
 // The general steps: top-p 0.95 at temperature 100 takes 97 us for one row of 151936 and 0.95 ms for 256, over equal logits
 // 72 us and 0.80 ms, top-k 5000 45 us and 0.50 ms (60 us and 0.64 ms with top-p); 97 rows of 32000 in bf16 47 to 100 us.
